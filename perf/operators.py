@@ -115,7 +115,7 @@ def _quantize(x):
     """MXFP8 codes and biased scale exponents of fp32 rows (last axis in blocks of 32)."""
     b = x.unflatten(-1, (-1, BLOCK))
     f, k = torch.frexp(b.abs().amax(-1))
-    e = torch.where(f <= 0.875, k - 9, k - 8).clamp(-100, 120)  # smallest e with amax <= 448 * 2^e
+    e = torch.where(f <= 0.875, k - 9, k - 8).clamp(-100, 119)  # smallest e with amax <= 448 * 2^e
     e = torch.where(f == 0, torch.full_like(e, -100), e)
     y = torch.ldexp(b, -e.unsqueeze(-1))
     return y.flatten(-2).to(torch.float8_e4m3fn).view(torch.uint8), (e + 127).to(torch.uint8)
@@ -374,7 +374,7 @@ def _exact_rows(x):
     b = x.double().unflatten(-1, (-1, BLOCK))
     a = b.abs().amax(-1, keepdim=True)
     e = torch.floor(torch.log2(a.clamp(min=2.0 ** -140))) - 8
-    e = torch.where(a > 448 * torch.exp2(e), e + 1, e).clamp(-100, 120)
+    e = torch.where(a > 448 * torch.exp2(e), e + 1, e).clamp(-100, 119)
     return _e4m3(b / torch.exp2(e)).flatten(-2)
 
 
