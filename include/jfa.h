@@ -70,10 +70,15 @@ typedef enum {
   JFA_ERR_WORKSPACE = 3,   /* workspace missing, misaligned or too small */
   JFA_ERR_BAD_OFFSETS = 4, /* (device) offsets are not a jagged layout of the given totals */
   JFA_ERR_TIMEOUT = 5,     /* (device) a bounded wait inside a kernel gave up */
-  JFA_ERR_CUDA = 6         /* a CUDA runtime or driver call failed */
+  JFA_ERR_CUDA = 6,        /* a CUDA runtime or driver call failed */
+  JFA_ERR_BAD_PAGES = 7    /* (device) a page table names a page outside the cache */
 } jfa_status;
 
-typedef enum { JFA_F32 = 0, JFA_BF16 = 1 } jfa_dtype;
+typedef enum {
+  JFA_F32 = 0,
+  JFA_BF16 = 1,
+  JFA_MXFP8 = 2 /* caches only: e4m3 codes, one power-of-two scale per 32 columns */
+} jfa_dtype;
 
 typedef struct {
   int64_t batch;   /* B >= 0 */
@@ -292,9 +297,166 @@ jfa_status jfa_block_rope_bwd(const jfa_params* p, const void* q, const void* k,
                               jfa_stream_t stream);
 
 /*
+ * RMS norm of every query and key head with the rotary position embedding, in one
+ * pass over the values (training and serving; q and k may be slices of one
+ * projection's output).  Per row x of D = dim values (one token, one head), with
+ * r = 1 / sqrt(mean(x^2) + eps) and weight w (wq or wk, fp32 [D]; NULL: ones):
+ *   n = x r w (norm = 1) or n = x (norm = 0; the weights and their gradients are
+ *   then NULL);
+ *   pair i < rope.dim / 2 of columns (a, b) = (i, i + rope.dim/2) (JFA_ROPE_HALVES) or
+ *   (2i, 2i + 1) (JFA_ROPE_PAIRS) turns by the angle pos[t] theta_i:
+ *     y_a = amp (n_a cos - n_b sin), y_b = amp (n_a sin + n_b cos);
+ *   the columns from rope.dim on are y = n.  rope.dim = 0: no rotation, pos may be NULL.
+ * Frequencies: theta_i = base^(-2i / rope.dim), for contexts `factor` times longer than
+ * the model was trained on changed by `scaling`:
+ *   JFA_ROPE_LINEAR  theta_i / factor (positions squeezed);
+ *   JFA_ROPE_NTK     base * factor^(rope.dim / (rope.dim - 2)) in place of base;
+ *   JFA_ROPE_YARN    theta_i (g + (1 - g) / factor), g = clamp((n_i - turns_slow) /
+ *                    (turns_fast - turns_slow), 0, 1), n_i = orig_len theta_i / 2 pi the
+ *                    turns pair i makes over the trained context; the method's
+ *                    temperature is the caller's choice of amp.
+ * pos is int64 [T] on the device, any values (negative too); the angle is exact to
+ * |pos| 2^-64 turns.
+ *
+ * Strides are in elements between tokens; a token's heads are contiguous, [heads, dim].
+ * heads_q or heads_k may be 0 (that tensor is then absent).  yq may be q (and yk be k)
+ * with the same stride; outputs overlap inputs in no other way.
+ *
+ * Backward: dyq, dyk are the gradients of yq, yk (strides stride_yq, stride_yk); dq, dk
+ * (strides stride_dq, stride_dk) those of q, k; dwq, dwk (fp32 [D], or NULL: not wanted)
+ * the weights', summed over tokens and heads in a fixed order without atomics (bitwise
+ * reproducible on one GPU).  The row's r is recomputed from q, k.  dq may be dyq or q
+ * with the same stride.  q, k may be NULL when norm = 0.  No tokens: dwq, dwk are zeroed.
+ *
+ * Values are fp32 or bf16 (dtype), pointers aligned to a value; pointers and strides of
+ * whole 16 bytes with dim and rope.dim multiples of 16 take the fast kernels.  dim <= 256
+ * and tokens <= 2^31 - 1, else JFA_ERR_UNSUPPORTED.  The forward needs no workspace; the
+ * backward's (256-byte aligned, jfa_norm_rope_workspace_size; 0 for bad params) is scratch
+ * without a status word.  The library finds no errors on the device here.
+ */
+enum { JFA_ROPE_HALVES = 0, JFA_ROPE_PAIRS = 1 };
+enum { JFA_ROPE_PLAIN = 0, JFA_ROPE_LINEAR = 1, JFA_ROPE_NTK = 2, JFA_ROPE_YARN = 3 };
+typedef struct {
+  int32_t dim;     /* rotated columns of a head: even, 0 .. head dim */
+  int32_t layout;  /* JFA_ROPE_HALVES or JFA_ROPE_PAIRS */
+  int32_t scaling; /* JFA_ROPE_PLAIN, _LINEAR, _NTK (dim >= 4) or _YARN */
+  float amp;       /* factor of the rotated columns, normally 1 */
+  double base;     /* >= 1, normally 10000 */
+  double factor;   /* >= 1 (LINEAR, NTK, YARN) */
+  double orig_len, turns_fast, turns_slow; /* YARN: > 0, > turns_slow, >= 0 */
+} jfa_rope;
+typedef struct {
+  int64_t tokens;
+  int64_t stride_q, stride_k;   /* q, k */
+  int64_t stride_yq, stride_yk; /* yq, yk; backward: dyq, dyk */
+  int64_t stride_dq, stride_dk; /* backward: dq, dk */
+  int32_t heads_q, heads_k, dim;
+  int32_t dtype; /* JFA_F32 or JFA_BF16 */
+  int32_t norm;  /* 1: RMS norm, 0: rotation only */
+  float eps;     /* >= 0 */
+  jfa_rope rope;
+} jfa_norm_rope_params;
+
+size_t jfa_norm_rope_workspace_size(const jfa_norm_rope_params* p);
+jfa_status jfa_norm_rope_fwd(const jfa_norm_rope_params* p, const void* q, const void* k,
+                             const int64_t* pos, const float* wq, const float* wk, void* yq,
+                             void* yk, jfa_stream_t stream);
+jfa_status jfa_norm_rope_bwd(const jfa_norm_rope_params* p, const void* q, const void* k,
+                             const int64_t* pos, const float* wq, const float* wk,
+                             const void* dyq, const void* dyk, void* dq, void* dk, float* dwq,
+                             float* dwk, void* ws, size_t ws_bytes, jfa_stream_t stream);
+
+/*
+ * Paged cache.  Keys and values of sequences that grow are kept in pages of page_size
+ * positions (16, 32, 64, 128 or 256):
+ *   k_cache [pages, Hk, page_size, Dqk], v_cache [pages, Hk, page_size, Dv], contiguous.
+ * Position x of sequence b is row x % page_size of page table[b, x / page_size] (int32
+ * [B, max_pages]; sequences may share pages).  lens [B] (int64) holds the sequences'
+ * cached lengths, the new tokens of the call among them: a call's T = offs[B] new tokens
+ * (offs int64 [B+1], a jagged layout as elsewhere) are the last ones of their sequences,
+ * token i of sequence b at position lens[b] - L_b + i, L_b = offs[b+1] - offs[b].
+ * Where L_b > lens[b] the first tokens come before the cache's start: they are not
+ * written, read back as zeros, and see no keys.
+ *
+ * The cache holds the values' own type, or MXFP8 (cache_dtype JFA_MXFP8): e4m3 codes,
+ * one byte a value, with k_scale [pages, Hk, page_size, Dqk / 32] and v_scale likewise,
+ * biased E8M0 exponents (2^(s - 127)) per 32 columns.  Writing takes the smallest power
+ * of two with max|x| <= 448 * scale, exponent kept in [-100, 119], and rounds x / scale
+ * to the nearest code, ties to even, saturating (NaN stays NaN).  Scales read may be any
+ * in [1, 254]; 0 reads as zeros.
+ *
+ * Index arrays live on the device.  jfa_paged_plan and every call without JFA_PLANNED
+ * reset the workspace's status word; invalid offs or lens outside [0, max_pages *
+ * page_size] give JFA_ERR_BAD_OFFSETS, and a page index outside [0, pages) that a call
+ * meets JFA_ERR_BAD_PAGES.  jfa_paged_fwd computes nothing on the former.  Rows behind a
+ * bad page are not written, are read as zeros, and count as zero keys and values.  Nothing
+ * outside the buffers is touched.  Pages' rows behind a sequence's length are never
+ * read as values (they may hold anything).
+ *
+ * jfa_cache_write puts the new keys and values k [T, Hk, Dqk], v [T, Hk, Dv] (token
+ * strides stride_k, stride_v; any slice of a projection's output) into their pages.  Two
+ * tokens of a call that share a slot leave either's row, in parts.  jfa_cache_read
+ * gathers the same tokens' rows back into contiguous k [T, Hk, Dqk], v [T, Hk, Dv]
+ * (L_b = lens[b] reads whole sequences); MXFP8 values are exact in fp32 and bf16.
+ *
+ * jfa_paged_fwd: softmax attention of the new tokens' queries q [T, Hq, Dqk] (token
+ * stride stride_q) over their sequences' cached keys, from one token a sequence to whole
+ * prompts.  Query head h reads key head h / (Hq / Hk).  With causal = 1 token i of
+ * sequence b sees positions <= lens[b] - L_b + i, else all lens[b].  o [T, Hq, Dv] and
+ * lse [T, Hq] as in jfa_fwd; a row that sees no key gets o = 0, lse = -inf.  Scores,
+ * statistics and sums are fp32; on the tensor-core kernels (bf16, dims 64 and 128) the
+ * weights are rounded to bf16 for the product with the values.  Keys and values of
+ * positions that a sequence's other queries see must be finite where a row's own mask
+ * hides them.  Results repeat bit for bit on one GPU.
+ *
+ * Every call cuts its work into equal shares on the device (jfa_paged_plan does it once for
+ * several calls, which then pass flags = JFA_PLANNED, the same params but for scale and
+ * strides, the same offs and lens, unchanged, and the same workspace).  The plan serves
+ * jfa_cache_write, jfa_cache_read and jfa_paged_fwd.  One workspace must not be used by
+ * calls that may run concurrently.
+ *
+ * Limits (JFA_ERR_UNSUPPORTED): dims multiples of 8 (MXFP8: 32), at most 256, in
+ * jfa_paged_fwd 128; cache_dtype the values' type or JFA_MXFP8; max_pages * page_size,
+ * total_q, batch and pages at most 2^31 - 1.  k, v, q and the caches are 16-byte aligned
+ * with strides of whole 16 bytes.
+ */
+typedef struct {
+  int64_t batch;   /* B >= 0 */
+  int64_t total_q; /* T = offs[B] */
+  int64_t pages;   /* pages of the cache */
+  int64_t stride_q, stride_k, stride_v; /* elements between tokens (>= heads * dim) */
+  int32_t heads_q; /* Hq, a multiple of Hk (attention) */
+  int32_t heads_k; /* Hk */
+  int32_t dim_qk, dim_v;
+  int32_t page_size, max_pages;
+  float scale;         /* score scale > 0 (attention) */
+  int32_t causal;      /* 0 or 1 (attention) */
+  int32_t dtype;       /* of q, k, v, o: JFA_F32 or JFA_BF16 */
+  int32_t cache_dtype; /* dtype or JFA_MXFP8 */
+  int32_t flags;       /* 0 or JFA_PLANNED */
+} jfa_paged_params;
+
+/* Bytes of workspace (256-byte aligned) of all four calls; 0 for bad params. */
+size_t jfa_paged_workspace_size(const jfa_paged_params* p);
+jfa_status jfa_cache_write(const jfa_paged_params* p, const void* k, const void* v,
+                           const int64_t* offs, const int64_t* lens, const int32_t* table,
+                           void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                           void* ws, size_t ws_bytes, jfa_stream_t stream);
+jfa_status jfa_cache_read(const jfa_paged_params* p, const void* k_cache, const void* v_cache,
+                          const uint8_t* k_scale, const uint8_t* v_scale, const int64_t* offs,
+                          const int64_t* lens, const int32_t* table, void* k, void* v, void* ws,
+                          size_t ws_bytes, jfa_stream_t stream);
+jfa_status jfa_paged_plan(const jfa_paged_params* p, const int64_t* offs, const int64_t* lens,
+                          void* ws, size_t ws_bytes, jfa_stream_t stream);
+jfa_status jfa_paged_fwd(const jfa_paged_params* p, const void* q, const void* k_cache,
+                         const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                         const int64_t* offs, const int64_t* lens, const int32_t* table, void* o,
+                         float* lse, void* ws, size_t ws_bytes, jfa_stream_t stream);
+
+/*
  * Synchronises `stream`, then returns the device status word of the last
- * call that used `ws` (JFA_OK, JFA_ERR_BAD_OFFSETS or JFA_ERR_TIMEOUT), or
- * JFA_ERR_CUDA if the synchronisation itself failed.
+ * call that used `ws` (JFA_OK, JFA_ERR_BAD_OFFSETS, JFA_ERR_BAD_PAGES or
+ * JFA_ERR_TIMEOUT), or JFA_ERR_CUDA if the synchronisation itself failed.
  */
 jfa_status jfa_status_check(const void* ws, jfa_stream_t stream);
 
@@ -315,7 +477,10 @@ enum {
   JFA_KERNEL_BWD_DKDV = 3, /* key-tile-major dK/dV pass */
   JFA_KERNEL_BWD_DQ = 4,   /* query-tile-major dQ pass */
   JFA_KERNEL_AUX = 5,      /* pooled query broadcast and gradient sum; block offsets */
-  JFA_KERNEL_KINDS = 6
+  JFA_KERNEL_NORM_ROPE = 6, /* norms with rotary positions (backward: with its weight sums) */
+  JFA_KERNEL_CACHE = 7,     /* paged cache written or read */
+  JFA_KERNEL_PAGED = 8,     /* attention over a paged cache, with the join of split tiles */
+  JFA_KERNEL_KINDS = 9
 };
 jfa_status jfa_profile_enable(int on);
 jfa_status jfa_profile_reset(void);

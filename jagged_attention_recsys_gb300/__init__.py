@@ -27,13 +27,19 @@ JFA_ERR_WORKSPACE = 3
 JFA_ERR_BAD_OFFSETS = 4
 JFA_ERR_TIMEOUT = 5
 JFA_ERR_CUDA = 6
+JFA_ERR_BAD_PAGES = 7
 
 JFA_F32 = 0
 JFA_BF16 = 1
+JFA_MXFP8 = 2
 
 JFA_PLANNED = 1
 
-KERNEL_KINDS = {"schedule": 0, "fwd": 1, "bwd_d": 2, "bwd_dkdv": 3, "bwd_dq": 4, "aux": 5}
+KERNEL_KINDS = {"schedule": 0, "fwd": 1, "bwd_d": 2, "bwd_dkdv": 3, "bwd_dq": 4, "aux": 5,
+                "norm_rope": 6, "cache": 7, "paged": 8}
+
+ROPE_LAYOUTS = {"halves": 0, "pairs": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 # Every symbol include/jfa.h declares.
 EXPORTS = ("jfa_workspace_size", "jfa_fwd", "jfa_bwd", "jfa_cross_fwd", "jfa_cross_bwd",
@@ -42,7 +48,9 @@ EXPORTS = ("jfa_workspace_size", "jfa_fwd", "jfa_bwd", "jfa_cross_fwd", "jfa_cro
            "jfa_fwd_noalloc", "jfa_bbs_plan", "jfa_pooled_workspace_size", "jfa_pooled_fwd",
            "jfa_pooled_bwd", "jfa_block_workspace_size", "jfa_block_fwd", "jfa_block_bwd",
            "jfa_test_hold", "jfa_block_rope_fwd", "jfa_block_rope_bwd", "jfa_plan",
-           "jfa_block_plan")
+           "jfa_block_plan", "jfa_norm_rope_workspace_size", "jfa_norm_rope_fwd",
+           "jfa_norm_rope_bwd", "jfa_paged_workspace_size", "jfa_cache_write", "jfa_cache_read",
+           "jfa_paged_plan", "jfa_paged_fwd")
 
 
 class JfaError(RuntimeError):
@@ -57,6 +65,32 @@ class jfa_params(ctypes.Structure):
                 ("dim_qk", ctypes.c_int32), ("dim_v", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("causal", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class _rope(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("amp", ctypes.c_float), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("orig_len", ctypes.c_double), ("turns_fast", ctypes.c_double),
+                ("turns_slow", ctypes.c_double)]
+
+
+class jfa_norm_rope_params(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("stride_q", ctypes.c_int64),
+                ("stride_k", ctypes.c_int64), ("stride_yq", ctypes.c_int64),
+                ("stride_yk", ctypes.c_int64), ("stride_dq", ctypes.c_int64),
+                ("stride_dk", ctypes.c_int64), ("heads_q", ctypes.c_int32),
+                ("heads_k", ctypes.c_int32), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("rope", _rope)]
+
+
+class jfa_paged_params(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("total_q", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("stride_q", ctypes.c_int64), ("stride_k", ctypes.c_int64),
+                ("stride_v", ctypes.c_int64), ("heads_q", ctypes.c_int32),
+                ("heads_k", ctypes.c_int32), ("dim_qk", ctypes.c_int32), ("dim_v", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("causal", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("cache_dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
 
 
 _lib = None
@@ -124,6 +158,21 @@ def lib():
         L.jfa_plan.restype = ctypes.c_int
         L.jfa_block_plan.argtypes = [P, i64p, vp, sz, vp]
         L.jfa_block_plan.restype = ctypes.c_int
+        N = ctypes.POINTER(jfa_norm_rope_params)
+        G = ctypes.POINTER(jfa_paged_params)
+        L.jfa_norm_rope_workspace_size.argtypes = [N]
+        L.jfa_norm_rope_workspace_size.restype = sz
+        L.jfa_norm_rope_fwd.argtypes = [N] + [vp] * 8
+        L.jfa_norm_rope_bwd.argtypes = [N] + [vp] * 12 + [sz, vp]
+        L.jfa_paged_workspace_size.argtypes = [G]
+        L.jfa_paged_workspace_size.restype = sz
+        L.jfa_cache_write.argtypes = [G] + [vp] * 10 + [sz, vp]
+        L.jfa_cache_read.argtypes = [G] + [vp] * 10 + [sz, vp]
+        L.jfa_paged_plan.argtypes = [G, vp, vp, vp, sz, vp]
+        L.jfa_paged_fwd.argtypes = [G] + [vp] * 11 + [sz, vp]
+        for f in ("jfa_norm_rope_fwd", "jfa_norm_rope_bwd", "jfa_cache_write", "jfa_cache_read",
+                  "jfa_paged_plan", "jfa_paged_fwd"):
+            getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -450,3 +499,264 @@ def jfa_block_bwd(q, k, v, o, lse, dout, offs, *, scale=None, causal=False, dq=N
                                 _ptr(dout), _ptr(offs), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws),
                                 ws.numel(), _stream(stream)), name)
     return dq, dk, dv
+
+
+# ----------------------------------------------------------------------------- shared checks
+def _on(device, stream):
+    """The raw stream of a call whose tensors live on ``device``, which must be current."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError("tensors are on %s, which is not the current device" % device)
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    if stream.device != device:
+        raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device, device))
+    return stream.cuda_stream
+
+
+def _rows(name, t, dtype, device, heads=None, dim=None, tokens=None):
+    """Checks [T, heads, dim] rows with contiguous heads; returns the stride between tokens."""
+    if t.dim() != 3 or not t.is_cuda or t.device != device or t.dtype != dtype:
+        raise ValueError("%s must be a [tokens, heads, dim] %s tensor on %s" % (name, dtype, device))
+    if (heads not in (None, t.shape[1]) or dim not in (None, t.shape[2])
+            or tokens not in (None, t.shape[0])):
+        raise ValueError("%s has shape %s, which does not fit the other arguments" % (name, tuple(t.shape)))
+    if t.numel() and ((t.shape[2] > 1 and t.stride(2) != 1)
+                      or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _plain(name, t, dtype, shape, device):
+    if (not t.is_cuda or t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape)
+            or not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+                         % (name, dtype, tuple(shape), device))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+# ----------------------------------------------------------------------------- norms, rotary positions
+def jfa_rope(dim, *, layout="halves", base=10000.0, scaling="none", factor=1.0, orig_len=0.0,
+             turns_fast=32.0, turns_slow=1.0, amp=1.0):
+    """The rotation of jfa_norm_rope_*: the first ``dim`` columns of every head, in ``layout``
+    "halves" or "pairs", frequencies changed by ``scaling`` ("none", "linear", "ntk", "yarn")."""
+    return _rope(int(dim), ROPE_LAYOUTS[layout], ROPE_SCALINGS[scaling], amp, base, factor, orig_len,
+                 turns_fast, turns_slow)
+
+
+def _norm_rope_params(q, k, pos, wq, wk, eps, rope, norm):
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q and k are both None")
+    if not x.is_cuda or x.dim() != 3:
+        raise ValueError("q and k must be [tokens, heads, dim] CUDA tensors")
+    if not norm and (wq is not None or wk is not None):
+        raise ValueError("norm=False takes no weights")
+    T, _, D = x.shape
+    p = jfa_norm_rope_params(tokens=T, dim=D, dtype=_dtype_code(x.dtype), norm=int(bool(norm)), eps=eps)
+    if rope is not None:
+        p.rope = rope
+        _plain("pos", pos, torch.int64, (T,), x.device)
+    if q is not None:
+        p.stride_q, p.heads_q = _rows("q", q, x.dtype, x.device, None, D, T), q.shape[1]
+    if k is not None:
+        p.stride_k, p.heads_k = _rows("k", k, x.dtype, x.device, None, D, T), k.shape[1]
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            _plain(name, w, torch.float32, (D,), x.device)
+    return p, x
+
+
+def _like(t):
+    return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def jfa_norm_rope_fwd(q, k, pos, wq=None, wk=None, *, rope=None, eps=1e-6, norm=True, yq=None,
+                      yk=None, stream=None):
+    """RMS norm of every head of q [T, Hq, D] and k [T, Hk, D] (either may be None) with the
+    rotary position embedding ``rope`` (jfa_rope) at positions ``pos`` [T]; returns (yq, yk)."""
+    p, x = _norm_rope_params(q, k, pos, wq, wk, eps, rope, norm)
+    if q is not None:
+        yq = _like(q) if yq is None else yq
+        p.stride_yq = _rows("yq", yq, q.dtype, q.device, *q.shape[1:], q.shape[0])
+    if k is not None:
+        yk = _like(k) if yk is None else yk
+        p.stride_yk = _rows("yk", yk, k.dtype, k.device, *k.shape[1:], k.shape[0])
+    _check(lib().jfa_norm_rope_fwd(ctypes.byref(p), _addr(q), _addr(k), _addr(pos), _addr(wq), _addr(wk),
+                                   _addr(yq), _addr(yk), _on(x.device, stream)), "jfa_norm_rope_fwd")
+    return yq, yk
+
+
+def jfa_norm_rope_bwd(q, k, pos, dyq, dyk, wq=None, wk=None, *, rope=None, eps=1e-6, norm=True,
+                      dq=None, dk=None, dwq=None, dwk=None, ws=None, stream=None):
+    """Backward of jfa_norm_rope_fwd; returns (dq, dk, dwq, dwk).  The weights' gradients are
+    summed over tokens and heads in fp32 (None where the norm has no such weight)."""
+    p, x = _norm_rope_params(q, k, pos, wq, wk, eps, rope, norm)
+    f32 = dict(dtype=torch.float32, device=x.device)
+    if q is not None:
+        p.stride_yq = _rows("dyq", dyq, q.dtype, q.device, *q.shape[1:], q.shape[0])
+        dq = _like(q) if dq is None else dq
+        p.stride_dq = _rows("dq", dq, q.dtype, q.device, *q.shape[1:], q.shape[0])
+        if wq is not None and dwq is None:
+            dwq = torch.empty(p.dim, **f32)
+    if k is not None:
+        p.stride_yk = _rows("dyk", dyk, k.dtype, k.device, *k.shape[1:], k.shape[0])
+        dk = _like(k) if dk is None else dk
+        p.stride_dk = _rows("dk", dk, k.dtype, k.device, *k.shape[1:], k.shape[0])
+        if wk is not None and dwk is None:
+            dwk = torch.empty(p.dim, **f32)
+    for name, w in (("dwq", dwq), ("dwk", dwk)):
+        if w is not None:
+            _plain(name, w, torch.float32, (p.dim,), x.device)
+    if ws is None:
+        n = int(lib().jfa_norm_rope_workspace_size(ctypes.byref(p)))
+        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=x.device)
+    _check(lib().jfa_norm_rope_bwd(ctypes.byref(p), _addr(q), _addr(k), _addr(pos), _addr(wq), _addr(wk),
+                                   _addr(dyq), _addr(dyk), _addr(dq), _addr(dk), _addr(dwq), _addr(dwk),
+                                   _addr(ws), ws.numel(), _on(x.device, stream)), "jfa_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+# ----------------------------------------------------------------------------- paged cache
+class PagedCache:
+    """The arrays of a paged cache: k [pages, heads, page_size, dim], v likewise; with
+    k_scale and v_scale (uint8 [pages, heads, page_size, dim / 32]) k and v are uint8 MXFP8
+    codes, without them values."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or v.dim() != 4 or k.shape[:3] != v.shape[:3]:
+            raise ValueError("k and v must be [pages, heads, page_size, dim] with the same pages")
+        for name, t, s in (("k", k, k_scale), ("v", v, v_scale)):
+            if not t.is_cuda or not t.is_contiguous() or t.device != k.device:
+                raise ValueError("the cache's arrays must be contiguous CUDA tensors on one device")
+            if (k_scale is None) != (s is None):
+                raise ValueError("k_scale and v_scale belong together")
+            if s is None:
+                if t.dtype not in (torch.float32, torch.bfloat16) or t.dtype != k.dtype:
+                    raise ValueError("%s must be fp32 or bf16 values, as k is" % name)
+            else:
+                if t.dtype != torch.uint8 or t.shape[3] % 32:
+                    raise ValueError("%s must be uint8 codes, columns a multiple of 32" % name)
+                _plain(name + "_scale", s, torch.uint8, (*t.shape[:3], t.shape[3] // 32), k.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.mxfp8 = k_scale is not None
+        self.pages, self.heads, self.page_size, self.dim_qk = k.shape
+        self.dim_v = v.shape[3]
+
+    @property
+    def device(self):
+        return self.k.device
+
+
+def paged_cache(pages, heads, dim_qk, dim_v=None, *, page_size=64, dtype=torch.bfloat16, mxfp8=False,
+                device="cuda"):
+    """An empty PagedCache of values of ``dtype``, or of MXFP8 codes."""
+    dim_v = dim_qk if dim_v is None else dim_v
+    new = lambda d, t: torch.zeros(pages, heads, page_size, d, dtype=t, device=device)
+    if not mxfp8:
+        return PagedCache(new(dim_qk, dtype), new(dim_v, dtype))
+    u = torch.uint8
+    return PagedCache(new(dim_qk, u), new(dim_v, u), new(dim_qk // 32, u), new(dim_v // 32, u))
+
+
+def paged_params(cache, table, offs, lens, total, dtype, *, heads_q=None, scale=None, causal=True):
+    """Params of the calls on a paged cache (strides of contiguous rows)."""
+    hk, d, dv = cache.heads, cache.dim_qk, cache.dim_v
+    hq = hk if heads_q is None else heads_q
+    if cache.mxfp8:
+        kind = JFA_MXFP8
+    else:
+        kind = _dtype_code(cache.k.dtype)
+    return jfa_paged_params(offs.numel() - 1, total, cache.pages, hq * d, hk * d, hk * dv, hq, hk, d, dv,
+                            cache.page_size, table.shape[1],
+                            1.0 / math.sqrt(d) if scale is None else scale, int(bool(causal)),
+                            _dtype_code(dtype), kind, 0)
+
+
+def paged_workspace(p: jfa_paged_params, device="cuda") -> torch.Tensor:
+    """A workspace for every call on a paged cache with these params."""
+    return torch.empty(max(int(lib().jfa_paged_workspace_size(ctypes.byref(p))), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def _paged_prep(cache, table, offs, lens, total, dtype, heads_q, scale, causal, ws, planned):
+    dev = cache.device
+    if offs.dim() != 1 or offs.numel() < 1 or table.dim() != 2:
+        raise ValueError("offs must be [B + 1], table [B, max_pages]")
+    B = offs.numel() - 1
+    _plain("offs", offs, torch.int64, (B + 1,), dev)
+    _plain("lens", lens, torch.int64, (B,), dev)
+    _plain("table", table, torch.int32, (B, table.shape[1]), dev)
+    p = paged_params(cache, table, offs, lens, total, dtype, heads_q=heads_q, scale=scale, causal=causal)
+    if planned:
+        if ws is None:
+            raise ValueError("a planned call needs the workspace its plan was built in")
+        p.flags = JFA_PLANNED
+    if ws is None:
+        ws = paged_workspace(p, dev)
+    elif not ws.is_cuda or ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous uint8 tensor on %s" % dev)
+    return p, ws
+
+
+def jfa_cache_write(k, v, cache, table, offs, lens, *, ws=None, stream=None, planned=False):
+    """Writes the new tokens' k [T, Hk, Dqk] and v [T, Hk, Dv] into their pages of ``cache``:
+    token i of sequence b at position lens[b] - L_b + i.  Returns the workspace, whose status
+    word jfa_status_check reads."""
+    p, ws = _paged_prep(cache, table, offs, lens, k.shape[0], k.dtype, None, None, True, ws, planned)
+    p.stride_k = _rows("k", k, k.dtype, cache.device, cache.heads, cache.dim_qk)
+    p.stride_v = _rows("v", v, k.dtype, cache.device, cache.heads, cache.dim_v, k.shape[0])
+    _check(lib().jfa_cache_write(ctypes.byref(p), _addr(k), _addr(v), _addr(offs), _addr(lens), _addr(table),
+                                 _addr(cache.k), _addr(cache.v), _addr(cache.k_scale), _addr(cache.v_scale),
+                                 _addr(ws), ws.numel(), _on(cache.device, stream)), "jfa_cache_write")
+    return ws
+
+
+def jfa_cache_read(cache, table, offs, lens, total, *, dtype=torch.bfloat16, k=None, v=None, ws=None,
+                   stream=None, planned=False):
+    """The last L_b cached rows of every sequence, ``total`` = offs[B] of them, gathered into
+    (k [total, Hk, Dqk], v [total, Hk, Dv]) of ``dtype``."""
+    p, ws = _paged_prep(cache, table, offs, lens, total, dtype, None, None, True, ws, planned)
+    dev = cache.device
+    kshape, vshape = (total, cache.heads, cache.dim_qk), (total, cache.heads, cache.dim_v)
+    k = torch.empty(kshape, dtype=dtype, device=dev) if k is None else k
+    v = torch.empty(vshape, dtype=dtype, device=dev) if v is None else v
+    _plain("k", k, dtype, kshape, dev)
+    _plain("v", v, dtype, vshape, dev)
+    _check(lib().jfa_cache_read(ctypes.byref(p), _addr(cache.k), _addr(cache.v), _addr(cache.k_scale),
+                                _addr(cache.v_scale), _addr(offs), _addr(lens), _addr(table), _addr(k),
+                                _addr(v), _addr(ws), ws.numel(), _on(dev, stream)), "jfa_cache_read")
+    return k, v
+
+
+def jfa_paged_plan(q, cache, table, offs, lens, *, causal=True, ws=None, stream=None):
+    """The shares of work of a step's calls on ``cache`` (same offs and lens), built into
+    ``ws`` (allocated if None); returns ``ws`` for calls with ``planned=True``."""
+    p, ws = _paged_prep(cache, table, offs, lens, q.shape[0], q.dtype, q.shape[1], None, causal, ws, False)
+    p.stride_q = _rows("q", q, q.dtype, cache.device, None, cache.dim_qk)
+    _check(lib().jfa_paged_plan(ctypes.byref(p), _addr(offs), _addr(lens), _addr(ws), ws.numel(),
+                                _on(cache.device, stream)), "jfa_paged_plan")
+    return ws
+
+
+def jfa_paged_fwd(q, cache, table, offs, lens, *, scale=None, causal=True, o=None, lse=None, ws=None,
+                  stream=None, planned=False):
+    """Attention of the new tokens' queries q [T, Hq, Dqk] over their sequences' cached keys
+    and values (the new tokens' own among them), Hq a multiple of the cache's heads; returns
+    (o [T, Hq, Dv], lse [T, Hq])."""
+    p, ws = _paged_prep(cache, table, offs, lens, q.shape[0], q.dtype, q.shape[1], scale, causal, ws, planned)
+    dev = cache.device
+    p.stride_q = _rows("q", q, q.dtype, dev, None, cache.dim_qk)
+    T, H = q.shape[0], q.shape[1]
+    if o is None:
+        o = torch.empty(T, H, cache.dim_v, dtype=q.dtype, device=dev)
+    if lse is None:
+        lse = torch.empty(T, H, dtype=torch.float32, device=dev)
+    _plain("o", o, q.dtype, (T, H, cache.dim_v), dev)
+    _plain("lse", lse, torch.float32, (T, H), dev)
+    _check(lib().jfa_paged_fwd(ctypes.byref(p), _addr(q), _addr(cache.k), _addr(cache.v), _addr(cache.k_scale),
+                               _addr(cache.v_scale), _addr(offs), _addr(lens), _addr(table), _addr(o),
+                               _addr(lse), _addr(ws), ws.numel(), _on(dev, stream)), "jfa_paged_fwd")
+    return o, lse

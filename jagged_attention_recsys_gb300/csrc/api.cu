@@ -10,6 +10,7 @@
 
 #include "internal.h"
 #include "tc.h"
+#include "timed.h"
 
 namespace jfa {
 
@@ -146,31 +147,28 @@ jfa_status drain() {
   return st;
 }
 
-// Records events around one launch when profiling is on.
-struct Timed {
-  int kind;
-  cudaStream_t s;
-  cudaEvent_t a = nullptr, b = nullptr;
-  Timed(int k, cudaStream_t st) : kind(k), s(st) {
-    if (!prof().on) return;
-    if (prof().pending.size() > 65536) drain();
-    a = take_event();
-    b = take_event();
-    if (!a || !b) {  // no timing for this launch; keep whichever event was made
-      if (a) prof().pool.push_back(a);
-      if (b) prof().pool.push_back(b);
-      a = b = nullptr;
-      return;
-    }
-    cudaEventRecord(a, s);
-  }
-  ~Timed() {
-    if (!a || !b) return;
-    cudaEventRecord(b, s);
-    prof().pending.push_back({kind, a, b});
-  }
-};
+}  // namespace
 
+Timed::Timed(int k, cudaStream_t st) : kind(k), s(st) {
+  if (!prof().on) return;
+  if (prof().pending.size() > 65536) drain();
+  a = take_event();
+  b = take_event();
+  if (!a || !b) {  // no timing for this launch; keep whichever event was made
+    if (a) prof().pool.push_back(a);
+    if (b) prof().pool.push_back(b);
+    a = b = nullptr;
+    return;
+  }
+  cudaEventRecord(a, s);
+}
+Timed::~Timed() {
+  if (!a || !b) return;
+  cudaEventRecord(b, s);
+  prof().pending.push_back({kind, a, b});
+}
+
+namespace {
 inline jfa_status cu(cudaError_t e) { return e == cudaSuccess ? JFA_OK : JFA_ERR_CUDA; }
 
 // A second stream per device and host thread, with a fork and a join event, for
@@ -721,7 +719,7 @@ jfa_status jfa_status_check(const void* ws, jfa_stream_t stream) {
   if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return JFA_ERR_CUDA;
   int st = 0;
   if (cudaMemcpy(&st, ws, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return JFA_ERR_CUDA;
-  if (st < 0 || st > JFA_ERR_CUDA) return JFA_ERR_CUDA;
+  if (st < 0 || st > JFA_ERR_BAD_PAGES) return JFA_ERR_CUDA;
   return (jfa_status)st;
 }
 
@@ -734,6 +732,7 @@ const char* jfa_status_string(jfa_status s) {
     case JFA_ERR_BAD_OFFSETS: return "offsets are not a valid jagged layout";
     case JFA_ERR_TIMEOUT: return "a bounded wait inside a kernel timed out";
     case JFA_ERR_CUDA: return "CUDA error";
+    case JFA_ERR_BAD_PAGES: return "a page table names a page outside the cache";
   }
   return "unknown status";
 }
