@@ -108,10 +108,12 @@ paged_plan_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
     w.hdr->status = bad ? JFA_ERR_BAD_OFFSETS : JFA_OK;
     w.hdr->n_ctas = ctas;
   }
+  // little work goes to fewer CTAs, so that a share is worth its tile's fixed cost
+  const int64_t n = max((int64_t)1, min((int64_t)ctas, W / t.share));
   for (int c = tid; c <= ctas; c += kPlanThreads) {
     PagedPos r{(int)B, 0, 0, 0};  // the end; a bad batch begins there
-    const int64_t x = W / ctas * c + W % ctas * c / ctas;
-    if (!bad && c < ctas && x < W) {
+    const int64_t x = W / n * c + W % n * c / n;
+    if (!bad && c < n && x < W) {
       int64_t lo = 0, hi = B - 1;
       while (lo < hi) {  // the first b with cum[b + 1] > x
         const int64_t m = (lo + hi) >> 1;
@@ -348,22 +350,30 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-int paged_kernel(const Paged&, int) { return kPagedSimt; }
+// The tensor-core kernels take bf16 queries at dims 64 and 128 whose cache rows a 32-bit index
+// reaches (TMA coordinates); everything else runs on CUDA cores.
+int paged_kernel(const Paged& p, int dtype) {
+  const bool dims = (p.dim_qk == 64 || p.dim_qk == 128) && (p.dim_v == 64 || p.dim_v == 128);
+  const int64_t rows = (p.pages * p.heads_k) << p.page_shift;
+  if (dtype != JFA_BF16 || !dims || p.pages == 0 || p.total_q == 0 || rows >= INT32_MAX) return kPagedSimt;
+  return kPagedRows16;
+}
 
-TileShape paged_shape(const Paged& p, int) {
+TileShape paged_shape(const Paged& p, int kernel) {
   TileShape t;
   const int most = kRows;
   t.gsub = p.group < most ? p.group : most;
   t.nsub = (p.group + t.gsub - 1) / t.gsub;
   t.tokens = most / t.gsub;
   t.rows = t.tokens * t.gsub;
-  t.keys = kKeys;
-  t.overhead = kKeys;
+  t.keys = kernel == kPagedRows16 ? paged_rows16_keys(p.dim_qk, p.dim_v, p.kind) : kKeys;
+  t.overhead = kernel == kPagedRows16 ? 64 : kKeys;
+  t.share = kernel == kPagedRows16 ? 192 : kKeys;
   return t;
 }
 
-int paged_ctas(const Paged&, int) {
-  const int n = num_sms() * 3;
+int paged_ctas(const Paged&, int kernel) {
+  const int n = num_sms() * (kernel == kPagedRows16 ? 2 : 3);
   return n < kMaxPagedCtas ? n : kMaxPagedCtas;
 }
 

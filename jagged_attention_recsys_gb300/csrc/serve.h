@@ -80,9 +80,14 @@ static_assert(sizeof(PagedHeader) == 256, "workspace header");
 struct TileShape {
   int rows, tokens, gsub, nsub, keys;
   int overhead;  // cost of a tile beside its keys, in keys
+  int share;     // least cost of a CTA's share
 };
 
 constexpr int kMaxPagedCtas = 640;
+// Keys of a block of the 16-row kernel.
+constexpr int paged_rows16_keys(int dim_qk, int dim_v, int kind) {
+  return kind == kCacheBf16 && dim_qk + dim_v > 192 ? 16 : 32;
+}
 
 struct PagedWs {
   PagedHeader* hdr;
@@ -105,6 +110,7 @@ cudaError_t launch_cache_read(const Paged& p, int dtype, void* k, void* v, Paged
 cudaError_t launch_paged_plan(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
 cudaError_t launch_paged_simt(const Paged& p, const TileShape& t, int ctas, int dtype, const PagedWs& w,
                               cudaStream_t s);
+cudaError_t launch_paged_rows16(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
 cudaError_t launch_paged_combine(const Paged& p, const TileShape& t, int ctas, int dtype, const PagedWs& w,
                                  cudaStream_t s);
 
