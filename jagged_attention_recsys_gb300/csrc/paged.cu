@@ -322,6 +322,7 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
       const int64_t pr = slot_row(i);
       const float f = exp2f(w.part_ml[2 * pr] - ref);
       l = fmaf(w.part_ml[2 * pr + 1], f, l);
+      if (w.part_ml[2 * pr] == -INFINITY) continue;  // no keys: the part has no output
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (lane + 32 * k < p.dim_v) acc[k] = fmaf(w.part_o[pr * p.dim_v + lane + 32 * k], f, acc[k]);
@@ -356,11 +357,24 @@ int paged_kernel(const Paged& p, int dtype) {
   const bool dims = (p.dim_qk == 64 || p.dim_qk == 128) && (p.dim_v == 64 || p.dim_v == 128);
   const int64_t rows = (p.pages * p.heads_k) << p.page_shift;
   if (dtype != JFA_BF16 || !dims || p.pages == 0 || p.total_q == 0 || rows >= INT32_MAX) return kPagedSimt;
-  return kPagedRows16;
+  // Rows that share a key head, over the sequences with new tokens at most: up to 16 go to one
+  // mma.sync tile, more to tcgen05's 128-row tiles (groups larger than one would split them).
+  const int64_t rows_per_seq = p.total_q * p.group / p.batch;
+  return rows_per_seq <= 16 || p.group > 128 ? kPagedRows16 : kPagedTc;
 }
 
 TileShape paged_shape(const Paged& p, int kernel) {
   TileShape t;
+  if (kernel == kPagedTc) {
+    t.gsub = p.group;
+    t.nsub = 1;
+    t.tokens = 2 * (128 / p.group);  // two MMA tiles
+    t.rows = t.tokens * t.gsub;
+    t.keys = 128;
+    t.overhead = 192;
+    t.share = 512;
+    return t;
+  }
   const int most = kRows;
   t.gsub = p.group < most ? p.group : most;
   t.nsub = (p.group + t.gsub - 1) / t.gsub;
@@ -373,6 +387,7 @@ TileShape paged_shape(const Paged& p, int kernel) {
 }
 
 int paged_ctas(const Paged&, int kernel) {
+  if (kernel == kPagedTc) return num_sms() < kMaxTcCtas ? num_sms() : kMaxTcCtas;
   const int n = num_sms() * (kernel == kPagedRows16 ? 2 : 3);
   return n < kMaxPagedCtas ? n : kMaxPagedCtas;
 }
@@ -388,7 +403,7 @@ size_t paged_layout(const Paged& p, void* base, PagedWs* out) {
   off = up256(off + sizeof(PagedPos) * (kMaxPagedCtas + 2));
   w.cum = (int64_t*)(b + off);
   off = up256(off + sizeof(int64_t) * (size_t)(p.batch + 1));
-  constexpr size_t rows = (size_t)2 * kMaxPagedCtas * 16;
+  constexpr size_t rows = 2 * (kMaxPagedCtas * 16 > kMaxTcCtas * 256 ? kMaxPagedCtas * 16 : kMaxTcCtas * 256);
   w.part_ml = (float*)(b + off);
   off = up256(off + sizeof(float) * 2 * rows);
   w.part_o = (float*)(b + off);

@@ -83,7 +83,7 @@ struct TileShape {
   int share;     // least cost of a CTA's share
 };
 
-constexpr int kMaxPagedCtas = 640;
+constexpr int kMaxPagedCtas = 640, kMaxTcCtas = 160;
 // Keys of a block of the 16-row kernel.
 constexpr int paged_rows16_keys(int dim_qk, int dim_v, int kind) {
   return kind == kCacheBf16 && dim_qk + dim_v > 192 ? 16 : 32;
@@ -111,6 +111,7 @@ cudaError_t launch_paged_plan(const Paged& p, const TileShape& t, int ctas, cons
 cudaError_t launch_paged_simt(const Paged& p, const TileShape& t, int ctas, int dtype, const PagedWs& w,
                               cudaStream_t s);
 cudaError_t launch_paged_rows16(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
+cudaError_t launch_paged_tc(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
 cudaError_t launch_paged_combine(const Paged& p, const TileShape& t, int ctas, int dtype, const PagedWs& w,
                                  cudaStream_t s);
 

@@ -325,8 +325,9 @@ jfa_status jfa_paged_fwd(const jfa_paged_params* p, const void* q, const void* k
   const TileShape shape = paged_shape(r, kernel);
   const int ctas = paged_ctas(r, kernel);
   Timed t(JFA_KERNEL_PAGED, s);
-  st = cu(kernel == kPagedRows16 ? launch_paged_rows16(r, shape, ctas, w, s)
-                                 : launch_paged_simt(r, shape, ctas, p->dtype, w, s));
+  st = cu(kernel == kPagedTc       ? launch_paged_tc(r, shape, ctas, w, s)
+          : kernel == kPagedRows16 ? launch_paged_rows16(r, shape, ctas, w, s)
+                                   : launch_paged_simt(r, shape, ctas, p->dtype, w, s));
   if (st != JFA_OK) return st;
   return cu(launch_paged_combine(r, shape, ctas, p->dtype, w, s));
 }
