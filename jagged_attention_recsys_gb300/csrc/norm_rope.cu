@@ -29,6 +29,7 @@
 
 #include "internal.h"
 #include "serve.h"
+#include "tc_ptx.cuh"
 
 namespace jfa {
 namespace {
@@ -37,36 +38,64 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int V = 16;  // values of a lane slot
 
+// A slot's values as eight pairs (a_i, b_i), two to a float2: a[j] = (a_2j, a_2j+1).
+struct Slot16 {
+  float2 a[4], b[4];
+};
+
+// A slot as it lies in memory: columns [a, a + 8) and [b, b + 8).
 template <typename T>
-struct Row16;
+struct Raw16;
 template <>
-struct Row16<__nv_bfloat16> {
+struct Raw16<__nv_bfloat16> {
+  static constexpr int kBatch = 4;  // rows a lane has in flight
   uint4 a, b;
   __device__ void load(const __nv_bfloat16* pa, const __nv_bfloat16* pb) {
     a = __ldcs(reinterpret_cast<const uint4*>(pa));
     b = __ldcs(reinterpret_cast<const uint4*>(pb));
   }
-  __device__ void get(float (&v)[V]) const {
+  __device__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
+  static __device__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+  static __device__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+  template <int LAYOUT>
+  __device__ void get(Slot16& s) const {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int j = 0; j < 4; ++j) {
+      if (LAYOUT == JFA_ROPE_HALVES) {
+        s.a[j] = make_float2(lo(w[j]), hi(w[j]));
+        s.b[j] = make_float2(lo(w[4 + j]), hi(w[4 + j]));
+      } else {
+        s.a[j] = make_float2(lo(w[2 * j]), lo(w[2 * j + 1]));
+        s.b[j] = make_float2(hi(w[2 * j]), hi(w[2 * j + 1]));
+      }
     }
   }
-  static __device__ uint32_t pack(float lo, float hi) {  // round to nearest even, the result's type
+  static __device__ uint32_t pack(float x, float y) {  // round to nearest even: the result's type
     uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
     return r;
   }
-  static __device__ void store(__nv_bfloat16* pa, __nv_bfloat16* pb, const float (&v)[V]) {
-    __stcs(reinterpret_cast<uint4*>(pa), make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7])));
-    __stcs(reinterpret_cast<uint4*>(pb),
-           make_uint4(pack(v[8], v[9]), pack(v[10], v[11]), pack(v[12], v[13]), pack(v[14], v[15])));
+  template <int LAYOUT>
+  static __device__ void store(__nv_bfloat16* pa, __nv_bfloat16* pb, const Slot16& s) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (LAYOUT == JFA_ROPE_HALVES) {
+        w[j] = pack(s.a[j].x, s.a[j].y);
+        w[4 + j] = pack(s.b[j].x, s.b[j].y);
+      } else {
+        w[2 * j] = pack(s.a[j].x, s.b[j].x);
+        w[2 * j + 1] = pack(s.a[j].y, s.b[j].y);
+      }
+    }
+    __stcs(reinterpret_cast<uint4*>(pa), make_uint4(w[0], w[1], w[2], w[3]));
+    __stcs(reinterpret_cast<uint4*>(pb), make_uint4(w[4], w[5], w[6], w[7]));
   }
 };
 template <>
-struct Row16<float> {
+struct Raw16<float> {
+  static constexpr int kBatch = 2;
   float4 q[4];
   __device__ void load(const float* pa, const float* pb) {
     q[0] = __ldcs(reinterpret_cast<const float4*>(pa));
@@ -74,20 +103,38 @@ struct Row16<float> {
     q[2] = __ldcs(reinterpret_cast<const float4*>(pb));
     q[3] = __ldcs(reinterpret_cast<const float4*>(pb) + 1);
   }
-  __device__ void get(float (&v)[V]) const {
+  __device__ void zero() { q[0] = q[1] = q[2] = q[3] = make_float4(0.f, 0.f, 0.f, 0.f); }
+  template <int LAYOUT>
+  __device__ void get(Slot16& s) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[4 * i] = q[i].x;
-      v[4 * i + 1] = q[i].y;
-      v[4 * i + 2] = q[i].z;
-      v[4 * i + 3] = q[i].w;
+    for (int j = 0; j < 4; ++j) {
+      if (LAYOUT == JFA_ROPE_HALVES) {
+        const float4 x = q[j >> 1], y = q[2 + (j >> 1)];
+        s.a[j] = j & 1 ? make_float2(x.z, x.w) : make_float2(x.x, x.y);
+        s.b[j] = j & 1 ? make_float2(y.z, y.w) : make_float2(y.x, y.y);
+      } else {
+        s.a[j] = make_float2(q[j].x, q[j].z);
+        s.b[j] = make_float2(q[j].y, q[j].w);
+      }
     }
   }
-  static __device__ void store(float* pa, float* pb, const float (&v)[V]) {
-    __stcs(reinterpret_cast<float4*>(pa), make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(reinterpret_cast<float4*>(pa) + 1, make_float4(v[4], v[5], v[6], v[7]));
-    __stcs(reinterpret_cast<float4*>(pb), make_float4(v[8], v[9], v[10], v[11]));
-    __stcs(reinterpret_cast<float4*>(pb) + 1, make_float4(v[12], v[13], v[14], v[15]));
+  template <int LAYOUT>
+  static __device__ void store(float* pa, float* pb, const Slot16& s) {
+    float4 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (LAYOUT == JFA_ROPE_HALVES) {
+        const float2* v = j < 2 ? s.a : s.b;
+        const int k = 2 * (j & 1);
+        w[j] = make_float4(v[k].x, v[k].y, v[k + 1].x, v[k + 1].y);
+      } else {
+        w[j] = make_float4(s.a[j].x, s.b[j].x, s.a[j].y, s.b[j].y);
+      }
+    }
+    __stcs(reinterpret_cast<float4*>(pa), w[0]);
+    __stcs(reinterpret_cast<float4*>(pa) + 1, w[1]);
+    __stcs(reinterpret_cast<float4*>(pb), w[2]);
+    __stcs(reinterpret_cast<float4*>(pb) + 1, w[3]);
   }
 };
 
@@ -119,15 +166,48 @@ __device__ __forceinline__ Slot slot_of(int slot, int rot, int layout) {
   return r;
 }
 
-// v turned by cs (sign = 1) or back (sign = -1)
-template <int LAYOUT>
-__device__ __forceinline__ void turn16(float (&v)[V], const float2 (&cs)[8], float sign) {
+// The rotations of a token's pairs, computed once by the warp, two to four pairs a lane, into
+// its table (cosines, then sines).
+constexpr int kMaxPairs = kMaxNormDim / 2;
+struct Turns {
+  unsigned long long turn[kMaxPairs / 32];
+  __device__ __forceinline__ void init(const NormRopeArgs& p, int lane) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int ia = LAYOUT == JFA_ROPE_HALVES ? i : 2 * i, ib = LAYOUT == JFA_ROPE_HALVES ? 8 + i : 2 * i + 1;
-    const float a = v[ia], b = v[ib], s = sign * cs[i].y;
-    v[ia] = fmaf(a, cs[i].x, -b * s);
-    v[ib] = fmaf(a, s, b * cs[i].x);
+    for (int i = 0; i < kMaxPairs / 32; ++i) turn[i] = p.turn[lane + 32 * i];
+  }
+  __device__ __forceinline__ void table(float* tb, const NormRopeArgs& p, int64_t pos, int lane) const {
+    __syncwarp();  // the last token's reads are done
+#pragma unroll
+    for (int i = 0; i < kMaxPairs / 32; ++i) {
+      const int k = lane + 32 * i;
+      if (32 * i < p.rot / 2 && k < p.rot / 2) {
+        const float2 cs = rotation(pos, turn[i], p.amp);
+        tb[k] = cs.x;
+        tb[kMaxPairs + k] = cs.y;
+      }
+    }
+    __syncwarp();
+  }
+};
+__device__ __forceinline__ void load4(float2 (&v)[4], const float* x) {  // eight floats of shared memory
+  const float4 p = *reinterpret_cast<const float4*>(x), q = *reinterpret_cast<const float4*>(x + 4);
+  v[0] = make_float2(p.x, p.y);
+  v[1] = make_float2(p.z, p.w);
+  v[2] = make_float2(q.x, q.y);
+  v[3] = make_float2(q.z, q.w);
+}
+// The slot's pairs turned by the table's angles, backwards with BACK.
+template <bool BACK>
+__device__ __forceinline__ void turn16(Slot16& v, const float* tb, int pair0) {
+  float2 c[4], s[4];
+  load4(c, tb + pair0);
+  load4(s, tb + kMaxPairs + pair0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 a = v.a[j], b = v.b[j];
+    const float2 sn = make_float2(-s[j].x, -s[j].y);
+    v.a[j] = tc::ffma2(a, c[j], tc::fmul2(b, BACK ? s[j] : sn));
+    v.b[j] = tc::ffma2(b, c[j], tc::fmul2(a, BACK ? sn : s[j]));
   }
 }
 
@@ -136,98 +216,117 @@ __device__ __forceinline__ float group_sum(float x, int group) {
   return x;
 }
 
-__device__ __forceinline__ void load_weight(float (&w)[V], const float* p, const Slot& sl, bool lane_ok) {
+// The slot's weights out of a row of dim floats in shared memory, in the slot's order
+template <int LAYOUT>
+__device__ __forceinline__ void weights16(Slot16& w, const float* row, const Slot& sl) {
+  if (LAYOUT == JFA_ROPE_HALVES) {
+    load4(w.a, row + sl.a);
+    load4(w.b, row + sl.b);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    w[i] = p && lane_ok ? __ldg(p + sl.a + i) : 1.f;
-    w[8 + i] = p && lane_ok ? __ldg(p + sl.b + i) : 1.f;
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = *reinterpret_cast<const float4*>(row + sl.a + 4 * j);
+      w.a[j] = make_float2(x.x, x.z);
+      w.b[j] = make_float2(x.y, x.w);
+    }
   }
 }
 
-// The rows of one token's part, warp by warp.  group lanes (a power of two) serve a row, of
-// which slots = D/16 have values; parts warps share a token's heads.
+// group lanes (a power of two) serve a row, of which slots = D/16 have values; parts warps share
+// a token's heads.  A step is the 32 / group rows of one tensor that a warp takes at once.
 struct FastShape {
   int group, slots, parts;
 };
 
-// Visits the part's rows of both tensors: f(side, head, valid).  Every lane of the warp
-// calls f the same number of times.
-template <class F>
-__device__ __forceinline__ void each_row(const NormRopeArgs& p, int side, const FastShape& g, int part, int lane, F f) {
-  const int per = 32 / g.group, sub = lane / g.group, H = p.side[side].heads;
-  const int steps = (H + per - 1) / per;
-  const int s0 = (int)((int64_t)steps * part / g.parts), s1 = (int)((int64_t)steps * (part + 1) / g.parts);
-#pragma unroll 2
-  for (int s = s0; s < s1; ++s) {
-    const int h = s * per + sub;
-    f(h, h < H);
-  }
-}
-
 template <typename T, int LAYOUT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 norm_rope_fwd_kernel(const __grid_constant__ NormRopeArgs p, const FastShape g) {
-  const int lane = threadIdx.x & 31;
-  const int ls = lane % g.group;
+  __shared__ __align__(16) float tables[kWarps][2 * kMaxPairs];
+  __shared__ __align__(16) float weights[2][kMaxNormDim];
+  constexpr int U = Raw16<T>::kBatch;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < 2 * p.dim; i += kThreads) {
+    const float* w = p.side[i >= p.dim].w;
+    weights[i >= p.dim][i % p.dim] = w ? w[i % p.dim] : 1.f;
+  }
+  __syncthreads();
+  float* tb = tables[warp];
+  const int per = 32 / g.group, sub = lane / g.group, ls = lane % g.group;
   const bool lane_ok = ls < g.slots;
   const Slot sl = slot_of(lane_ok ? ls : 0, p.rot, LAYOUT);
-  unsigned long long turn[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) turn[i] = sl.rot ? p.turn[sl.pair0 + i] : 0;
+  Turns turns;
+  turns.init(p, lane);
+  const int steps_q = (p.side[0].heads + per - 1) / per, steps = steps_q + (p.side[1].heads + per - 1) / per;
   const int64_t nw = (int64_t)gridDim.x * kWarps, tasks = p.tokens * g.parts;
-  for (int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); task < tasks; task += nw) {
+  for (int64_t task = (int64_t)blockIdx.x * kWarps + warp; task < tasks; task += nw) {
     const int64_t t = task / g.parts;
     const int part = (int)(task - t * g.parts);
-    float2 cs[8];
-    if (sl.rot) {
-      const int64_t pos = __ldg(p.pos + t);
+    const int s0 = (int)((int64_t)steps * part / g.parts), s1 = (int)((int64_t)steps * (part + 1) / g.parts);
+    bool fresh = p.rot > 0;
+    for (int sb = s0; sb < s1; sb += U) {
+      Raw16<T> raw[U];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) cs[i] = rotation(pos, turn[i], p.amp);
-    }
-#pragma unroll 1
-    for (int side = 0; side < 2; ++side) {
-      const NormRopeSide& sd = p.side[side];
-      if (sd.heads == 0) continue;
-      float w[V];
-      load_weight(w, sd.w, sl, lane_ok);
-      const T* x = (const T*)sd.x + t * sd.sx;
-      T* y = (T*)sd.out + t * sd.sout;
-      each_row(p, side, g, part, lane, [&](int h, bool ok) {
-        ok = ok && lane_ok;
-        float v[V];
-        if (ok) {
-          Row16<T> r;
-          r.load(x + (int64_t)h * p.dim + sl.a, x + (int64_t)h * p.dim + sl.b);
-          r.get(v);
+      for (int u = 0; u < U; ++u) {
+        const int side = sb + u >= steps_q, h = (sb + u - (side ? steps_q : 0)) * per + sub;
+        const NormRopeSide& sd = p.side[side];
+        if (sb + u < s1 && h < sd.heads && lane_ok) {
+          const T* x = (const T*)sd.x + t * sd.sx + (int64_t)h * p.dim;
+          raw[u].load(x + sl.a, x + sl.b);
         } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i) v[i] = 0.f;
+          raw[u].zero();
         }
+      }
+      if (fresh) {  // under the first rows' loads
+        turns.table(tb, p, __ldg(p.pos + t), lane);
+        fresh = false;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (sb + u >= s1) break;
+        const int side = sb + u >= steps_q, h = (sb + u - (side ? steps_q : 0)) * per + sub;
+        const NormRopeSide& sd = p.side[side];
+        Slot16 v;
+        raw[u].template get<LAYOUT>(v);
         if (p.norm) {
-          float ss = 0.f;
+          float2 ss = tc::fmul2(v.a[0], v.a[0]);
 #pragma unroll
-          for (int i = 0; i < V; ++i) ss = fmaf(v[i], v[i], ss);
-          const float r = rsqrtf(fmaf(group_sum(ss, g.group), p.inv_dim, p.eps));
+          for (int j = 1; j < 4; ++j) ss = tc::ffma2(v.a[j], v.a[j], ss);
 #pragma unroll
-          for (int i = 0; i < V; ++i) v[i] *= r * w[i];
+          for (int j = 0; j < 4; ++j) ss = tc::ffma2(v.b[j], v.b[j], ss);
+          const float r = rsqrtf(fmaf(group_sum(ss.x + ss.y, g.group), p.inv_dim, p.eps));
+          const float2 rr = make_float2(r, r);
+          Slot16 w;
+          weights16<LAYOUT>(w, weights[side], sl);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v.a[j] = tc::fmul2(v.a[j], tc::fmul2(w.a[j], rr));
+            v.b[j] = tc::fmul2(v.b[j], tc::fmul2(w.b[j], rr));
+          }
         }
-        if (sl.rot) turn16<LAYOUT>(v, cs, 1.f);
-        if (ok) Row16<T>::store(y + (int64_t)h * p.dim + sl.a, y + (int64_t)h * p.dim + sl.b, v);
-      });
+        if (sl.rot) turn16<false>(v, tb, sl.pair0);
+        if (h < sd.heads && lane_ok) {
+          T* y = (T*)sd.out + t * sd.sout + (int64_t)h * p.dim;
+          Raw16<T>::template store<LAYOUT>(y + sl.a, y + sl.b, v);
+        }
+      }
     }
   }
 }
 
 // Adds the CTA's per-lane sums of one tensor in a fixed order (lanes of a slot, then warps)
 // and writes the CTA's partial.
-__device__ __forceinline__ void write_partial(const float (&acc)[V], const Slot& sl, const FastShape& g, int ls,
-                                              bool lane_ok, float* red, float* part, int dim) {
+template <int LAYOUT>
+__device__ __forceinline__ void write_partial(const Slot16& acc, const Slot& sl, const FastShape& g, bool lane_ok,
+                                              float* red, float* part, int dim) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    float x = acc[i];
+    const int j = i & 7;  // values 0 .. 7: a's, 8 .. 15: b's
+    const float2 two = i < 8 ? acc.a[j >> 1] : acc.b[j >> 1];
+    float x = j & 1 ? two.y : two.x;
     for (int m = 16; m >= g.group; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-    if (lane < g.group && lane_ok) red[warp * dim + (i < 8 ? sl.a + i : sl.b + i - 8)] = x;
+    const int c = LAYOUT == JFA_ROPE_HALVES ? (i < 8 ? sl.a : sl.b) + j : sl.a + 2 * j + (i >= 8);
+    if (lane < g.group && lane_ok) red[warp * dim + c] = x;
   }
   __syncthreads();
   for (int c = threadIdx.x; c < dim; c += kThreads) {
@@ -239,71 +338,99 @@ __device__ __forceinline__ void write_partial(const float (&acc)[V], const Slot&
 }
 
 template <typename T, int LAYOUT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs p, const FastShape g, float* part_ws) {
   extern __shared__ float red[];
-  const int lane = threadIdx.x & 31;
-  const int ls = lane % g.group;
+  __shared__ __align__(16) float tables[kWarps][2 * kMaxPairs];
+  __shared__ __align__(16) float weights[2][kMaxNormDim];
+  constexpr int U = Raw16<T>::kBatch / 2;  // two tensors in flight
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < 2 * p.dim; i += kThreads) {
+    const float* w = p.side[i >= p.dim].w;
+    weights[i >= p.dim][i % p.dim] = w ? w[i % p.dim] : 1.f;
+  }
+  __syncthreads();
+  float* tb = tables[warp];
+  const int per = 32 / g.group, sub = lane / g.group, ls = lane % g.group;
   const bool lane_ok = ls < g.slots;
   const Slot sl = slot_of(lane_ok ? ls : 0, p.rot, LAYOUT);
+  Turns turns;
+  turns.init(p, lane);
   const int64_t nw = (int64_t)gridDim.x * kWarps, tasks = p.tokens * g.parts;
-  unsigned long long turn[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) turn[i] = sl.rot ? p.turn[sl.pair0 + i] : 0;
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
     const NormRopeSide& sd = p.side[side];
     if (sd.heads == 0) continue;
-    float acc[V], w[V];
+    const int steps = (sd.heads + per - 1) / per;
+    Slot16 acc, w;
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    load_weight(w, sd.w, sl, lane_ok);
-    for (int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); task < tasks; task += nw) {
+    for (int j = 0; j < 4; ++j) acc.a[j] = acc.b[j] = make_float2(0.f, 0.f);
+    weights16<LAYOUT>(w, weights[side], sl);
+    for (int64_t task = (int64_t)blockIdx.x * kWarps + warp; task < tasks; task += nw) {
       const int64_t t = task / g.parts;
       const int part = (int)(task - t * g.parts);
-      float2 cs[8];
-      if (sl.rot) {
-        const int64_t pos = __ldg(p.pos + t);
+      const int s0 = (int)((int64_t)steps * part / g.parts), s1 = (int)((int64_t)steps * (part + 1) / g.parts);
+      bool fresh = p.rot > 0;
+      for (int sb = s0; sb < s1; sb += U) {
+        Raw16<T> rx[U], rd[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i] = rotation(pos, turn[i], p.amp);
+        for (int u = 0; u < U; ++u) {
+          const int h = (sb + u) * per + sub;
+          if (sb + u < s1 && h < sd.heads && lane_ok) {
+            const int64_t o = (int64_t)h * p.dim;
+            const T* dy = (const T*)sd.dy + t * sd.sdy + o;
+            rd[u].load(dy + sl.a, dy + sl.b);
+            if (p.norm) {
+              const T* x = (const T*)sd.x + t * sd.sx + o;
+              rx[u].load(x + sl.a, x + sl.b);
+            }
+          } else {
+            rd[u].zero();
+            rx[u].zero();
+          }
+        }
+        if (fresh) {
+          turns.table(tb, p, __ldg(p.pos + t), lane);
+          fresh = false;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (sb + u >= s1) break;
+          const int h = (sb + u) * per + sub;
+          Slot16 d;
+          rd[u].template get<LAYOUT>(d);
+          if (sl.rot) turn16<true>(d, tb, sl.pair0);
+          if (p.norm) {
+            Slot16 v;
+            rx[u].template get<LAYOUT>(v);
+            float2 ss = make_float2(0.f, 0.f), ux = ss;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              ss = tc::ffma2(v.a[j], v.a[j], ss);
+              ss = tc::ffma2(v.b[j], v.b[j], ss);
+              ux = tc::ffma2(tc::fmul2(d.a[j], w.a[j]), v.a[j], ux);
+              ux = tc::ffma2(tc::fmul2(d.b[j], w.b[j]), v.b[j], ux);
+            }
+            const float r = rsqrtf(fmaf(group_sum(ss.x + ss.y, g.group), p.inv_dim, p.eps));
+            const float k = group_sum(ux.x + ux.y, g.group) * p.inv_dim * r * r;
+            const float2 rr = make_float2(r, r), kn = make_float2(-k, -k);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              acc.a[j] = tc::ffma2(d.a[j], tc::fmul2(v.a[j], rr), acc.a[j]);
+              acc.b[j] = tc::ffma2(d.b[j], tc::fmul2(v.b[j], rr), acc.b[j]);
+              d.a[j] = tc::fmul2(rr, tc::ffma2(v.a[j], kn, tc::fmul2(d.a[j], w.a[j])));
+              d.b[j] = tc::fmul2(rr, tc::ffma2(v.b[j], kn, tc::fmul2(d.b[j], w.b[j])));
+            }
+          }
+          if (h < sd.heads && lane_ok) {
+            T* dx = (T*)sd.out + t * sd.sout + (int64_t)h * p.dim;
+            Raw16<T>::template store<LAYOUT>(dx + sl.a, dx + sl.b, d);
+          }
+        }
       }
-      const T* x = (const T*)sd.x + t * sd.sx;
-      const T* dy = (const T*)sd.dy + t * sd.sdy;
-      T* dx = (T*)sd.out + t * sd.sout;
-      each_row(p, side, g, part, lane, [&](int h, bool ok) {
-        ok = ok && lane_ok;
-        float v[V], d[V];
-        if (ok) {
-          Row16<T> rx, rd;
-          const int64_t o = (int64_t)h * p.dim;
-          if (p.norm) rx.load(x + o + sl.a, x + o + sl.b);
-          rd.load(dy + o + sl.a, dy + o + sl.b);
-          if (p.norm) rx.get(v);
-          rd.get(d);
-        } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i) v[i] = d[i] = 0.f;
-        }
-        if (sl.rot) turn16<LAYOUT>(d, cs, -1.f);
-        if (p.norm) {
-          float ss = 0.f, ux = 0.f;
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            ss = fmaf(v[i], v[i], ss);
-            ux = fmaf(d[i] * w[i], v[i], ux);
-          }
-          const float r = rsqrtf(fmaf(group_sum(ss, g.group), p.inv_dim, p.eps));
-          const float k = group_sum(ux, g.group) * p.inv_dim * r * r;
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            acc[i] = fmaf(d[i], v[i] * r, acc[i]);
-            d[i] = r * fmaf(-v[i], k, d[i] * w[i]);
-          }
-        }
-        if (ok) Row16<T>::store(dx + (int64_t)h * p.dim + sl.a, dx + (int64_t)h * p.dim + sl.b, d);
-      });
     }
-    if (sd.dw) write_partial(acc, sl, g, ls, lane_ok, red, part_ws + ((int64_t)blockIdx.x * 2 + side) * p.dim, p.dim);
+    if (sd.dw)
+      write_partial<LAYOUT>(acc, sl, g, lane_ok, red, part_ws + ((int64_t)blockIdx.x * 2 + side) * p.dim, p.dim);
   }
 }
 
@@ -455,8 +582,7 @@ bool fast_shape(const NormRopeArgs& a, size_t e, FastShape* g) {
   while (g->group < g->slots) g->group *= 2;
   // With fewer tokens than the GPU has warps to give, several warps share a token's heads.
   const int per = 32 / g->group;
-  const int hmax = a.side[0].heads > a.side[1].heads ? a.side[0].heads : a.side[1].heads;
-  const int steps = (hmax + per - 1) / per;
+  const int steps = (a.side[0].heads + per - 1) / per + (a.side[1].heads + per - 1) / per;
   const int64_t warps = (int64_t)num_sms() * kWarps * 2;
   int64_t parts = (warps + a.tokens - 1) / a.tokens;
   if (parts > steps) parts = steps;
@@ -476,7 +602,7 @@ template <typename T>
 cudaError_t fwd_t(const NormRopeArgs& a, cudaStream_t s) {
   FastShape g;
   if (fast_shape(a, sizeof(T), &g)) {
-    const int grid = grid_for(a.tokens * g.parts, 4, INT32_MAX);
+    const int grid = grid_for(a.tokens * g.parts, 3, INT32_MAX);
     if (a.layout == JFA_ROPE_HALVES)
       norm_rope_fwd_kernel<T, JFA_ROPE_HALVES><<<grid, kThreads, 0, s>>>(a, g);
     else
@@ -493,7 +619,7 @@ cudaError_t bwd_t(const NormRopeArgs& a, float* part, cudaStream_t s) {
   FastShape g;
   int grid;
   if (fast_shape(a, sizeof(T), &g)) {
-    grid = grid_for(a.tokens * g.parts, 4, kNormRopeParts);
+    grid = grid_for(a.tokens * g.parts, 2, kNormRopeParts);
     const size_t smem = sizeof(float) * kWarps * a.dim;
     if (a.layout == JFA_ROPE_HALVES)
       norm_rope_bwd_kernel<T, JFA_ROPE_HALVES><<<grid, kThreads, smem, s>>>(a, g, part);
