@@ -6,18 +6,23 @@
 // and B of the same key head, rows = consecutive tokens by the group's heads, so a key block
 // loaded once serves 256 rows.  A and B are two streams of steps, one per block of 128 keys:
 //   S = Q K^T -> softmax -> P -> O += P V,
-// and the issuer interleaves them (PV_A, S_A', PV_B, S_B'), so that the softmax of one stream
-// runs under the products of the other.  Where B has no rows (a chunk of at most 128 rows, the
+// so that the softmax of one stream runs under the products of the other.  Where B has no rows (a chunk of at most 128 rows, the
 // last tile of an odd number) the streams share A's queries and take the key blocks in turn,
 // and A joins both outputs: two loads and two softmaxes in flight instead of one.
 // Warps (a softmax thread owns a row: no exchange of row statistics):
 //   0-3, 4-7  softmax of A and B, and their epilogues
-//   8         issues every MMA (in one order, which the reuse of TMEM below relies on)
+//   8, 10     issue the MMAs of A and of B.  An issue holds its thread for most of the MMA's own
+//             time, so one issuer for both left the tensor pipe idle at every wait and commit
+//             (3,990 cycles for a block of both streams, of which the MMAs take 2,048).
 //   9         loads Q, K and V by TMA; looks up 32 page table entries at a time
-//   12-15     MXFP8 only: turn codes and scales into bf16 tiles (exact)
+//   11        zeroes the rows of a V tile that lie behind the sequence's end
+//   12-19     MXFP8 only: turn codes and scales into bf16 tiles (exact)
+// Tiles of K and V go round one ring (K0, V0, K1, ...).  Both issuers pass every stage in order
+// and free it once, whether they use it or not: an mbarrier's phase is known by its parity
+// alone, so a role that left phases out could take an older one for its own.
 // TMEM: S_A, S_B at columns 0, 128; O_A, O_B at 256, 384.  P (bf16) replaces the first half of
-// its S.  S of a stream's next step is issued behind PV of this one, so by its commit PV has
-// completed: O may then be rescaled without a further wait.
+// its S.  S of a stream's next step is issued behind PV of this one by the same thread, so by
+// its commit PV has completed: O may then be rescaled without a further wait.
 // The row maximum is kept lazily: O and the sum are rescaled only when it grows by more
 // than 2^8.
 #include <cuda.h>
@@ -38,12 +43,13 @@ constexpr int kKeys = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kIssuer = 8, kLoader = 9;
+constexpr int kIssuerA = 8, kLoader = 9, kIssuerB = 10, kCleaner = 11;
 
 template <int DQK, int DV, int KIND>
 struct Layout {
   static constexpr bool MX = KIND == kCacheMx;
-  static constexpr int kThreads = MX ? 512 : 384;
+  static constexpr int kThreads = MX ? 640 : 384;
+  static constexpr int kConverters = 8;  // warps (MXFP8)
   static constexpr uint32_t Q_BYTES = DQK / 64 * 16384, K_BYTES = DQK / 64 * 16384, V_BYTES = DV / 64 * 16384;
   static constexpr uint32_t STAGE = K_BYTES > V_BYTES ? K_BYTES : V_BYTES;  // bf16 tile, K or V
   // MXFP8: tiles of codes and their scales as loaded
@@ -61,7 +67,7 @@ struct Layout {
 };
 enum : uint32_t {
   B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PFULL = 6, B_OFULL = 8, B_OEMPTY = 10, B_XCH = 12, B_DRAIN = 13,
-  B_FULL = 14, B_EMPTY = 22, B_RFULL = 30, B_REMPTY = 34, B_COUNT = 38
+  B_FULL = 15, B_EMPTY = 23, B_RFULL = 31, B_REMPTY = 35, B_VTAIL = 39, B_COUNT = 47
 };
 static_assert(8 * B_COUNT + 8 <= 1024, "front");
 constexpr uint32_t T_S = 0, T_O = 256;
@@ -100,7 +106,6 @@ struct Streams {
   __device__ __forceinline__ int n(int x) const { return x ? n1 : n0; }
   // block of stream x's step i
   __device__ __forceinline__ int block(int x, int i) const { return split ? 2 * i + x : i; }
-  __device__ __forceinline__ bool both(int d) const { return !split && d < n0; }  // both streams use the block
 };
 __device__ __forceinline__ Streams streams_of(const Paged& p, const TileShape& t, const PagedSegment& g) {
   Streams s;
@@ -141,26 +146,27 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar(B_QFULL + x), 1);
-      mbar_init(bar(B_QEMPTY + x), 1);
+      mbar_init(bar(B_QEMPTY + x), x ? 1 : 2);  // A's queries: both issuers, B's: B's
       mbar_init(bar(B_SFULL + x), 1);
-      mbar_init(bar(B_PFULL + x), 128);
+      mbar_init(bar(B_PFULL + x), 4);  // a warp arrives once
       mbar_init(bar(B_OFULL + x), 1);
-      mbar_init(bar(B_OEMPTY + x), 128);
+      mbar_init(bar(B_OEMPTY + x), 4);
+      mbar_init(bar(B_DRAIN + x), 1);
     }
-    mbar_init(bar(B_XCH), 128);
-    mbar_init(bar(B_DRAIN), 1);
+    mbar_init(bar(B_XCH), 4);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(bar(B_FULL + s), MX ? 4 : 1);  // MXFP8: the four converting warps
-      mbar_init(bar(B_EMPTY + s), 2);          // a commit of each stream (or two of one)
+      mbar_init(bar(B_FULL + s), MX ? L::kConverters : 1);
+      mbar_init(bar(B_EMPTY + s), 2);  // both issuers
+      mbar_init(bar(B_VTAIL + s), 1);
     }
     for (int s = 0; s < NR; ++s) {
       mbar_init(bar(B_RFULL + s), 1);
-      mbar_init(bar(B_REMPTY + s), 4);
+      mbar_init(bar(B_REMPTY + s), L::kConverters);
     }
     *abort = 0;
     fence_mbar_init();
   }
-  if (warp == kIssuer) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == kIssuerA) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -168,8 +174,8 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
   const int rows1 = t.rows / 2;  // rows of an MMA tile
 
   // The softmax warpgroups take registers that the others do not need: (2 x 208 + 88) x 128 of
-  // the launch's 384 x 168, with MXFP8 (2 x 176 + 80 + 72) x 128 of its 512 x 128.
-  if (warp >= 8 && warp < 12) few_registers<MX ? 80 : 88>();
+  // the launch's 384 x 168, with MXFP8 (2 x 168 + 64 + 2 x 40) x 128 of its 640 x 96.
+  if (warp >= 8 && warp < 12) few_registers<MX ? 64 : 88>();
   if (warp == kLoader) {
     // ---------------------------------------------------------------- loads
     PagedWalk walk;
@@ -226,7 +232,9 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
             const int D = kv ? DV : DQK;
             const CUtensorMap* tm = kv ? &tm_v : &tm_k;
             const uint32_t dst = MX ? sb + L::RAW0 + st * L::RAW : sb + L::ST0 + st * L::STAGE;
-            if (lane == 0) mbar_expect_tx(full, MX ? kKeys * D + kKeys * D / 32 : kKeys * D * 2);
+            // the last block's values land on a barrier of their own and become full once cleaned
+            const uint32_t lands = !MX && kv == 1 && g.seq.lk < (i0 + i + 1) * kKeys ? bar(B_VTAIL + st) : full;
+            if (lane == 0) mbar_expect_tx(lands, MX ? kKeys * D + kKeys * D / 32 : kKeys * D * 2);
             for (int s2 = 0; s2 < per; ++s2) {
               const int r = __shfl_sync(0xffffffffu, row, i * per + s2);
               if (lane == 0) {
@@ -237,7 +245,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
                             box * (D / 32), full);
                 } else {
                   for (int a = 0; a < D / 64; ++a)
-                    tma_load_2d(dst + a * 16384 + s2 * box * 128, tm, a * 64, r, full);
+                    tma_load_2d(dst + a * 16384 + s2 * box * 128, tm, a * 64, r, lands);
                 }
               }
             }
@@ -251,90 +259,109 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
       drain_ring(bar(B_QFULL + 1), 1, q_it[1], status);
     }
     __syncwarp();
-  } else if (warp == kIssuer) {
-    // ---------------------------------------------------------------- products
+  } else if (warp == kIssuerA || warp == kIssuerB) {
+    // ---------------------------------------------------------------- products of one stream
     PagedWalk walk;
     walk.init(w.pos, blockIdx.x);
     PagedSegment g;
     constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, 0, 0), idesc_o = idesc_bf16(128, DV, 0, 1);
-    uint32_t base = 0;                                      // ring index of the segment's first load
-    uint32_t q0 = 0, q1 = 0, p0 = 0, p1 = 0, o0 = 0, o1 = 0;  // phases: queries, weights, outputs of A and B
+    const int x = warp == kIssuerB;
+    const uint32_t t_s = tmem + T_S + x * 128, t_o = tmem + T_O + x * 128;
+    uint32_t it = 0, qa_it = 0, qb_it = 0, p_it = 0, o_it = 0;
     bool ok = true;
     while (ok && walk.next(p, t, g)) {
       const Streams s = streams_of(p, t, g);
       if (s.blocks == 0) continue;
-      auto scores = [&](int x, int i) -> bool {  // S of stream x's step i
-        const int d = s.block(x, i), qx = s.split ? 0 : x;
-        const uint32_t idx = base + 2 * d, st = idx % NS;
-        if ((i == 0 && !mbar_wait(bar(B_QFULL + qx), (qx ? q1 : q0) & 1, abort, status)) ||
-            !mbar_wait(bar(B_FULL + st), (idx / NS) & 1, abort, status))
-          return false;
-        __syncwarp();
-        tc_fence_after();
-        const uint32_t q_tile = sb + L::TILE0 + qx * L::Q_BYTES, k_tile = sb + L::ST0 + st * L::STAGE;
-#pragma unroll
-        for (int kk = 0; kk < DQK / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-          mma_bf16(tmem + T_S + x * 128, sw128_desc(q_tile + off, 16, 1024), sw128_desc(k_tile + off, 16, 1024),
-                   idesc_s, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(bar(B_SFULL + x));
-        mma_commit(bar(B_EMPTY + st));
-        if (!s.both(d)) mma_commit(bar(B_EMPTY + st));
-        // the queries' last use: in a split tile, the last step of either stream
-        if (s.split ? d == s.blocks - 1 : i == s.n(x) - 1) mma_commit(bar(B_QEMPTY + qx));
-        return true;
-      };
-      auto output = [&](int x, int i) -> bool {  // O += P V of stream x's step i
-        const int d = s.block(x, i);
-        const uint32_t idx = base + 2 * d + 1, st = idx % NS;
-        if (!mbar_wait(bar(B_PFULL + x), (x ? p1 : p0) & 1, abort, status) ||
-            !mbar_wait(bar(B_FULL + st), (idx / NS) & 1, abort, status) ||
-            (i == 0 && !mbar_wait(bar(B_OEMPTY + x), ((x ? o1 : o0) & 1) ^ 1, abort, status)))
-          return false;
-        if (x) ++p1;
-        else ++p0;
-        const uint32_t v_tile = sb + L::ST0 + st * L::STAGE;
-        const int nk = g.seq.lk - (g.blk0 + d) * kKeys;
-        if (!MX && nk < kKeys && (x == 0 || !s.both(d))) {
-          // values behind the sequence's end may be anything: as zeros they meet zero weights
-          for (int c = lane; c < (kKeys - nk) * (DV / 8); c += 32) {
-            const int row = nk + c / (DV / 8), ch = c % (DV / 8);
-            st_shared_v4(v_tile + (ch >> 3) * 16384 + row * 128 + (ch & 7) * 16, 0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_bf16_tmem_a(tmem + T_O + x * 128, tmem + T_S + x * 128 + kk * 8,
-                          sw128_desc(v_tile + kk * 2048, 16384, 1024), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(bar(B_EMPTY + st));
-        if (!s.both(d)) mma_commit(bar(B_EMPTY + st));
-        if (i == s.n(x) - 1) {
-          mma_commit(bar(B_OFULL + x));
-          if (x) ++o1;
-          else ++o0;
-        }
-        return true;
-      };
-      if (s.n0 > 0) ok = scores(0, 0);
-      if (ok && s.n1 > 0) ok = scores(1, 0);
-      for (int i = 0; ok && (i < s.n0 || i < s.n1); ++i) {
-        if (i < s.n0) ok = output(0, i) && (i + 1 >= s.n0 || scores(0, i + 1));
-        if (ok && i < s.n1) ok = output(1, i) && (i + 1 >= s.n1 || scores(1, i + 1));
+      const int n = s.n(x);
+      // B may work on A's queries: it passes every phase of both tiles, and frees A's at once where
+      // it does not use them
+      if (s.n0 > 0) {
+        if (!(ok = mbar_wait(bar(B_QFULL), qa_it++ & 1, abort, status))) break;
+        if (x == 1 && (!s.split || n == 0) && lane == 0) mbar_arrive(bar(B_QEMPTY));
       }
-      base += 2 * s.blocks;
-      q0 += s.n0 > 0;
-      q1 += !s.split && s.n1 > 0;
+      if (x == 1 && !s.split && !(ok = mbar_wait(bar(B_QFULL + 1), qb_it++ & 1, abort, status))) break;
+      const uint32_t qx = s.split ? 0 : x, q_tile = sb + L::TILE0 + qx * L::Q_BYTES;
+      int i = 0;  // steps of the stream
+      for (int d = 0; ok && d < s.blocks; ++d) {
+        const bool mine = s.split ? (d & 1) == x : d < n;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++it) {
+          const uint32_t st = it % NS, tile = sb + L::ST0 + st * L::STAGE;
+          if (mine && kv == 1 &&
+              (!mbar_wait(bar(B_PFULL + x), p_it & 1, abort, status) ||
+               (i == 0 && !mbar_wait(bar(B_OEMPTY + x), (o_it & 1) ^ 1, abort, status)))) {
+            ok = false;
+            break;
+          }
+          if (!mbar_wait(bar(B_FULL + st), (it / NS) & 1, abort, status)) {
+            ok = false;
+            break;
+          }
+          __syncwarp();  // converged for elect.sync
+          if (!mine) {
+            if (lane == 0) mbar_arrive(bar(B_EMPTY + st));
+            continue;
+          }
+          tc_fence_after();
+          if (kv == 0) {
+#pragma unroll
+            for (int kk = 0; kk < DQK / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+              mma_bf16(t_s, sw128_desc(q_tile + off, 16, 1024), sw128_desc(tile + off, 16, 1024), idesc_s,
+                       kk > 0 ? 1u : 0u);
+            }
+            mma_commit(bar(B_SFULL + x));
+            mma_commit(bar(B_EMPTY + st));
+            if (i == n - 1) mma_commit(bar(B_QEMPTY + qx));  // the queries' last use here
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_bf16_tmem_a(t_o, t_s + kk * 8, sw128_desc(tile + kk * 2048, 16384, 1024), idesc_o,
+                              (i > 0 || kk > 0) ? 1u : 0u);
+            if (i == n - 1) {
+              mma_commit(bar(B_OFULL + x));
+              ++o_it;
+            }
+            mma_commit(bar(B_EMPTY + st));
+            ++p_it;
+            ++i;
+          }
+        }
+      }
     }
     __syncwarp();
-    mma_drain(bar(B_DRAIN), status);  // every MMA issued has completed
+    mma_drain(bar(B_DRAIN + x), status);  // every MMA issued has completed
     __syncwarp();
+  } else if (warp == kCleaner) {
+    // ---------------------------------------------------------------- ends of sequences
+    if constexpr (!MX) {
+      PagedWalk walk;
+      walk.init(w.pos, blockIdx.x);
+      PagedSegment g;
+      uint32_t it = 0, phase = 0;  // phase: a bit a stage
+      bool ok = true;
+      while (ok && walk.next(p, t, g)) {
+        const int nk = g.seq.lk - (g.blk1 - 1) * kKeys;  // keys of the segment's last block
+        if (g.blk1 > g.blk0 && nk < kKeys) {
+          // values behind the sequence's end may be anything: as zeros they meet zero weights
+          const uint32_t st = (it + 2 * (g.blk1 - g.blk0) - 1) % NS, tile = sb + L::ST0 + st * L::STAGE;
+          ok = mbar_wait(bar(B_VTAIL + st), (phase >> st) & 1, abort, status);
+          if (!ok) break;
+          phase ^= 1u << st;
+          for (int c = lane; c < (kKeys - nk) * (DV / 8); c += 32) {
+            const int row = nk + c / (DV / 8), ch = c % (DV / 8);
+            st_shared_v4(tile + (ch >> 3) * 16384 + row * 128 + (ch & 7) * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_FULL + st));
+        }
+        it += 2 * (g.blk1 - g.blk0);
+      }
+    }
   } else if (warp < 8) {
     // ---------------------------------------------------------------- softmax and epilogue
-    more_registers<MX ? 176 : 208>();
+    more_registers<MX ? 168 : 208>();
     PagedWalk walk;
     walk.init(w.pos, blockIdx.x);
     PagedSegment g;
@@ -418,7 +445,8 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
         l += rr.x + rr.y;
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(B_PFULL + x));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_PFULL + x));
       }
       if (!ok) break;
       // ------------------------------------------------------------ the tile's end
@@ -430,7 +458,8 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
           // only now: B's first product has waited for A to have read the last tile's
           xch[r] = make_float2(m, l);
           tc_fence_before();
-          mbar_arrive(bar(B_XCH));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_XCH));
         }
         continue;
       }
@@ -476,8 +505,11 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
           }
         }
         tc_fence_before();
-        mbar_arrive(bar(B_OEMPTY + x));
-        if (joins) mbar_arrive(bar(B_OEMPTY + 1));
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(B_OEMPTY + x));
+          if (joins) mbar_arrive(bar(B_OEMPTY + 1));
+        }
       } else if (whole && row_ok) {
         const float z[32] = {0.f};
         for (int c = 0; c < DV / 32; ++c) store32_bf16((__nv_bfloat16*)p.o + orow * DV + 32 * c, z, 1.f);
@@ -492,21 +524,20 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
     }
   } else if (MX && warp >= 12) {
     // ---------------------------------------------------------------- MXFP8 to bf16 tiles
-    few_registers<72>();
+    few_registers<40>();
     if constexpr (MX) {
       PagedWalk walk;
       walk.init(w.pos, blockIdx.x);
       PagedSegment g;
-      const int row = threadIdx.x - 384;  // key of the block
+      const int row = threadIdx.x & 127, part = (threadIdx.x - 384) >> 7;  // key of the block, half of its columns
       uint32_t it = 0;
       bool ok = true;
       while (ok && walk.next(p, t, g)) {
         for (int blk = g.blk0; ok && blk < g.blk1; ++blk) {
           const bool live = blk * kKeys + row < g.seq.lk;  // rows behind the end become zeros
-#pragma unroll
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++it) {
-            constexpr int RB_K = DQK, RB_V = DV;  // bytes of a row of codes
-            const int D = kv ? RB_V : RB_K;
+            const int D = kv ? DV : DQK;
             const uint32_t rs = it % NR, st = it % NS;
             if (!mbar_wait(bar(B_RFULL + rs), (it / NR) & 1, abort, status) ||
                 !mbar_wait(bar(B_EMPTY + st), ((it / NS) & 1) ^ 1, abort, status)) {
@@ -515,8 +546,9 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
             }
             const uint32_t src = sb + L::RAW0 + rs * L::RAW, sc = sb + L::SC0 + rs * L::RAW_SC + row * (D / 32);
             const uint32_t dst = sb + L::ST0 + st * L::STAGE;
-#pragma unroll
-            for (int c = 0; c < (kv ? DV : DQK) / 16; ++c) {
+            const int c0 = part * (D / 32), c1 = c0 + D / 32;  // 16-byte chunks of codes
+#pragma unroll 2
+            for (int c = c0; c < c1; ++c) {
               const uint32_t at = D == 128 ? src + row * 128 + ((c ^ (row & 7)) << 4)
                                            : src + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
               const uint4 v = ld_shared_v4(at);
@@ -548,7 +580,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kIssuer) {
+  if (warp == kIssuerA) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -5,9 +5,9 @@ producer fills stages in order, each load lands at any later time, and the fills
 four consumers, each of which reads and frees its own.  Every interleaving has to finish, and
 every consumer has to find its own fill in the stage when its wait is over.
 
-The 128-row kernel (`csrc/paged_tc.cu`): loader, MXFP8 converters, MMA issuer and two softmax
-warpgroups, with loads that land in any order and MMAs and commits that complete in issue order
-at any later time.  Every interleaving has to finish, and every role has to find in the shared
+The 128-row kernel (`csrc/paged_tc.cu`): loader, the cleaner of the last block's values or MXFP8
+converters, an MMA issuer and a softmax warpgroup for each stream, with loads that land in any
+order and MMAs and commits that complete in their thread's order at any later time.  Every interleaving has to finish, and every role has to find in the shared
 and tensor memory that it reads what its step needs."""
 import random
 
@@ -97,28 +97,29 @@ class Segment:
     """`blocks` key blocks; `split`: the streams share A's queries and take the blocks in turn,
     else A takes the first `n0` and B all."""
 
-    def __init__(self, blocks, split, n0=0):
-        self.blocks, self.split = blocks, split
+    def __init__(self, blocks, split, n0=0, tail=False):
+        self.blocks, self.split, self.tail = blocks, split, tail
         self.n = [(blocks + 1) // 2, blocks // 2] if split else [min(n0, blocks), blocks]
 
     def block(self, x, i):
         return 2 * i + x if self.split else i
 
-    def both(self, d):
-        return not self.split and d < self.n[0]
 
-
-def play_tc(segments, stages, raws, seed, xch_early=False, limit=100000):
-    """raws: stages of unconverted tiles (MXFP8), 0: tiles are loaded as they are used."""
+def play_tc(segments, stages, raws, seed, xch_early=False, pass_all=True, pass_queries=True,
+            limit=100000):
+    """raws: stages of unconverted tiles (MXFP8), 0: tiles are loaded as they are used.
+    pass_all=False: an issuer leaves out the stages that it does not use (and the user frees them
+    twice).  pass_queries=False: B waits for A's queries without freeing them."""
     rng = random.Random(seed)
     B = lambda n, c=1: [Bar(c) for _ in range(n)]
-    qfull, qempty, sfull, pfull, ofull, oempty = (B(2) for _ in range(6))
+    qfull, sfull, pfull, ofull, oempty = (B(2) for _ in range(5))
+    qempty = [Bar(2 if pass_queries else 1), Bar(1)]
     xch_bar = Bar(1)
-    full, empty = B(stages), B(stages, 2)
+    full, empty, vtail = B(stages), B(stages, 2), B(stages)
     rfull, rempty = B(max(raws, 1)), B(max(raws, 1))
     qmem, stage, raw = [None, None], [None] * stages, [None] * max(raws, 1)
     S, O = [None, None], [[], []]  # tensor memory: ("s" or "p", step) and the steps in O
-    xch, flying, pipe, outputs = [None], [], [], []
+    xch, flying, pipes = [None], [], [[], []]
     segs = [(n, g) for n, g in enumerate(segments) if g.blocks]
 
     def need(ok, what):
@@ -148,8 +149,22 @@ def play_tc(segments, stages, raws, seed, xch_early=False, limit=100000):
                     f, e, mem, ring = (rfull, rempty, raw, raws) if raws else (full, empty, stage, stages)
                     st = it % ring
                     yield lambda: e[st].done(((it // ring) & 1) ^ 1)
-                    fly(land(f[st], mem, st, (n, d, kv)))
+                    tail = not raws and g.tail and kv and d == g.blocks - 1
+                    fly(land((vtail if tail else f)[st], mem, st, (n, d, kv, "dirty") if tail else (n, d, kv)))
                     it += 1
+
+    def cleaner():
+        it, phase = 0, [0] * stages
+        for n, g in segs:
+            it += 2 * g.blocks
+            if g.tail:
+                st = (it - 1) % stages
+                yield lambda: vtail[st].done(phase[st])
+                phase[st] ^= 1
+                need(stage[st] == (n, g.blocks - 1, 1, "dirty"), "cleans another tile")
+                yield lambda: True
+                stage[st] = (n, g.blocks - 1, 1)
+                full[st].arrive()
 
     def converter():
         it = 0
@@ -165,68 +180,65 @@ def play_tc(segments, stages, raws, seed, xch_early=False, limit=100000):
                     rempty[rs].arrive()
                     it += 1
 
-    def issuer():
-        base, q, p, o = 0, [0, 0], [0, 0], [0, 0]
-        commit = lambda bar: pipe.append(bar.arrive)
-
-        def scores(n, g, x, i):
-            d, qx = g.block(x, i), 0 if g.split else x
-            idx = base + 2 * d
-            st = idx % stages
-            if i == 0:
-                yield lambda: qfull[qx].done(q[qx] & 1)
-            yield lambda: full[st].done((idx // stages) & 1)
-
-            def run():
-                need(qmem[qx] == n and stage[st] == (n, d, 0), "S of other tiles")
-                need(S[x] is None or S[x][0] == "used", "S over weights in use")
-                S[x] = ("s", n, i)
-            pipe.append(run)
-            commit(sfull[x])
-            commit(empty[st])
-            if not g.both(d):
-                commit(empty[st])
-            if (d == g.blocks - 1) if g.split else (i == g.n[x] - 1):
-                commit(qempty[qx])
-
-        def output(n, g, x, i):
-            d = g.block(x, i)
-            idx = base + 2 * d + 1
-            st = idx % stages
-            yield lambda: pfull[x].done(p[x] & 1)
-            yield lambda: full[st].done((idx // stages) & 1)
-            if i == 0:
-                yield lambda: oempty[x].done((o[x] & 1) ^ 1)
-            p[x] += 1
-
-            def run():
-                need(S[x] == ("p", n, i) and stage[st] == (n, d, 1), "P V of other tiles")
-                if i == 0:
-                    need(O[x] in ([], ["read"]), "O over an output that was not read")
-                    O[x] = []
-                O[x].append((n, d))
-                S[x] = ("used", n, i)
-            pipe.append(run)
-            commit(empty[st])
-            if not g.both(d):
-                commit(empty[st])
-            if i == g.n[x] - 1:
-                commit(ofull[x])
-                o[x] += 1
-
+    def issuer(x):
+        it = p = o = qa = qb = 0
+        commit = lambda bar: pipes[x].append(bar.arrive)
         for n, g in segs:
-            for x in (0, 1):
-                if g.n[x]:
-                    yield from scores(n, g, x, 0)
-            for i in range(max(g.n)):
-                for x in (0, 1):
-                    if i < g.n[x]:
-                        yield from output(n, g, x, i)
-                        if i + 1 < g.n[x]:
-                            yield from scores(n, g, x, i + 1)
-            base += 2 * g.blocks
-            q[0] += g.n[0] > 0
-            q[1] += not g.split and g.n[1] > 0
+            if g.n[0]:
+                yield lambda: qfull[0].done(qa & 1)
+                qa += 1
+                if x and (not g.split or g.n[1] == 0) and pass_queries:
+                    qempty[0].arrive()
+            if x and not g.split:
+                yield lambda: qfull[1].done(qb & 1)
+                qb += 1
+            qx, i = 0 if g.split else x, 0
+            for d in range(g.blocks):
+                mine = (d & 1) == x if g.split else d < g.n[x]
+                for kv in (0, 1):
+                    st, par = it % stages, (it // stages) & 1
+                    it += 1
+                    if not mine and not pass_all:
+                        continue
+                    if mine and kv:
+                        yield lambda: pfull[x].done(p & 1)
+                        if i == 0:
+                            yield lambda: oempty[x].done((o & 1) ^ 1)
+                    yield lambda: full[st].done(par)
+                    if not mine:
+                        empty[st].arrive()
+                        continue
+                    twice = not pass_all and (g.split or d >= g.n[0])
+                    if kv == 0:
+                        def run(i=i, st=st, d=d, n=n, qx=qx):
+                            need(qmem[qx] == n and stage[st] == (n, d, 0), "S of other tiles")
+                            need(S[x] is None or S[x][0] == "used", "S over weights in use")
+                            S[x] = ("s", n, i)
+                        pipes[x].append(run)
+                        commit(sfull[x])
+                        commit(empty[st])
+                        if twice:
+                            commit(empty[st])
+                        if i == g.n[x] - 1:
+                            if pass_queries or x == 0 or not g.split:
+                                commit(qempty[qx])
+                    else:
+                        def run(i=i, st=st, d=d, n=n, qx=qx):
+                            need(S[x] == ("p", n, i) and stage[st] == (n, d, 1), "P V of other tiles")
+                            if i == 0:
+                                need(O[x] in ([], ["read"]), "O over an output that was not read")
+                                O[x] = []
+                            O[x].append((n, d))
+                            S[x] = ("used", n, i)
+                        pipes[x].append(run)
+                        if i == g.n[x] - 1:
+                            commit(ofull[x])
+                            o += 1
+                        commit(empty[st])
+                        if twice:
+                            commit(empty[st])
+                        p += 1
+                        i += 1
 
     def softmax(x):
         s_it = o_it = x_it = 0
@@ -270,9 +282,8 @@ def play_tc(segments, stages, raws, seed, xch_early=False, limit=100000):
                 O[1] = ["read"]
                 oempty[1].arrive()
 
-    roles = {"loader": loader(), "issuer": issuer(), "a": softmax(0), "b": softmax(1)}
-    if raws:
-        roles["converter"] = converter()
+    roles = {"loader": loader(), "issuer a": issuer(0), "issuer b": issuer(1), "a": softmax(0), "b": softmax(1)}
+    roles["converter" if raws else "cleaner"] = converter() if raws else cleaner()
     waits = {k: (lambda: True) for k in roles}
     stuck = 0
     try:
@@ -281,13 +292,13 @@ def play_tc(segments, stages, raws, seed, xch_early=False, limit=100000):
             if flying and z < 0.2:
                 flying.pop(rng.randrange(len(flying)))()
                 stuck = 0
-            elif pipe and z < 0.5:
-                pipe.pop(0)()
+            elif any(pipes) and z < 0.5:
+                rng.choice([q for q in pipes if q]).pop(0)()
                 stuck = 0
             k = rng.choice(sorted(roles))
             if not waits[k]():
                 stuck += 1
-                if stuck > limit and not flying and not pipe:
+                if stuck > limit and not flying and not any(pipes):
                     return "stuck: %s" % sorted(roles)
                 continue
             stuck = 0
@@ -305,14 +316,14 @@ def tc_segments(rng):
     for _ in range(rng.randint(1, 7)):
         blocks = rng.choice([0, 1, 1, 2, 3, 6, 11])
         split = rng.random() < 0.5
-        out.append(Segment(blocks, split, max(0, blocks - rng.choice([0, 0, 1, 2, 20]))))
+        out.append(Segment(blocks, split, max(0, blocks - rng.choice([0, 0, 1, 2, 20])), rng.random() < 0.4))
     return out
 
 
 @pytest.mark.parametrize("stages,raws", [(5, 0), (8, 0), (3, 3), (6, 3)])
 def test_streams_of_the_128_row_kernel(stages, raws):
     rng = random.Random(stages)
-    for seed in range(80):
+    for seed in range(150):
         assert play_tc(tc_segments(rng), stages, raws, seed) is None
 
 
@@ -320,3 +331,15 @@ def test_an_early_handover_of_statistics_is_caught():
     """B writes its statistics before its product has waited for A: A may read the next tile's."""
     segs = [Segment(2, True)] * 6
     assert any(play_tc(segs, 5, 0, seed, xch_early=True) for seed in range(300))
+
+
+def test_leaving_out_stages_is_caught():
+    """An issuer that does not pass every stage takes older phases for its own."""
+    segs = [Segment(24, True), Segment(24, True)]
+    assert any(play_tc(segs, 6, 0, seed, pass_all=False, limit=3000) for seed in range(200))
+
+
+def test_a_query_tile_that_one_issuer_does_not_free_is_caught():
+    """B sees the phases of A's queries only if the loader waits for it."""
+    rng = random.Random(2)
+    assert any(play_tc(tc_segments(rng), 5, 0, seed, pass_queries=False, limit=3000) for seed in range(200))
