@@ -67,7 +67,7 @@ struct Layout {
 };
 enum : uint32_t {
   B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PFULL = 6, B_OFULL = 8, B_OEMPTY = 10, B_XCH = 12, B_DRAIN = 13,
-  B_FULL = 15, B_EMPTY = 23, B_RFULL = 31, B_REMPTY = 35, B_VTAIL = 39, B_COUNT = 47
+  B_FULL = 15, B_EMPTY = 23, B_RFULL = 31, B_REMPTY = 35, B_VTAIL = 39, B_TURN = 47, B_COUNT = 49
 };
 static_assert(8 * B_COUNT + 8 <= 1024, "front");
 constexpr uint32_t T_S = 0, T_O = 256;
@@ -152,6 +152,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
       mbar_init(bar(B_OFULL + x), 1);
       mbar_init(bar(B_OEMPTY + x), 4);
       mbar_init(bar(B_DRAIN + x), 1);
+      mbar_init(bar(B_TURN + x), 1);
     }
     mbar_init(bar(B_XCH), 4);
     for (int s = 0; s < NS; ++s) {
@@ -267,7 +268,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
     constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, 0, 0), idesc_o = idesc_bf16(128, DV, 0, 1);
     const int x = warp == kIssuerB;
     const uint32_t t_s = tmem + T_S + x * 128, t_o = tmem + T_O + x * 128;
-    uint32_t it = 0, qa_it = 0, qb_it = 0, p_it = 0, o_it = 0;
+    uint32_t it = 0, qa_it = 0, qb_it = 0, p_it = 0, o_it = 0, turn = 0;
     bool ok = true;
     while (ok && walk.next(p, t, g)) {
       const Streams s = streams_of(p, t, g);
@@ -287,6 +288,13 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++it) {
           const uint32_t st = it % NS, tile = sb + L::ST0 + st * L::STAGE;
+          // The streams take turns, block by block: a turn is P V of a block and S of the next.
+          // Their MMAs then run one behind the other and each softmax under the other's products;
+          // left alone, streams that start together stay in step, and both pipes wait by turns.
+          if (kv == 1 && !mbar_wait(bar(B_TURN + x), (turn++ & 1) ^ (x == 0), abort, status)) {
+            ok = false;
+            break;
+          }
           if (mine && kv == 1 &&
               (!mbar_wait(bar(B_PFULL + x), p_it & 1, abort, status) ||
                (i == 0 && !mbar_wait(bar(B_OEMPTY + x), (o_it & 1) ^ 1, abort, status)))) {
@@ -298,8 +306,12 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
             break;
           }
           __syncwarp();  // converged for elect.sync
+          const bool passes = kv == 0 ? d > 0 : d == s.blocks - 1;  // the turn ends here
           if (!mine) {
-            if (lane == 0) mbar_arrive(bar(B_EMPTY + st));
+            if (lane == 0) {
+              mbar_arrive(bar(B_EMPTY + st));
+              if (passes) mbar_arrive(bar(B_TURN + (x ^ 1)));
+            }
             continue;
           }
           tc_fence_after();
@@ -310,6 +322,8 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
               mma_bf16(t_s, sw128_desc(q_tile + off, 16, 1024), sw128_desc(tile + off, 16, 1024), idesc_s,
                        kk > 0 ? 1u : 0u);
             }
+            if (passes && lane == 0) mbar_arrive(bar(B_TURN + (x ^ 1)));
+            __syncwarp();
             mma_commit(bar(B_SFULL + x));
             mma_commit(bar(B_EMPTY + st));
             if (i == n - 1) mma_commit(bar(B_QEMPTY + qx));  // the queries' last use here
@@ -318,6 +332,8 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
             for (int kk = 0; kk < kKeys / 16; ++kk)
               mma_bf16_tmem_a(t_o, t_s + kk * 8, sw128_desc(tile + kk * 2048, 16384, 1024), idesc_o,
                               (i > 0 || kk > 0) ? 1u : 0u);
+            if (passes && lane == 0) mbar_arrive(bar(B_TURN + (x ^ 1)));
+            __syncwarp();
             if (i == n - 1) {
               mma_commit(bar(B_OFULL + x));
               ++o_it;
@@ -398,13 +414,14 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
 #pragma unroll
           for (int k = 0; k < kKeys; ++k) sv[k] = k < seen ? sv[k] : -INFINITY;
         }
-        float m0 = fmaxf(sv[0], sv[1]), m1 = fmaxf(sv[2], sv[3]);
+        float mx[8];
 #pragma unroll
-        for (int k = 4; k < kKeys; k += 4) {
-          m0 = fmax3(m0, sv[k], sv[k + 1]);
-          m1 = fmax3(m1, sv[k + 2], sv[k + 3]);
-        }
-        const float mt = fmaxf(m0, m1) * c_score;
+        for (int k = 0; k < 8; ++k) mx[k] = fmaxf(sv[2 * k], sv[2 * k + 1]);
+#pragma unroll
+        for (int k = 16; k < kKeys; k += 16)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) mx[c] = fmax3(mx[c], sv[k + 2 * c], sv[k + 2 * c + 1]);
+        const float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * c_score;
         const bool need = mt > m + kRescaleLog2;  // m = -inf: any key
         if (__any_sync(0xffffffffu, need)) {
           float alpha = 1.f;

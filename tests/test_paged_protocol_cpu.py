@@ -105,7 +105,7 @@ class Segment:
         return 2 * i + x if self.split else i
 
 
-def play_tc(segments, stages, raws, seed, xch_early=False, pass_all=True, pass_queries=True,
+def play_tc(segments, stages, raws, seed, pass_all=True, pass_queries=True,
             limit=100000):
     """raws: stages of unconverted tiles (MXFP8), 0: tiles are loaded as they are used.
     pass_all=False: an issuer leaves out the stages that it does not use (and the user frees them
@@ -115,7 +115,7 @@ def play_tc(segments, stages, raws, seed, xch_early=False, pass_all=True, pass_q
     qfull, sfull, pfull, ofull, oempty = (B(2) for _ in range(5))
     qempty = [Bar(2 if pass_queries else 1), Bar(1)]
     xch_bar = Bar(1)
-    full, empty, vtail = B(stages), B(stages, 2), B(stages)
+    full, empty, vtail, turn = B(stages), B(stages, 2), B(stages), B(2)
     rfull, rempty = B(max(raws, 1)), B(max(raws, 1))
     qmem, stage, raw = [None, None], [None] * stages, [None] * max(raws, 1)
     S, O = [None, None], [[], []]  # tensor memory: ("s" or "p", step) and the steps in O
@@ -181,7 +181,7 @@ def play_tc(segments, stages, raws, seed, xch_early=False, pass_all=True, pass_q
                     it += 1
 
     def issuer(x):
-        it = p = o = qa = qb = 0
+        it = p = o = qa = qb = tn = 0
         commit = lambda bar: pipes[x].append(bar.arrive)
         for n, g in segs:
             if g.n[0]:
@@ -200,11 +200,17 @@ def play_tc(segments, stages, raws, seed, xch_early=False, pass_all=True, pass_q
                     it += 1
                     if not mine and not pass_all:
                         continue
+                    passes = pass_all and (d == g.blocks - 1 if kv else d > 0)
+                    if kv and pass_all:  # the streams take turns
+                        yield lambda: turn[x].done((tn & 1) ^ (x == 0))
+                        tn += 1
                     if mine and kv:
                         yield lambda: pfull[x].done(p & 1)
                         if i == 0:
                             yield lambda: oempty[x].done((o & 1) ^ 1)
                     yield lambda: full[st].done(par)
+                    if passes:
+                        pipes[x].append(turn[x ^ 1].arrive) if rng.random() < 0.5 else turn[x ^ 1].arrive()
                     if not mine:
                         empty[st].arrive()
                         continue
@@ -253,8 +259,6 @@ def play_tc(segments, stages, raws, seed, xch_early=False, pass_all=True, pass_q
                 pfull[x].arrive()
             if g.split and x:
                 if g.n[1]:
-                    if xch_early:
-                        xch[0] = n
                     yield lambda: ofull[1].done(o_it & 1)
                     o_it += 1
                     xch[0] = n
@@ -325,12 +329,6 @@ def test_streams_of_the_128_row_kernel(stages, raws):
     rng = random.Random(stages)
     for seed in range(150):
         assert play_tc(tc_segments(rng), stages, raws, seed) is None
-
-
-def test_an_early_handover_of_statistics_is_caught():
-    """B writes its statistics before its product has waited for A: A may read the next tile's."""
-    segs = [Segment(2, True)] * 6
-    assert any(play_tc(segs, 5, 0, seed, xch_early=True) for seed in range(300))
 
 
 def test_leaving_out_stages_is_caught():
