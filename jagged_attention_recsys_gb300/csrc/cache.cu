@@ -7,10 +7,12 @@
 // head's rows together, [page, head, position, column], so that the attention finds the
 // positions of a page and head in one stretch.
 //
-// Bound: HBM (bytes in plus bytes out; nothing to compute).  A warp takes a token, or part of
-// one where there are fewer tokens than warps; a lane takes eight columns, so a row of 128
-// is half a warp, loads are 16 (bf16) or 32 bytes a lane and consecutive over the token's
-// heads, and four lanes share a block's maximum by two shuffles.
+// Bound: HBM (bytes in plus bytes out; nothing to compute).  A warp takes a run of up to 32
+// consecutive tokens, or part of a token's heads where there are fewer tokens than warps: its
+// lanes first look up a token each (sequence, position, page: a chain of dependent loads that
+// would otherwise be paid token by token), then the warp goes through them.  A lane takes 16
+// columns (two lanes share a block's maximum by one shuffle), consecutive over the token's heads,
+// with up to two pieces of the keys and two of the values in flight.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -23,32 +25,53 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-__device__ __forceinline__ void load8(float (&v)[8], const __nv_bfloat16* x) {
-  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(x));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// W columns of a row as they lie in memory
+template <typename T, int W>
+struct Raw {
+  static constexpr int N = W * sizeof(T) / 16;
+  uint4 q[N];
+  __device__ __forceinline__ void load(const T* x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < N; ++i) q[i] = __ldcs(reinterpret_cast<const uint4*>(x) + i);
   }
-}
-__device__ __forceinline__ void load8(float (&v)[8], const float* x) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(x)), b = __ldcs(reinterpret_cast<const float4*>(x) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* y, const float (&v)[8]) {
-  uint32_t w[4];
+  __device__ __forceinline__ void store(T* y) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {  // the result's type: one rounding
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+    for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(y)[i] = q[i];
   }
-  *reinterpret_cast<uint4*>(y) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void store8(float* y, const float (&v)[8]) {
-  reinterpret_cast<float4*>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
+  __device__ __forceinline__ void get(float (&v)[W]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 2) {
+          v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+          v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        } else {
+          v[4 * i + j] = __uint_as_float(w[j]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[W]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 2)  // the result's type: one rounding
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[8 * i + 2 * j + 1]), "f"(v[8 * i + 2 * j]));
+        else
+          w[j] = __float_as_uint(v[4 * i + j]);
+      }
+      q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+};
 
 // The sequence of new token t: the guess serves batches of equal lengths (one token each in
 // a serving step) with one look, otherwise a binary search.  Any contents of offs end it,
@@ -77,81 +100,48 @@ __device__ __forceinline__ int token_position(const Paged& p, int64_t t, int b, 
   return pos < 0 ? -1 : (int)pos;
 }
 
-// Eight columns of a row into the cache.  All lanes call it; `ok` says which have a row.
-template <typename T, int KIND>
-__device__ __forceinline__ void write8(const Paged& p, void* codes, uint8_t* scales, int64_t row, int chunk, int dim,
-                                       const float (&v)[8], bool ok) {
-  if constexpr (KIND == kCacheMx) {
-    float a = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));  // a NaN is passed over, and stays one in its code
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    const int e = mx_scale_exp(a);
-    const float f = exp2i(-e);
-    if (ok) {
-      uint2 c;
-      c.x = e4m3_pair(v[0] * f, v[1] * f) | e4m3_pair(v[2] * f, v[3] * f) << 16;
-      c.y = e4m3_pair(v[4] * f, v[5] * f) | e4m3_pair(v[6] * f, v[7] * f) << 16;
-      *reinterpret_cast<uint2*>((uint8_t*)codes + row * dim + chunk * 8) = c;
-      if ((chunk & 3) == 0) scales[row * (dim >> 5) + (chunk >> 2)] = (uint8_t)(e + 127);
+// Pieces of W columns of one token's tensor: a lane's next piece is 32 further on.
+template <int W>
+struct Piece {
+  int c, head, col;  // index, head, piece of the head
+  __device__ __forceinline__ Piece(int c0, int per) : c(c0), head(c0 / per), col(c0 - c0 / per * per) {}
+  __device__ __forceinline__ void next(int per, int dh, int dc) {  // dh, dc: 32 / per and 32 % per
+    c += 32;
+    head += dh;
+    col += dc;
+    if (col >= per) {
+      col -= per;
+      ++head;
     }
-  } else {
-    if (ok) store8((T*)codes + row * dim + chunk * 8, v);
   }
-}
-template <typename T, int KIND>
-__device__ __forceinline__ void read8(float (&v)[8], const void* codes, const uint8_t* scales, int64_t row, int chunk,
-                                      int dim) {
-  if constexpr (KIND == kCacheMx) {
-    const uint2 c = __ldcs(reinterpret_cast<const uint2*>((const uint8_t*)codes + row * dim + chunk * 8));
-    const float f = __uint_as_float((uint32_t)__ldg(scales + row * (dim >> 5) + (chunk >> 2)) << 23);
-    const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = e4m3_values((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
-      v[2 * i] = x.x * f;
-      v[2 * i + 1] = x.y * f;
-    }
-  } else {
-    load8(v, (const T*)codes + row * dim + chunk * 8);
-  }
-}
+};
 
-// One tensor of a token: chunks [c0, c1) of its heads * dim / 8.
-template <typename T, int KIND, bool WRITE>
-__device__ __forceinline__ void token_rows(const Paged& p, int64_t t, int pos, int page, int c0, int c1, int dim,
-                                           const T* in, int64_t stride, T* out, void* codes, uint8_t* scales) {
-  const int lane = threadIdx.x & 31, per = dim / 8;
-  constexpr int U = 4;  // chunks a lane has in flight
-  for (int base = c0; base < c1; base += 32 * U) {
-    float v[U][8];
+// 16 columns as MXFP8.  All lanes call it (a block is two lanes'); `ok` says which have a row.
+template <typename T>
+__device__ __forceinline__ void write_mx(const Raw<T, 16>& raw, uint8_t* codes, uint8_t* scale, int col, bool ok) {
+  float v[16], a = 0.f;
+  raw.get(v);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = base + 32 * u + lane;
+  for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(v[i]));  // a NaN is passed over, and stays one in its code
+  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  const int e = mx_scale_exp(a);
+  const float f = exp2i(-e);
+  uint32_t c[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-      if (c < c1) {
-        if (WRITE) load8(v[u], in + t * stride + (int64_t)c * 8);
-        else if (page >= 0) read8<T, KIND>(v[u], codes, scales, paged_row(p, page, c / per, pos), c % per, dim);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = base + 32 * u + lane;
-      if (WRITE) {
-        const int h = c / per;
-        write8<T, KIND>(p, codes, scales, paged_row(p, page, h, pos), c - h * per, dim, v[u], c < c1);
-      } else if (c < c1) {
-        store8(out + (t * p.heads_k * (int64_t)dim + (int64_t)c * 8), v[u]);
-      }
-    }
+  for (int i = 0; i < 4; ++i)
+    c[i] = e4m3_pair(v[4 * i] * f, v[4 * i + 1] * f) | e4m3_pair(v[4 * i + 2] * f, v[4 * i + 3] * f) << 16;
+  if (ok) {
+    *reinterpret_cast<uint4*>(codes) = make_uint4(c[0], c[1], c[2], c[3]);
+    if ((col & 1) == 0) *scale = (uint8_t)(e + 127);
   }
 }
 
 template <typename T, int KIND, bool WRITE>
-__global__ void __launch_bounds__(kThreads)
-cache_kernel(const __grid_constant__ Paged p, T* k_out, T* v_out, PagedHeader* hdr, int parts, int planned) {
+__global__ void __launch_bounds__(kThreads, 3)
+cache_kernel(const __grid_constant__ Paged p, T* k_out, T* v_out, PagedHeader* hdr, int run, int parts, int planned) {
+  constexpr bool MX = KIND == kCacheMx;
+  constexpr int W = MX ? 16 : 8;
+  constexpr int U = W * sizeof(T) > 32 ? 1 : 2;  // pieces of each tensor in flight
   // a plan that found the batch invalid: nothing is computed (page errors do not stop the call,
   // so the check does not depend on what other CTAs have met so far)
   if (planned && *(volatile int*)&hdr->status == (int)JFA_ERR_BAD_OFFSETS) return;
@@ -163,35 +153,122 @@ cache_kernel(const __grid_constant__ Paged p, T* k_out, T* v_out, PagedHeader* h
         atomicExch(&hdr->status, (int)JFA_ERR_BAD_OFFSETS);
     }
   }
-  const int64_t tasks = p.total_q * parts, nw = (int64_t)gridDim.x * kWarps;
-  const int ck = p.heads_k * (p.dim_qk / 8), cv = p.heads_k * (p.dim_v / 8);
+  const int lane = threadIdx.x & 31;
+  const int perk = p.dim_qk / W, perv = p.dim_v / W;  // pieces of a head
+  const int ck = p.heads_k * perk, cv = p.heads_k * perv;
+  const int dhk = 32 / perk, dck = 32 - dhk * perk, dhv = 32 / perv, dcv = 32 - dhv * perv;
+  const int64_t runs = (p.total_q + run - 1) / run;
+  const int64_t tasks = runs * parts, nw = (int64_t)gridDim.x * kWarps;
   for (int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); task < tasks; task += nw) {
-    const int64_t t = task / parts;
-    const int part = (int)(task - t * parts);
-    const int b = find_sequence(p, t);
-    const int pos = token_position(p, t, b, &hdr->status);
-    const int page = pos >= 0 ? paged_page(p, b, pos, &hdr->status) : -1;
-    if (WRITE && page < 0) continue;
-    // a part is a stretch of whole groups of 32 chunks
-    auto cut = [&](int n, int i) { return min(n, (int)(((int64_t)((n + 31) / 32) * i / parts) * 32)); };
-    token_rows<T, KIND, WRITE>(p, t, max(pos, 0), page, cut(ck, part), cut(ck, part + 1), p.dim_qk, (const T*)p.k,
-                               p.sk, k_out, p.kc, p.ks);
-    token_rows<T, KIND, WRITE>(p, t, max(pos, 0), page, cut(cv, part), cut(cv, part + 1), p.dim_v, (const T*)p.v,
-                               p.sv, v_out, p.vc, p.vs);
+    const int64_t t0 = task / parts * run;
+    const int part = (int)(task % parts);
+    // this lane's token: its row of the cache for head 0, or -1
+    int64_t row = -1;
+    if (lane < run && t0 + lane < p.total_q) {
+      const int b = find_sequence(p, t0 + lane);
+      const int pos = token_position(p, t0 + lane, b, &hdr->status);
+      const int page = pos >= 0 ? paged_page(p, b, pos, &hdr->status) : -1;
+      if (page >= 0) row = paged_row(p, page, 0, pos);
+    }
+    const int n = (int)min((int64_t)run, p.total_q - t0);
+    // a part is a stretch of whole groups of 32 pieces
+    auto cut = [&](int m, int i) { return min(m, (int)((int64_t)((m + 31) / 32) * i / parts) * 32); };
+    const int k0 = cut(ck, part), k1 = cut(ck, part + 1), v0 = cut(cv, part), v1 = cut(cv, part + 1);
+    for (int i = 0; i < n; ++i) {
+      const int64_t t = t0 + i, r0 = __shfl_sync(0xffffffffu, row, i);
+      const bool has = r0 >= 0;
+      if (WRITE && !has) continue;
+      Piece<W> pk(k0 + lane, perk), pv(v0 + lane, perv);
+      for (int step = 0; k0 + 32 * step < k1 || v0 + 32 * step < v1; step += U) {
+        Raw<T, W> rk[U], rv[U];
+        uint4 code_k[MX ? U : 1], code_v[MX ? U : 1];
+        float fk[MX ? U : 1], fv[MX ? U : 1];
+        const Piece<W> sk = pk, sv = pv;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t rowk = r0 + ((int64_t)pk.head << p.page_shift), rowv = r0 + ((int64_t)pv.head << p.page_shift);
+          const bool okk = pk.c < k1, okv = pv.c < v1;
+          if constexpr (WRITE) {
+            rk[u].zero();
+            rv[u].zero();
+            if (okk) rk[u].load((const T*)p.k + t * p.sk + (int64_t)pk.c * W);
+            if (okv) rv[u].load((const T*)p.v + t * p.sv + (int64_t)pv.c * W);
+          } else if constexpr (MX) {
+            code_k[u] = code_v[u] = make_uint4(0u, 0u, 0u, 0u);
+            fk[u] = fv[u] = 0.f;
+            if (okk && has) {
+              code_k[u] = __ldcs(reinterpret_cast<const uint4*>((const uint8_t*)p.kc + rowk * p.dim_qk) + pk.col);
+              fk[u] = __uint_as_float((uint32_t)__ldg(p.ks + rowk * (p.dim_qk >> 5) + (pk.col >> 1)) << 23);
+            }
+            if (okv && has) {
+              code_v[u] = __ldcs(reinterpret_cast<const uint4*>((const uint8_t*)p.vc + rowv * p.dim_v) + pv.col);
+              fv[u] = __uint_as_float((uint32_t)__ldg(p.vs + rowv * (p.dim_v >> 5) + (pv.col >> 1)) << 23);
+            }
+          } else {
+            rk[u].zero();
+            rv[u].zero();
+            if (okk && has) rk[u].load((const T*)p.kc + rowk * p.dim_qk + pk.col * W);
+            if (okv && has) rv[u].load((const T*)p.vc + rowv * p.dim_v + pv.col * W);
+          }
+          pk.next(perk, dhk, dck);
+          pv.next(perv, dhv, dcv);
+        }
+        pk = sk;
+        pv = sv;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t rowk = r0 + ((int64_t)pk.head << p.page_shift), rowv = r0 + ((int64_t)pv.head << p.page_shift);
+          const bool okk = pk.c < k1, okv = pv.c < v1;
+          if constexpr (WRITE && MX) {
+            write_mx<T>(rk[u], (uint8_t*)p.kc + rowk * p.dim_qk + pk.col * W,
+                        p.ks + rowk * (p.dim_qk >> 5) + (pk.col >> 1), pk.col, okk);
+            write_mx<T>(rv[u], (uint8_t*)p.vc + rowv * p.dim_v + pv.col * W,
+                        p.vs + rowv * (p.dim_v >> 5) + (pv.col >> 1), pv.col, okv);
+          } else if constexpr (WRITE) {
+            if (okk) rk[u].store((T*)p.kc + rowk * p.dim_qk + pk.col * W);
+            if (okv) rv[u].store((T*)p.vc + rowv * p.dim_v + pv.col * W);
+          } else {
+            if constexpr (MX) {
+              auto values = [](const uint4& c, float f, Raw<T, W>& out) {
+                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+                float x[W];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const float2 y = e4m3_values((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+                  x[2 * j] = y.x * f;
+                  x[2 * j + 1] = y.y * f;
+                }
+                out.set(x);
+              };
+              values(code_k[u], fk[u], rk[u]);
+              values(code_v[u], fv[u], rv[u]);
+            }
+            if (okk) rk[u].store(k_out + t * ck * W + (int64_t)pk.c * W);
+            if (okv) rv[u].store(v_out + t * cv * W + (int64_t)pv.c * W);
+          }
+          pk.next(perk, dhk, dck);
+          pv.next(perv, dhv, dcv);
+        }
+      }
+    }
   }
 }
 
 template <typename T, int KIND, bool WRITE>
 cudaError_t launch_t(const Paged& p, void* k, void* v, PagedHeader* hdr, int planned, cudaStream_t s) {
-  // warps a token: one, more where the tokens alone do not fill the GPU
-  const int64_t warps = (int64_t)num_sms() * kWarps * 4;
-  const int most = (p.heads_k * ((p.dim_qk > p.dim_v ? p.dim_qk : p.dim_v) / 8) + 31) / 32;
-  int64_t parts = (warps + p.total_q - 1) / p.total_q;
+  // Runs of tokens to about two a warp of a full GPU; with fewer tokens than warps, several
+  // warps a token instead (a serving step of 256 tokens would leave most SMs without work).
+  constexpr int W = KIND == kCacheMx ? 16 : 8;
+  const int64_t warps = (int64_t)num_sms() * kWarps * 3;
+  int64_t run = p.total_q / (2 * warps);
+  run = run < 1 ? 1 : run > 32 ? 32 : run;
+  const int most = (p.heads_k * ((p.dim_qk > p.dim_v ? p.dim_qk : p.dim_v) / W) + 31) / 32;
+  int64_t parts = run > 1 ? 1 : (warps + p.total_q - 1) / p.total_q;
   if (parts > most) parts = most;
-  int64_t grid = (p.total_q * parts + kWarps - 1) / kWarps;
-  const int64_t cap = (int64_t)num_sms() * 8;
+  int64_t grid = ((p.total_q + run - 1) / run * parts + kWarps - 1) / kWarps;
+  const int64_t cap = (int64_t)num_sms() * 3;
   if (grid > cap) grid = cap;
-  cache_kernel<T, KIND, WRITE><<<(unsigned)grid, kThreads, 0, s>>>(p, (T*)k, (T*)v, hdr, (int)parts, planned);
+  cache_kernel<T, KIND, WRITE><<<(unsigned)grid, kThreads, 0, s>>>(p, (T*)k, (T*)v, hdr, (int)run, (int)parts, planned);
   return cudaGetLastError();
 }
 template <bool WRITE>

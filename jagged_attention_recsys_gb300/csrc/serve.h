@@ -70,7 +70,8 @@ struct __align__(16) PagedPos {
 struct PagedHeader {
   int status;
   int n_ctas;  // CTAs the work is cut for
-  int pad[62];
+  int pad[2];
+  int zeros[60];  // stays zero: scales of keys that are not there
 };
 static_assert(sizeof(PagedHeader) == 256, "workspace header");
 

@@ -190,6 +190,23 @@ def test_large_scores_and_scale():
         check_attention(b, 4, scale=3.0)
 
 
+@pytest.mark.parametrize("low,high", [(119, 136), (60, 190), (1, 3), (223, 230)])
+@pytest.mark.parametrize("kind,hq,hk,dqk,dv", [("step", 8, 2, 128, 128), ("chunk", 3, 1, 64, 64), ("chunk", 8, 2, 128, 64),
+                                               ("one long", 4, 2, 64, 128)])
+def test_mxfp8_values_of_any_size(kind, hq, hk, dqk, dv, low, high):
+    """Values whose scales lie up to the whole range apart, key by key and block by block: every
+    column keeps its precision relative to its own sum of p |v|."""
+    b = Batch(*ragged(kind), hk, dqk, dv, 32, "mxfp8", "bf16", seed=3)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    s = torch.randint(low, high + 1, b.cache.v_scale.shape, generator=g, device="cuda", dtype=torch.int32)
+    # some blocks of columns only, and some keys
+    s = torch.where(torch.rand(s.shape, generator=g, device="cuda") < 0.5, s, (low + high) // 2)
+    b.cache.v_scale.copy_(torch.where(b.owned, s, 255).to(torch.uint8))
+    v, vs = b.cache.v.cpu().numpy(), b.cache.v_scale.cpu().numpy()
+    b.v_h = ref.decode(v, vs)
+    check_attention(b, hq)
+
+
 def test_rows_behind_the_last_and_strided_queries():
     """Queries as a slice of a projection's output; rows behind the call's stay as they were."""
     n, lens = ragged("chunk")
