@@ -515,20 +515,20 @@ def _on(device, stream):
 
 def _rows(name, t, dtype, device, heads=None, dim=None, tokens=None):
     """Checks [T, heads, dim] rows with contiguous heads; returns the stride between tokens."""
-    if t.dim() != 3 or not t.is_cuda or t.device != device or t.dtype != dtype:
+    if t.dim() != 3 or t.dtype is not dtype or t.device != device:
         raise ValueError("%s must be a [tokens, heads, dim] %s tensor on %s" % (name, dtype, device))
-    if (heads not in (None, t.shape[1]) or dim not in (None, t.shape[2])
-            or tokens not in (None, t.shape[0])):
+    T, H, D = t.shape
+    if heads not in (None, H) or dim not in (None, D) or tokens not in (None, T):
         raise ValueError("%s has shape %s, which does not fit the other arguments" % (name, tuple(t.shape)))
-    if t.numel() and ((t.shape[2] > 1 and t.stride(2) != 1)
-                      or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
-        raise ValueError("%s: the heads of a token must be contiguous" % name)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        if T * H * D:
+            raise ValueError("%s: the heads of a token must be contiguous" % name)
+    return st if T > 1 else H * D
 
 
 def _plain(name, t, dtype, shape, device):
-    if (not t.is_cuda or t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape)
-            or not t.is_contiguous()):
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
                          % (name, dtype, tuple(shape), device))
 
@@ -550,7 +550,7 @@ def _norm_rope_params(q, k, pos, wq, wk, eps, rope, norm):
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
-    if not x.is_cuda or x.dim() != 3:
+    if x.dim() != 3 or not x.is_cuda:
         raise ValueError("q and k must be [tokens, heads, dim] CUDA tensors")
     if not norm and (wq is not None or wk is not None):
         raise ValueError("norm=False takes no weights")
@@ -569,8 +569,12 @@ def _norm_rope_params(q, k, pos, wq, wk, eps, rope, norm):
     return p, x
 
 
-def _like(t):
-    return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+def _out(name, t, like, make=True):
+    """A tensor of the rows of ``like`` and its stride between tokens; made if None."""
+    T, H, D = like.shape
+    if t is None and make:
+        return torch.empty((T, H, D), dtype=like.dtype, device=like.device), H * D
+    return t, _rows(name, t, like.dtype, like.device, H, D, T)
 
 
 def jfa_norm_rope_fwd(q, k, pos, wq=None, wk=None, *, rope=None, eps=1e-6, norm=True, yq=None,
@@ -579,11 +583,9 @@ def jfa_norm_rope_fwd(q, k, pos, wq=None, wk=None, *, rope=None, eps=1e-6, norm=
     rotary position embedding ``rope`` (jfa_rope) at positions ``pos`` [T]; returns (yq, yk)."""
     p, x = _norm_rope_params(q, k, pos, wq, wk, eps, rope, norm)
     if q is not None:
-        yq = _like(q) if yq is None else yq
-        p.stride_yq = _rows("yq", yq, q.dtype, q.device, *q.shape[1:], q.shape[0])
+        yq, p.stride_yq = _out("yq", yq, q)
     if k is not None:
-        yk = _like(k) if yk is None else yk
-        p.stride_yk = _rows("yk", yk, k.dtype, k.device, *k.shape[1:], k.shape[0])
+        yk, p.stride_yk = _out("yk", yk, k)
     _check(lib().jfa_norm_rope_fwd(ctypes.byref(p), _addr(q), _addr(k), _addr(pos), _addr(wq), _addr(wk),
                                    _addr(yq), _addr(yk), _on(x.device, stream)), "jfa_norm_rope_fwd")
     return yq, yk
@@ -596,15 +598,13 @@ def jfa_norm_rope_bwd(q, k, pos, dyq, dyk, wq=None, wk=None, *, rope=None, eps=1
     p, x = _norm_rope_params(q, k, pos, wq, wk, eps, rope, norm)
     f32 = dict(dtype=torch.float32, device=x.device)
     if q is not None:
-        p.stride_yq = _rows("dyq", dyq, q.dtype, q.device, *q.shape[1:], q.shape[0])
-        dq = _like(q) if dq is None else dq
-        p.stride_dq = _rows("dq", dq, q.dtype, q.device, *q.shape[1:], q.shape[0])
+        p.stride_yq = _out("dyq", dyq, q, False)[1]
+        dq, p.stride_dq = _out("dq", dq, q)
         if wq is not None and dwq is None:
             dwq = torch.empty(p.dim, **f32)
     if k is not None:
-        p.stride_yk = _rows("dyk", dyk, k.dtype, k.device, *k.shape[1:], k.shape[0])
-        dk = _like(k) if dk is None else dk
-        p.stride_dk = _rows("dk", dk, k.dtype, k.device, *k.shape[1:], k.shape[0])
+        p.stride_yk = _out("dyk", dyk, k, False)[1]
+        dk, p.stride_dk = _out("dk", dk, k)
         if wk is not None and dwk is None:
             dwk = torch.empty(p.dim, **f32)
     for name, w in (("dwq", dwq), ("dwk", dwk)):
@@ -628,22 +628,24 @@ class PagedCache:
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if k.dim() != 4 or v.dim() != 4 or k.shape[:3] != v.shape[:3]:
             raise ValueError("k and v must be [pages, heads, page_size, dim] with the same pages")
-        for name, t, s in (("k", k, k_scale), ("v", v, v_scale)):
-            if not t.is_cuda or not t.is_contiguous() or t.device != k.device:
-                raise ValueError("the cache's arrays must be contiguous CUDA tensors on one device")
-            if (k_scale is None) != (s is None):
-                raise ValueError("k_scale and v_scale belong together")
-            if s is None:
-                if t.dtype not in (torch.float32, torch.bfloat16) or t.dtype != k.dtype:
-                    raise ValueError("%s must be fp32 or bf16 values, as k is" % name)
-            else:
-                if t.dtype != torch.uint8 or t.shape[3] % 32:
-                    raise ValueError("%s must be uint8 codes, columns a multiple of 32" % name)
-                _plain(name + "_scale", s, torch.uint8, (*t.shape[:3], t.shape[3] // 32), k.device)
+        if (k_scale is None) != (v_scale is None):
+            raise ValueError("k_scale and v_scale belong together")
+        if not k.is_cuda or v.device != k.device or not k.is_contiguous() or not v.is_contiguous():
+            raise ValueError("the cache's arrays must be contiguous CUDA tensors on one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.mxfp8 = k_scale is not None
         self.pages, self.heads, self.page_size, self.dim_qk = k.shape
         self.dim_v = v.shape[3]
+        if self.mxfp8:
+            if k.dtype is not torch.uint8 or v.dtype is not torch.uint8 or (self.dim_qk | self.dim_v) % 32:
+                raise ValueError("MXFP8 codes must be uint8, columns a multiple of 32")
+            _plain("k_scale", k_scale, torch.uint8, k.shape[:3] + (self.dim_qk // 32,), k.device)
+            _plain("v_scale", v_scale, torch.uint8, k.shape[:3] + (self.dim_v // 32,), k.device)
+            self.dtype_code = JFA_MXFP8
+        else:
+            if v.dtype is not k.dtype:
+                raise ValueError("k and v must be of one type")
+            self.dtype_code = _dtype_code(k.dtype)
 
     @property
     def device(self):
@@ -665,14 +667,10 @@ def paged_params(cache, table, offs, lens, total, dtype, *, heads_q=None, scale=
     """Params of the calls on a paged cache (strides of contiguous rows)."""
     hk, d, dv = cache.heads, cache.dim_qk, cache.dim_v
     hq = hk if heads_q is None else heads_q
-    if cache.mxfp8:
-        kind = JFA_MXFP8
-    else:
-        kind = _dtype_code(cache.k.dtype)
     return jfa_paged_params(offs.numel() - 1, total, cache.pages, hq * d, hk * d, hk * dv, hq, hk, d, dv,
                             cache.page_size, table.shape[1],
-                            1.0 / math.sqrt(d) if scale is None else scale, int(bool(causal)),
-                            _dtype_code(dtype), kind, 0)
+                            1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0,
+                            _dtype_code(dtype), cache.dtype_code, 0)
 
 
 def paged_workspace(p: jfa_paged_params, device="cuda") -> torch.Tensor:
@@ -683,7 +681,7 @@ def paged_workspace(p: jfa_paged_params, device="cuda") -> torch.Tensor:
 
 def _paged_prep(cache, table, offs, lens, total, dtype, heads_q, scale, causal, ws, planned):
     dev = cache.device
-    if offs.dim() != 1 or offs.numel() < 1 or table.dim() != 2:
+    if offs.dim() != 1 or table.dim() != 2 or offs.numel() < 1:
         raise ValueError("offs must be [B + 1], table [B, max_pages]")
     B = offs.numel() - 1
     _plain("offs", offs, torch.int64, (B + 1,), dev)
@@ -696,7 +694,7 @@ def _paged_prep(cache, table, offs, lens, total, dtype, heads_q, scale, causal, 
         p.flags = JFA_PLANNED
     if ws is None:
         ws = paged_workspace(p, dev)
-    elif not ws.is_cuda or ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+    elif ws.device != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous uint8 tensor on %s" % dev)
     return p, ws
 
@@ -721,10 +719,14 @@ def jfa_cache_read(cache, table, offs, lens, total, *, dtype=torch.bfloat16, k=N
     p, ws = _paged_prep(cache, table, offs, lens, total, dtype, None, None, True, ws, planned)
     dev = cache.device
     kshape, vshape = (total, cache.heads, cache.dim_qk), (total, cache.heads, cache.dim_v)
-    k = torch.empty(kshape, dtype=dtype, device=dev) if k is None else k
-    v = torch.empty(vshape, dtype=dtype, device=dev) if v is None else v
-    _plain("k", k, dtype, kshape, dev)
-    _plain("v", v, dtype, vshape, dev)
+    if k is None:
+        k = torch.empty(kshape, dtype=dtype, device=dev)
+    else:
+        _plain("k", k, dtype, kshape, dev)
+    if v is None:
+        v = torch.empty(vshape, dtype=dtype, device=dev)
+    else:
+        _plain("v", v, dtype, vshape, dev)
     _check(lib().jfa_cache_read(ctypes.byref(p), _addr(cache.k), _addr(cache.v), _addr(cache.k_scale),
                                 _addr(cache.v_scale), _addr(offs), _addr(lens), _addr(table), _addr(k),
                                 _addr(v), _addr(ws), ws.numel(), _on(dev, stream)), "jfa_cache_read")
@@ -751,11 +753,13 @@ def jfa_paged_fwd(q, cache, table, offs, lens, *, scale=None, causal=True, o=Non
     p.stride_q = _rows("q", q, q.dtype, dev, None, cache.dim_qk)
     T, H = q.shape[0], q.shape[1]
     if o is None:
-        o = torch.empty(T, H, cache.dim_v, dtype=q.dtype, device=dev)
+        o = torch.empty((T, H, cache.dim_v), dtype=q.dtype, device=dev)
+    else:
+        _plain("o", o, q.dtype, (T, H, cache.dim_v), dev)
     if lse is None:
-        lse = torch.empty(T, H, dtype=torch.float32, device=dev)
-    _plain("o", o, q.dtype, (T, H, cache.dim_v), dev)
-    _plain("lse", lse, torch.float32, (T, H), dev)
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _plain("lse", lse, torch.float32, (T, H), dev)
     _check(lib().jfa_paged_fwd(ctypes.byref(p), _addr(q), _addr(cache.k), _addr(cache.v), _addr(cache.k_scale),
                                _addr(cache.v_scale), _addr(offs), _addr(lens), _addr(table), _addr(o),
                                _addr(lse), _addr(ws), ws.numel(), _on(dev, stream)), "jfa_paged_fwd")

@@ -376,7 +376,8 @@ TileShape paged_shape(const Paged& p, int kernel) {
     t.share = 512;
     return t;
   }
-  const int most = kRows;
+  // the 16-row kernel's tiles of 8 rows where a sequence's rows of a key head fit them
+  const int most = kernel == kPagedRows16 && p.group <= 8 && p.total_q * p.group <= 8 * p.batch ? 8 : kRows;
   t.gsub = p.group < most ? p.group : most;
   t.nsub = (p.group + t.gsub - 1) / t.gsub;
   t.tokens = most / t.gsub;
@@ -387,9 +388,9 @@ TileShape paged_shape(const Paged& p, int kernel) {
   return t;
 }
 
-int paged_ctas(const Paged&, int kernel) {
+int paged_ctas(const Paged& p, int kernel) {
   if (kernel == kPagedTc) return num_sms() < kMaxTcCtas ? num_sms() : kMaxTcCtas;
-  const int n = num_sms() * (kernel == kPagedRows16 ? 2 : 3);
+  const int n = num_sms() * (kernel == kPagedRows16 && paged_shape(p, kernel).rows > 8 ? 2 : 3);
   return n < kMaxPagedCtas ? n : kMaxPagedCtas;
 }
 

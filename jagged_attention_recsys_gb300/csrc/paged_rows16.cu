@@ -9,15 +9,23 @@
 // sum and output, so the warps meet only at a tile's end, where they join through shared
 // memory while the producer already fills the ring with the next tile.
 //
-// The products run on mma.sync (16 x 8 x 16): the 16 rows are its M, where tcgen05's smallest
-// tile would be seven eighths empty, and the fragments' operands come straight from the stage
-// by ldmatrix (swizzled, no bank conflicts).
+// The products run on mma.sync (16 x 8 x 16) transposed, S^T = K Q^T and O^T = V^T P^T: keys and
+// value columns are the 16 of its M and the rows its N, 8 or 16 of them, so that a step with one
+// token and up to 8 heads a key head pads little and needs half the registers and MMAs (three
+// CTAs an SM instead of two).  tcgen05's smallest tile would be seven eighths empty.  K and V
+// come straight from the stage by ldmatrix (swizzled, no bank conflicts), and P turns from S^T's
+// layout into an operand's by movmatrix.
 //
 // MXFP8.  Codes are exact in fp16, and a row of bf16 queries times a power of two that brings
 // its largest value to [2^14, 2^15) is exact in fp16 too (values under 2^-31 of the largest lose
 // at most 2^-39 of it), so the scores are fp16 products of codes, one block of 32 columns at a
-// time, and a block's scale multiplies its fp32 sum.  Values are brought to bf16 (exact: 3-bit
-// mantissas times a power of two) in registers.
+// time, and a block's scale multiplies its fp32 sum.  For the output the scales go to the
+// weights: a block of columns has a reference scale, the largest it met (O is kept in its
+// units), and the weights times scale / reference, at most 1, are rounded to fp16 (2^-12 of a
+// weight down to 2^-14, absolutely 2^-25 below) against fp16 codes.  A stage with a scale under
+// 2^-8 of its reference takes its values to bf16 instead (exact) and rounds the weights alone,
+// so that keys of small values keep their precision beside keys of large ones.  With every value
+// taken to bf16 an MXFP8 step ran at 4.0 TB/s, held by the conversions.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -37,8 +45,9 @@ constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int DQK, int DV, int KIND>
+template <int DQK, int DV, int KIND, int NT>
 struct Layout {
+  static constexpr int R = 8 * NT;  // rows of a tile
   static constexpr int E = KIND == kCacheMx ? 1 : 2;  // bytes of an element
   // Keys of a stage: 32, or 16 where twelve stages would not fit otherwise.
   static constexpr int kKeys = paged_rows16_keys(DQK, DV, KIND);
@@ -47,12 +56,15 @@ struct Layout {
   static constexpr uint32_t BYTES = KB + VB + KS + VS;  // of a stage's loads
   static constexpr uint32_t STAGE = KB + VB;
   static constexpr uint32_t SCALES = 256;  // a stage's scales (K at 0, V at 128)
-  static constexpr uint32_t LIMIT = 113 * 1024;  // two CTAs an SM
-  // in front: barriers, abort flag, statistics; then the join's buffer, the scales, the stages
-  static constexpr uint32_t ML = 512;  // [warps][16][2] floats
-  static constexpr uint32_t JOIN = ML + kConsumers * 16 * 2 * 4;
+  static constexpr int CTAS = NT == 1 ? 3 : 2;  // of an SM
+  static constexpr uint32_t LIMIT = NT == 1 ? 74 * 1024 + 512 : 113 * 1024;
+  // in front: barriers, abort flag, statistics; then the join's buffer, the value scales as fp16
+  // factors, the scales, the stages
+  static constexpr uint32_t ML = 512;  // [warps][R][2] floats
+  static constexpr uint32_t JOIN = ML + kConsumers * R * 2 * 4;
   static constexpr int JOIN_LD = 36;  // 32 columns a round, padded
-  static constexpr uint32_t SCALE0 = JOIN + kConsumers * 16 * JOIN_LD * 4;
+  static constexpr uint32_t FAC = JOIN + kConsumers * R * JOIN_LD * 4;  // [warps][blocks][32 keys] halves
+  static constexpr uint32_t SCALE0 = FAC + (KS ? kConsumers * (DV / 32) * 64 : 0);
   static constexpr int NS_ = (LIMIT - SCALE0 - 1024) / (STAGE + (KS ? SCALES : 0));
   // A multiple of the consumers, so that a stage is always the same warp's: fills land in any
   // order, and a warp that came to a stage before another's previous fill of it had landed
@@ -89,6 +101,14 @@ __device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint32_t* a, 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// c = a b, nothing added
+__device__ __forceinline__ void mma_16816_f16_zero(float (&c)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+      "%10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t e4m3_half2(uint32_t pair) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pair));
@@ -99,12 +119,26 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// 2^(s - 127); 255 (a scale that is no number) counts as the largest, so that zeros stay zeros
-__device__ __forceinline__ float scale_of(uint32_t s) { return __uint_as_float(min(s & 255u, 254u) << 23); }
+// 2^(s - 127) of byte B of x (0: zero)
+template <int B>
+__device__ __forceinline__ float scale_byte(uint32_t x) {
+  return __uint_as_float((B < 3 ? x << (23 - 8 * B) : x >> 1) & 0x7f800000u);
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
+}
+// an 8 x 8 matrix of 16-bit values, transposed
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
@@ -125,11 +159,11 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
   return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
 }
 
-template <int DQK, int DV, int KIND>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int DQK, int DV, int KIND, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedWs w,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
-  using L = Layout<DQK, DV, KIND>;
+  using L = Layout<DQK, DV, KIND, NT>;
   constexpr int E = L::E, NS = L::NS, kKeys = L::kKeys;
   constexpr bool MX = KIND == kCacheMx;
   extern __shared__ uint8_t smem_raw[];
@@ -192,10 +226,13 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
                 tma_load_2d(tile + L::KB + h * kKeys * 128 + s * box * (DV * E < 128 ? DV * E : 128), &tm_v,
                             h * (128 / E), r, bar);
               if constexpr (MX) {
-                const int64_t rs = r == none ? 0 : r;  // no row: any scales do, its codes are zeros
+                // no row: scales of zero, from the header
                 const uint32_t sc = sb + L::SCALE0 + st * L::SCALES;
-                bulk_load(sc + s * box * (DQK / 32), p.ks + rs * (DQK / 32), box * (DQK / 32), bar);
-                bulk_load(sc + 128 + s * box * (DV / 32), p.vs + rs * (DV / 32), box * (DV / 32), bar);
+                const uint8_t* zeros = reinterpret_cast<const uint8_t*>(w.hdr->zeros);
+                bulk_load(sc + s * box * (DQK / 32), r == none ? zeros : p.ks + (int64_t)r * (DQK / 32),
+                          box * (DQK / 32), bar);
+                bulk_load(sc + 128 + s * box * (DV / 32), r == none ? zeros : p.vs + (int64_t)r * (DV / 32),
+                          box * (DV / 32), bar);
               }
             }
           }
@@ -208,33 +245,33 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
   }
 
   // -------------------------------------------------------------------- consumers
-  const int rq = lane >> 2, q = lane & 3;  // rows rq and rq + 8 of the tile; column pair q
-  constexpr int NT = kKeys / 8;            // score tiles of a stage
-  constexpr int OT = DV / 8;               // output tiles
+  // Fragments: a lane's keys (or value columns) are kq and kq + 8 of 16, its rows 2 q and 2 q + 1
+  // of 8; as an operand's holder of Q and P it has row kq.
+  const int kq = lane >> 2, q = lane & 3;
+  constexpr int G16 = kKeys / 16;  // groups of 16 keys
+  constexpr int MT = DV / 16;      // output tiles
+  constexpr int NBK = DQK / 32, NBV = DV / 32;
   // a consumer that gave up in a wait walks on without computing, so that its barriers still match
   bool dead = false;
   while (walk.next(p, t, g)) {
     const int head_k = g.unit / t.nsub, gs0 = (g.unit % t.nsub) * t.gsub;
-    uint32_t qa[DQK / 16][4];
-    int limit[2];  // keys the rows see
-    int64_t orow[2];
-    float cs[2];   // score units to log2 units
+    uint32_t qb[NT][DQK / 16][2];
+    int limit[NT][2];  // keys that rows 2 q, 2 q + 1 see
+    float cs[NT][2];   // their score units to log2 units
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int r = rq + 8 * x, tok = g.tile * t.tokens + r / t.gsub, gh = gs0 + r % t.gsub;
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + kq, tok = g.tile * t.tokens + r / t.gsub, gh = gs0 + r % t.gsub;
       const bool row_ok = r < t.rows && tok < g.seq.lq && gh < p.group;
+      const __nv_bfloat16* src = (const __nv_bfloat16*)p.q + (int64_t)(g.seq.q0 + tok) * p.sq +
+                                 (int64_t)(head_k * p.group + gh) * DQK;
       const int64_t lim = g.seq.off + tok + 1;
-      limit[x] = !row_ok ? 0 : p.causal ? (int)max((int64_t)0, lim) : g.seq.lk;
-      const int head = head_k * p.group + gh;
-      orow[x] = row_ok ? (int64_t)(g.seq.q0 + tok) * p.heads_q + head : -1;
-      const __nv_bfloat16* src =
-          (const __nv_bfloat16*)p.q + (int64_t)(g.seq.q0 + tok) * p.sq + (int64_t)head * DQK;
-      cs[x] = p.scale * kLog2e;
+      const int mine = !row_ok ? 0 : p.causal ? (int)max((int64_t)0, lim) : g.seq.lk;
+      float c = p.scale * kLog2e;
       if constexpr (!MX) {
 #pragma unroll
         for (int k = 0; k < DQK / 16; ++k) {
-          qa[k][x] = row_ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * q)) : 0u;
-          qa[k][2 + x] = row_ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * q + 8)) : 0u;
+          qb[nt][k][0] = row_ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * q)) : 0u;
+          qb[nt][k][1] = row_ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * q + 8)) : 0u;
         }
       } else {
         // columns 16 k + 4 q .. + 3, as the codes of a chunk fall to the lanes
@@ -250,17 +287,32 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);  // of the largest
         const float f = exp2i(14 - e);
-        cs[x] *= exp2i(e - 14);
+        c *= exp2i(e - 14);
 #pragma unroll
         for (int k = 0; k < DQK / 16; ++k) {
-          qa[k][x] = half2_of(__uint_as_float(v[k].x << 16) * f, __uint_as_float(v[k].x & 0xffff0000u) * f);
-          qa[k][2 + x] = half2_of(__uint_as_float(v[k].y << 16) * f, __uint_as_float(v[k].y & 0xffff0000u) * f);
+          qb[nt][k][0] = half2_of(__uint_as_float(v[k].x << 16) * f, __uint_as_float(v[k].x & 0xffff0000u) * f);
+          qb[nt][k][1] = half2_of(__uint_as_float(v[k].y << 16) * f, __uint_as_float(v[k].y & 0xffff0000u) * f);
         }
       }
-    }
-    float o[OT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < OT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      for (int e = 0; e < 2; ++e) {
+        limit[nt][e] = __shfl_sync(0xffffffffu, mine, (2 * q + e) * 4);
+        cs[nt][e] = __shfl_sync(0xffffffffu, c, (2 * q + e) * 4);
+      }
+    }
+    float o[NT][MT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+    // MXFP8: the blocks' reference scales (biased, at most 254; O of block b is in units of
+    // 2^(ref - 127))
+    int ref_scale[NBV];
+#pragma unroll
+    for (int i = 0; i < NBV; ++i) ref_scale[i] = 0;
 
     for (int blk = g.blk0; blk < g.blk1; ++blk, ++cnt) {
       if ((int)(cnt % kConsumers) != warp) continue;
@@ -277,142 +329,220 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
           const int row = DV * E >= 128 ? (i >> 3) % kKeys : i >> 2;
           if (row >= nk) st_shared_v4(vt + 16 * i, 0u, 0u, 0u, 0u);
         }
+        if constexpr (MX) {  // and their scales, which have to be numbers: the first key's
+          const uint32_t first = NBV == 4 ? ld_shared_u32(sc + 128) : ld_shared_u32(sc + 128) & 0xffffu;
+          if (lane >= nk) {
+            if constexpr (NBV == 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sc + 128 + lane * 4), "r"(first) : "memory");
+            else asm volatile("st.shared.u16 [%0], %1;" ::"r"(sc + 128 + lane * 2), "h"((uint16_t)first) : "memory");
+          }
+        }
         fence_proxy_async_smem();  // the stage's next loads come through the async proxy
         __syncwarp();
       }
+      // the four 8 x 8 matrices that a lane's address names: halves of 16 keys, chunks
+      const int mi = lane >> 3, mr = lane & 7;
       // ---- scores
-      float s[NT][4];
+      float s[G16][NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      for (int ks = 0; ks < G16; ++ks) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[ks][nt][0] = s[ks][nt][1] = s[ks][nt][2] = s[ks][nt][3] = 0.f;
         if constexpr (!MX) {
 #pragma unroll
-          for (int k2 = 0; k2 < DQK / 32; ++k2) {
-            uint32_t b[4];
-            ldsm4(b, kt + chunk_at<DQK, E, kKeys>(n * 8 + (lane & 7), 4 * k2 + (lane >> 3)));
-            mma_16816_bf16(s[n], qa[2 * k2], b[0], b[1]);
-            mma_16816_bf16(s[n], qa[2 * k2 + 1], b[2], b[3]);
+          for (int k = 0; k < DQK / 16; ++k) {
+            uint32_t a[4];
+            ldsm4(a, kt + chunk_at<DQK, E, kKeys>(ks * 16 + (mi & 1) * 8 + mr, 2 * k + (mi >> 1)));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16816_bf16(s[ks][nt], a, qb[nt][k][0], qb[nt][k][1]);
           }
         } else {
-          // scales of this lane's two keys (columns 2 q, 2 q + 1 of the score tile)
-          constexpr int NB = DQK / 32;
-          uint32_t sk[2];
-          if constexpr (NB == 4) {
-            sk[0] = ld_shared_u32(sc + (n * 8 + 2 * q) * 4);
-            sk[1] = ld_shared_u32(sc + (n * 8 + 2 * q + 1) * 4);
-          } else {
-            const uint32_t x = ld_shared_u32(sc + (n * 8 + 2 * q) * 2);
-            sk[0] = x & 0xffffu;
-            sk[1] = x >> 16;
+          uint32_t sk[2];  // scales of keys kq, kq + 8
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int key = ks * 16 + kq + 8 * i;
+            if constexpr (NBK == 4) sk[i] = ld_shared_u32(sc + key * 4);
+            else sk[i] = ld_shared_u32(sc + (key & ~1) * 2) >> (16 * (key & 1));
           }
-#pragma unroll
-          for (int h = 0; h < DQK / 64; ++h) {
+          auto block = [&](int c2, float f0, float f1) {  // a block: two chunks of 16 columns
             uint32_t b[4];
-            ldsm4(b, kt + chunk_at<DQK, E, kKeys>(n * 8 + (lane & 7), 4 * h + (lane >> 3)));
+            ldsm4(b, kt + chunk_at<DQK, E, kKeys>(ks * 16 + (mi & 1) * 8 + mr, 2 * c2 + (mi >> 1)));
+            uint32_t a[2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {  // a block: two chunks of 16 columns
-              float x[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_16816_f16(x, qa[4 * h + 2 * i], e4m3_half2(b[2 * i] & 0xffffu), e4m3_half2(b[2 * i] >> 16));
-              mma_16816_f16(x, qa[4 * h + 2 * i + 1], e4m3_half2(b[2 * i + 1] & 0xffffu), e4m3_half2(b[2 * i + 1] >> 16));
-              const float f0 = scale_of(sk[0] >> (8 * (2 * h + i))), f1 = scale_of(sk[1] >> (8 * (2 * h + i)));
-              s[n][0] = fmaf(x[0], f0, s[n][0]);
-              s[n][1] = fmaf(x[1], f1, s[n][1]);
-              s[n][2] = fmaf(x[2], f0, s[n][2]);
-              s[n][3] = fmaf(x[3], f1, s[n][3]);
+            for (int j = 0; j < 2; ++j) {
+              a[j][0] = e4m3_half2(b[2 * j] & 0xffffu);
+              a[j][1] = e4m3_half2(b[2 * j + 1] & 0xffffu);
+              a[j][2] = e4m3_half2(b[2 * j] >> 16);
+              a[j][3] = e4m3_half2(b[2 * j + 1] >> 16);
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float x[4];
+              mma_16816_f16_zero(x, a[0], qb[nt][2 * c2][0], qb[nt][2 * c2][1]);
+              mma_16816_f16(x, a[1], qb[nt][2 * c2 + 1][0], qb[nt][2 * c2 + 1][1]);
+              s[ks][nt][0] = fmaf(x[0], f0, s[ks][nt][0]);
+              s[ks][nt][1] = fmaf(x[1], f0, s[ks][nt][1]);
+              s[ks][nt][2] = fmaf(x[2], f1, s[ks][nt][2]);
+              s[ks][nt][3] = fmaf(x[3], f1, s[ks][nt][3]);
+            }
+          };
+          block(0, scale_byte<0>(sk[0]), scale_byte<0>(sk[1]));
+          block(1, scale_byte<1>(sk[0]), scale_byte<1>(sk[1]));
+          if constexpr (NBK == 4) {
+            block(2, scale_byte<2>(sk[0]), scale_byte<2>(sk[1]));
+            block(3, scale_byte<3>(sk[0]), scale_byte<3>(sk[1]));
           }
         }
       }
       // ---- weights
-      float mn[2], ref[2];
+      bool moved = false;
+      float mn[NT][2], ref[NT][2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int seen = min(limit[x], g.seq.lk) - k0;  // keys of this stage the row sees
-        float top = -INFINITY;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int e = 0; e < 2; ++e) {
+          const int seen = min(limit[nt][e], g.seq.lk) - k0;  // keys of this stage the row sees
+          float top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float& v = s[n][2 * x + i];
-            v = n * 8 + 2 * q + i < seen ? v * cs[x] : -INFINITY;
-            top = fmaxf(top, v);
-          }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        mn[x] = fmaxf(m[x], top);
-        ref[x] = mn[x] == -INFINITY ? 0.f : mn[x];
-      }
-      if (__any_sync(0xffffffffu, mn[0] != m[0] || mn[1] != m[1])) {
+          for (int ks = 0; ks < G16; ++ks)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float a = ex2(m[x] - ref[x]);
-          l[x] *= a;
-#pragma unroll
-          for (int i = 0; i < OT; ++i) {
-            o[i][2 * x] *= a;
-            o[i][2 * x + 1] *= a;
-          }
-          m[x] = mn[x];
+            for (int h = 0; h < 2; ++h) {
+              float& v = s[ks][nt][2 * h + e];
+              v = ks * 16 + 8 * h + kq < seen ? v * cs[nt][e] : -INFINITY;
+              top = fmaxf(top, v);
+            }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          mn[nt][e] = fmaxf(m[nt][e], top);
+          ref[nt][e] = mn[nt][e] == -INFINITY ? 0.f : mn[nt][e];
+          moved |= mn[nt][e] != m[nt][e];
         }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float a = ex2(m[nt][e] - ref[nt][e]);  // m = -inf: 0
+            l[nt][e] *= a;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              o[nt][i][e] *= a;
+              o[nt][i][2 + e] *= a;
+            }
+            m[nt][e] = mn[nt][e];
+          }
       }
-      uint32_t pa[NT / 2][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int ks = 0; ks < G16; ++ks)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float a = ex2(s[n][2 * x] - ref[x]), b = ex2(s[n][2 * x + 1] - ref[x]);
-          l[x] += a + b;
-          // the weights' rounding to bf16, as the operand's type (2^-9 on average, signs mixed)
-          pa[n >> 1][2 * (n & 1) + x] = pack_bf16(a, b);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[ks][nt][i] = ex2(s[ks][nt][i] - ref[nt][i & 1]);
+            l[nt][i & 1] += s[ks][nt][i];
+          }
+      // The weights as the products' operand: rounded to bf16 (2^-9 of a weight on average, signs
+      // mixed) or, against fp16 codes, to fp16.
+      bool wide = false;  // MXFP8: a scale far under its block's reference
+      if constexpr (MX) {
+        const uint32_t mine = NBV == 4 ? ld_shared_u32(sc + 128 + lane * 4)
+                                       : (ld_shared_u32(sc + 128 + (lane & ~1) * 2) >> (16 * (lane & 1))) & 0xffffu;
+        const uint32_t fac = sb + L::FAC + warp * NBV * 64;
+#pragma unroll
+        for (int i = 0; i < NBV; ++i) {
+          const int e = min((mine >> (8 * i)) & 255, 254u);
+          const int top = __reduce_max_sync(0xffffffffu, e), low = __reduce_min_sync(0xffffffffu, e);
+          if (top > ref_scale[i]) {  // O of the block goes to the new units
+            const float f = ref_scale[i] == 0 ? 1.f : exp2i(max(ref_scale[i] - top, -126));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                o[nt][2 * i][k] *= f;
+                o[nt][2 * i + 1][k] *= f;
+              }
+            ref_scale[i] = top;
+          }
+          wide |= low < ref_scale[i] - 8;
+          // the key's scale over the reference, 2^-8 to 1 as a half
+          const uint16_t h = (uint16_t)((e - ref_scale[i] + 15) << 10);
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(fac + (i * 32 + lane) * 2), "h"(h) : "memory");
         }
+        __syncwarp();
       }
+      uint32_t pb[G16][NT][2];
+#pragma unroll
+      for (int ks = 0; ks < G16; ++ks)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float a = s[ks][nt][2 * h], b = s[ks][nt][2 * h + 1];
+            pb[ks][nt][h] = movmatrix(MX && !wide ? half2_of(a, b) : pack_bf16(a, b));
+          }
       // ---- output
 #pragma unroll
-      for (int ks = 0; ks < kKeys / 16; ++ks) {
+      for (int ks = 0; ks < G16; ++ks) {
         if constexpr (!MX) {
 #pragma unroll
-          for (int np = 0; np < DV / 16; ++np) {
-            uint32_t b[4];
-            ldsm4t(b, vt + chunk_at<DV, E, kKeys>(ks * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * np + (lane >> 4)));
-            mma_16816_bf16(o[2 * np], pa[ks], b[0], b[1]);
-            mma_16816_bf16(o[2 * np + 1], pa[ks], b[2], b[3]);
-          }
-        } else {
-          // scales of this lane's four keys of the step
-          constexpr int NB = DV / 32;
-          uint32_t sv[4];
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t a[4];
+            ldsm4t(a, vt + chunk_at<DV, E, kKeys>(ks * 16 + (mi >> 1) * 8 + mr, 2 * mt + (mi & 1)));
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int key = ks * 16 + 8 * i + 2 * q;
-            if constexpr (NB == 4) {
-              sv[2 * i] = ld_shared_u32(sc + 128 + key * 4);
-              sv[2 * i + 1] = ld_shared_u32(sc + 128 + key * 4 + 4);
-            } else {
-              const uint32_t x = ld_shared_u32(sc + 128 + key * 2);
-              sv[2 * i] = x & 0xffffu;
-              sv[2 * i + 1] = x >> 16;
+            for (int nt = 0; nt < NT; ++nt) mma_16816_bf16(o[nt][mt], a, pb[ks][nt][0], pb[ks][nt][1]);
+          }
+        } else if (!wide) {
+          const uint32_t fac = sb + L::FAC + warp * NBV * 64 + (ks * 16 + 2 * q) * 2;
+#pragma unroll
+          for (int cp = 0; cp < NBV; ++cp) {  // two chunks of 16 columns: one block
+            uint32_t b[4], pw[NT][2];
+            ldsm4t(b, vt + chunk_at<DV, E, kKeys>(ks * 16 + (mi & 1) * 8 + mr, 2 * cp + (mi >> 1)));
+            const uint32_t f0 = ld_shared_u32(fac + cp * 64), f1 = ld_shared_u32(fac + cp * 64 + 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              pw[nt][0] = hmul2(pb[ks][nt][0], f0);
+              pw[nt][1] = hmul2(pb[ks][nt][1], f1);
             }
-          }
-#pragma unroll
-          for (int cp = 0; cp < DV / 32; ++cp) {  // two chunks of 16 columns: one block
-            uint32_t b[4];
-            ldsm4t(b, vt + chunk_at<DV, E, kKeys>(ks * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), 2 * cp + (lane >> 4)));
-            float f[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = scale_of(sv[i] >> (8 * cp));
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              uint32_t ev[2], od[2];  // even and odd columns, as two output tiles
+              // codes of keys 2 q, 2 q + 1: even columns to the low half, odd ones to the high, as
+              // rows kq and kq + 8 of the tile
+              const uint32_t r0 = __byte_perm(b[2 * c], 0, 0x3120), r1 = __byte_perm(b[2 * c + 1], 0, 0x3120);
+              const uint32_t a[4] = {e4m3_half2(r0 & 0xffffu), e4m3_half2(r0 >> 16), e4m3_half2(r1 & 0xffffu),
+                                     e4m3_half2(r1 >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_16816_f16(o[nt][2 * cp + c], a, pw[nt][0], pw[nt][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int cp = 0; cp < NBV; ++cp) {
+            uint32_t b[4];
+            ldsm4t(b, vt + chunk_at<DV, E, kKeys>(ks * 16 + (mi & 1) * 8 + mr, 2 * cp + (mi >> 1)));
+            // 2^(127 - reference), of which 2^-127 is no normal number, and its product with the
+            // scale 2^127 is exact all the same
+            const float unit = ref_scale[cp] == 254 ? __uint_as_float(0x00400000u) : exp2i(127 - ref_scale[cp]);
+            float f[4];  // of keys 2 q, 2 q + 1, 2 q + 8, 2 q + 9
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = ks * 16 + 2 * q + (i & 1) + 8 * (i >> 1);
+              const uint32_t x = NBV == 4 ? ld_shared_u32(sc + 128 + key * 4)
+                                          : ld_shared_u32(sc + 128 + (key & ~1) * 2) >> (16 * (key & 1));
+              f[i] = unit * __uint_as_float(((x >> (8 * cp)) & 255u) << 23);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t a[4];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const uint32_t r = b[2 * c + i];
                 const float2 x = fmul2(e4m3_values(r & 0xffffu), make_float2(f[2 * i], f[2 * i]));
                 const float2 y = fmul2(e4m3_values(r >> 16), make_float2(f[2 * i + 1], f[2 * i + 1]));
-                ev[i] = pack_bf16(x.x, y.x);
-                od[i] = pack_bf16(x.y, y.y);
+                a[2 * i] = pack_bf16(x.x, y.x);
+                a[2 * i + 1] = pack_bf16(x.y, y.y);
               }
-              mma_16816_bf16(o[4 * cp + 2 * c], pa[ks], ev[0], ev[1]);
-              mma_16816_bf16(o[4 * cp + 2 * c + 1], pa[ks], od[0], od[1]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_16816_bf16(o[nt][2 * cp + c], a, pb[ks][nt][0], pb[ks][nt][1]);
             }
           }
         }
@@ -424,37 +554,45 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
     // ---- the warps' parts of the tile become one
     const uint32_t ml = sb + L::ML;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-      if (q == 0) {
-        st_shared_f32(ml + ((warp * 16 + rq + 8 * x) * 2) * 4, m[x]);
-        st_shared_f32(ml + ((warp * 16 + rq + 8 * x) * 2 + 1) * 4, l[x]);
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+        if (kq == 0) {
+          const uint32_t at = ml + ((warp * L::R + 8 * nt + 2 * q + e) * 2) * 4;
+          st_shared_f32(at, m[nt][e]);
+          st_shared_f32(at + 4, l[nt][e]);
+        }
       }
-    }
     consumers_sync();
     const float* mls = (const float*)(smem_raw + (ml - smem_u32(smem_raw)));
     auto joined = [&](int r, float& M, float& Ls) {
       M = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kConsumers; ++i) M = fmaxf(M, mls[(i * 16 + r) * 2]);
+      for (int i = 0; i < kConsumers; ++i) M = fmaxf(M, mls[(i * L::R + r) * 2]);
       const float ref = M == -INFINITY ? 0.f : M;
       Ls = 0.f;
 #pragma unroll
-      for (int i = 0; i < kConsumers; ++i) Ls = fmaf(mls[(i * 16 + r) * 2 + 1], ex2(mls[(i * 16 + r) * 2] - ref), Ls);
+      for (int i = 0; i < kConsumers; ++i) Ls = fmaf(mls[(i * L::R + r) * 2 + 1], ex2(mls[(i * L::R + r) * 2] - ref), Ls);
     };
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      float M, Ls;
-      joined(rq + 8 * x, M, Ls);
-      const float a = ex2(m[x] - (M == -INFINITY ? 0.f : M));
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < OT; ++i) {
-        o[i][2 * x] *= a;
-        o[i][2 * x + 1] *= a;
+      for (int e = 0; e < 2; ++e) {
+        float M, Ls;
+        joined(8 * nt + 2 * q + e, M, Ls);
+        const float a = ex2(m[nt][e] - (M == -INFINITY ? 0.f : M));
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const float f = MX && ref_scale[i / 2] > 0 ? a * exp2i(ref_scale[i / 2] - 127) : a;
+          o[nt][i][e] *= f;
+          o[nt][i][2 + e] *= f;
+        }
       }
-    }
-    const int tid = threadIdx.x, jr = tid >> 3, jc = (tid & 7) * 4;  // row and columns this thread adds up
+    constexpr int CW = L::R / 4, PER = 32 / CW;  // columns a thread adds up in a round, threads of a row
+    const int tid = threadIdx.x, jr = tid / PER, jc = tid % PER * CW;
     const int tok = g.tile * t.tokens + jr / t.gsub, gh = gs0 + jr % t.gsub;
     const bool jrow_ok = jr < t.rows && tok < g.seq.lq && gh < p.group;
     float M, Ls;
@@ -465,32 +603,43 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
     const float* jb = (const float*)(smem_raw + (sb + L::JOIN - smem_u32(smem_raw)));
 #pragma unroll
     for (int rd = 0; rd < DV / 32; ++rd) {
-      const uint32_t mine = sb + L::JOIN + warp * 16 * L::JOIN_LD * 4;
+      const uint32_t mine = sb + L::JOIN + warp * L::R * L::JOIN_LD * 4;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = rq + 8 * (e >> 1);
-          // MXFP8 output tiles hold even and odd columns of 16
-          const int c = MX ? 16 * (i >> 1) + 4 * q + 2 * (e & 1) + (i & 1) : 8 * i + 2 * q + (e & 1);
-          st_shared_f32(mine + (r * L::JOIN_LD + c) * 4, o[4 * rd + i][e]);
-        }
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = 8 * nt + 2 * q + (e & 1);
+            // a tile's rows are columns in order; with MXFP8 rows kq, kq + 8 are columns 2 kq, 2 kq + 1
+            const int c = 16 * i + (MX ? 2 * kq + (e >> 1) : kq + 8 * (e >> 1));
+            st_shared_f32(mine + (r * L::JOIN_LD + c) * 4, o[nt][2 * rd + i][e]);
+          }
       consumers_sync();
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      float x[CW];
 #pragma unroll
-      for (int v = 0; v < kConsumers; ++v) {
-        const float4 a = *reinterpret_cast<const float4*>(jb + (v * 16 + jr) * L::JOIN_LD + jc);
-        x.x += a.x; x.y += a.y; x.z += a.z; x.w += a.w;
-      }
-      if (g.slot >= 0) {
-        if (jr < t.rows) *reinterpret_cast<float4*>(w.part_o + part_row * DV + 32 * rd + jc) = x;
-      } else if (jrow_ok) {
-        *reinterpret_cast<uint2*>((__nv_bfloat16*)p.o + out_row * DV + 32 * rd + jc) =
-            make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+      for (int c = 0; c < CW; ++c) x[c] = 0.f;
+#pragma unroll
+      for (int v = 0; v < kConsumers; ++v)
+#pragma unroll
+        for (int c = 0; c < CW; c += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(jb + (v * L::R + jr) * L::JOIN_LD + jc + c);
+          x[c] += y.x;
+          x[c + 1] += y.y;
+        }
+#pragma unroll
+      for (int c = 0; c < CW; c += 2) {
+        if (g.slot >= 0) {
+          if (jr < t.rows)
+            *reinterpret_cast<float2*>(w.part_o + part_row * DV + 32 * rd + jc + c) = make_float2(x[c], x[c + 1]);
+        } else if (jrow_ok) {
+          *reinterpret_cast<uint32_t*>((__nv_bfloat16*)p.o + out_row * DV + 32 * rd + jc + c) =
+              pack_bf16(x[c] * inv, x[c + 1] * inv);
+        }
       }
       consumers_sync();
     }
-    if ((tid & 7) == 0) {
+    if (tid % PER == 0) {
       if (g.slot >= 0) {
         if (jr < t.rows) {
           w.part_ml[2 * part_row] = M;
@@ -503,10 +652,10 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
   }
 }
 
-template <int DQK, int DV, int KIND>
+template <int DQK, int DV, int KIND, int NT>
 cudaError_t launch_t(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s) {
-  using L = Layout<DQK, DV, KIND>;
-  auto kern = paged_rows16_kernel<DQK, DV, KIND>;
+  using L = Layout<DQK, DV, KIND, NT>;
+  auto kern = paged_rows16_kernel<DQK, DV, KIND, NT>;
   cudaError_t e = kernel_setup((const void*)kern, kThreads, L::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t rows = (p.pages * p.heads_k) << p.page_shift;
@@ -518,11 +667,15 @@ cudaError_t launch_t(const Paged& p, const TileShape& t, int ctas, const PagedWs
   kern<<<ctas, kThreads, L::SMEM, s>>>(p, t, w, mk, mv);
   return cudaGetLastError();
 }
+template <int DQK, int DV, int KIND>
+cudaError_t launch_rows(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s) {
+  return t.rows <= 8 ? launch_t<DQK, DV, KIND, 1>(p, t, ctas, w, s) : launch_t<DQK, DV, KIND, 2>(p, t, ctas, w, s);
+}
 template <int KIND>
 cudaError_t launch_dims(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s) {
   if (p.dim_qk == 128)
-    return p.dim_v == 128 ? launch_t<128, 128, KIND>(p, t, ctas, w, s) : launch_t<128, 64, KIND>(p, t, ctas, w, s);
-  return p.dim_v == 128 ? launch_t<64, 128, KIND>(p, t, ctas, w, s) : launch_t<64, 64, KIND>(p, t, ctas, w, s);
+    return p.dim_v == 128 ? launch_rows<128, 128, KIND>(p, t, ctas, w, s) : launch_rows<128, 64, KIND>(p, t, ctas, w, s);
+  return p.dim_v == 128 ? launch_rows<64, 128, KIND>(p, t, ctas, w, s) : launch_rows<64, 64, KIND>(p, t, ctas, w, s);
 }
 
 }  // namespace

@@ -87,7 +87,7 @@ struct TileShape {
 constexpr int kMaxPagedCtas = 640, kMaxTcCtas = 160;
 // Keys of a block of the 16-row kernel.
 constexpr int paged_rows16_keys(int dim_qk, int dim_v, int kind) {
-  return kind == kCacheBf16 && dim_qk + dim_v > 192 ? 16 : 32;
+  return kind == kCacheBf16 && dim_qk + dim_v > 128 ? 16 : 32;
 }
 
 struct PagedWs {
