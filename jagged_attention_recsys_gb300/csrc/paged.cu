@@ -108,7 +108,6 @@ paged_plan_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
     w.hdr->status = bad ? JFA_ERR_BAD_OFFSETS : JFA_OK;
     w.hdr->n_ctas = ctas;
   }
-  if (tid < 60) w.hdr->zeros[tid] = 0;
   // little work goes to fewer CTAs, so that a share is worth its tile's fixed cost
   const int64_t n = max((int64_t)1, min((int64_t)ctas, W / t.share));
   for (int c = tid; c <= ctas; c += kPlanThreads) {

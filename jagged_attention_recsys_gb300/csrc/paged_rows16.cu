@@ -3,9 +3,9 @@
 //
 // Bound: HBM.  A key and its value are read once and meet at most 16 rows, 4 to 32 flops a
 // byte, so what counts is that loads never pause.  A CTA has one producer warp, which walks
-// the CTA's share of the work ahead of the others and fills a ring of stages (16 or 32
-// keys and their values each, by TMA; page table entries are looked up 32 at a time), and four consumer
-// warps.  Consecutive stages go to consecutive warps and a warp keeps its own running maximum,
+// the CTA's share of the work ahead of the others and fills a ring of stages (32 or 64 keys and
+// their values each, by TMA; page table entries are looked up 32 at a time), and four consumer
+// warps.  Two warps share a stage, half each, and a warp keeps its own running maximum,
 // sum and output, so the warps meet only at a tile's end, where they join through shared
 // memory while the producer already fills the ring with the next tile.
 //
@@ -21,11 +21,10 @@
 // at most 2^-39 of it), so the scores are fp16 products of codes, one block of 32 columns at a
 // time, and a block's scale multiplies its fp32 sum.  For the output the scales go to the
 // weights: a block of columns has a reference scale, the largest it met (O is kept in its
-// units), and the weights times scale / reference, at most 1, are rounded to fp16 (2^-12 of a
-// weight down to 2^-14, absolutely 2^-25 below) against fp16 codes.  A stage with a scale under
-// 2^-8 of its reference takes its values to bf16 instead (exact) and rounds the weights alone,
-// so that keys of small values keep their precision beside keys of large ones.  With every value
-// taken to bf16 an MXFP8 step ran at 4.0 TB/s, held by the conversions.
+// units), and the weights, rounded to fp16, times scale / reference, at most 1, meet fp16 codes
+// (2^-12 of a product of at least 2^-14, absolutely 2^-25 below).  A stage with a scale under
+// 2^-9 of its reference takes its values to bf16 instead (exact) and rounds the weights alone,
+// so that keys of small values keep their precision beside keys of large ones.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -40,23 +39,22 @@ namespace jfa {
 namespace {
 using namespace tc;
 
-constexpr int kConsumers = 4;
-constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleLog2 = 8.0f;
 
 template <int DQK, int DV, int KIND, int NT>
 struct Layout {
   static constexpr int R = 8 * NT;  // rows of a tile
+  static constexpr int kConsumers = 4, kThreads = 32 * (kConsumers + 1);
   static constexpr int E = KIND == kCacheMx ? 1 : 2;  // bytes of an element
-  // Keys of a stage: 32, or 16 where twelve stages would not fit otherwise.
-  static constexpr int kKeys = paged_rows16_keys(DQK, DV, KIND);
-  static constexpr uint32_t KB = kKeys * DQK * E, VB = kKeys * DV * E;
-  static constexpr uint32_t KS = KIND == kCacheMx ? kKeys * DQK / 32 : 0, VS = KIND == kCacheMx ? kKeys * DV / 32 : 0;
-  static constexpr uint32_t BYTES = KB + VB + KS + VS;  // of a stage's loads
+  // Keys of a stage, and of each of the two warps that share it.  A stage costs the producer
+  // about 850 cycles whatever its size, so at half the size an MXFP8 step ran at its pace.
+  static constexpr int kStage = paged_rows16_keys(DQK, DV, KIND), kKeys = kStage / 2;
+  static constexpr uint32_t KB = kStage * DQK * E, VB = kStage * DV * E;
+  static constexpr uint32_t KS = KIND == kCacheMx ? kStage * DQK / 32 : 0;
   static constexpr uint32_t STAGE = KB + VB;
-  static constexpr uint32_t SCALES = 256;  // a stage's scales (K at 0, V at 128)
-  static constexpr int CTAS = NT == 1 ? 3 : 2;  // of an SM
+  static constexpr uint32_t SCALES = 512;  // a stage's scales (K at 0, V at 256)
   static constexpr uint32_t LIMIT = NT == 1 ? 74 * 1024 + 512 : 113 * 1024;
   // in front: barriers, abort flag, statistics; then the join's buffer, the value scales as fp16
   // factors, the scales, the stages
@@ -66,13 +64,13 @@ struct Layout {
   static constexpr uint32_t FAC = JOIN + kConsumers * R * JOIN_LD * 4;  // [warps][blocks][32 keys] halves
   static constexpr uint32_t SCALE0 = FAC + (KS ? kConsumers * (DV / 32) * 64 : 0);
   static constexpr int NS_ = (LIMIT - SCALE0 - 1024) / (STAGE + (KS ? SCALES : 0));
-  // A multiple of the consumers, so that a stage is always the same warp's: fills land in any
-  // order, and a warp that came to a stage before another's previous fill of it had landed
-  // would take that fill's parity for its own.
-  static constexpr int NS = NS_ >= 16 ? 16 : NS_ / kConsumers * kConsumers;
+  // Even, so that a stage is always the same two warps': fills land in any order, and a warp that
+  // came to a stage before another's previous fill of it had landed would take that fill's
+  // parity for its own.
+  static constexpr int NS = (NS_ >= 16 ? 16 : NS_) / 2 * 2;
   static constexpr uint32_t TILES = (SCALE0 + (KS ? NS * SCALES : 0) + 1023) / 1024 * 1024;
   static constexpr uint32_t SMEM = TILES + NS * STAGE + 1024;  // 1 KB to align the base
-  static_assert(NS >= 8 && NS % kConsumers == 0 && SMEM <= LIMIT, "stages");
+  static_assert(NS >= 4 && SMEM <= LIMIT, "stages");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -88,14 +86,14 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 __device__ __forceinline__ void mma_16816_bf16(float (&c)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
       "%2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
       "%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -103,7 +101,7 @@ __device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint32_t* a, 
 }
 // c = a b, nothing added
 __device__ __forceinline__ void mma_16816_f16_zero(float (&c)[4], const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
       "%10, %10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
@@ -124,15 +122,17 @@ template <int B>
 __device__ __forceinline__ float scale_byte(uint32_t x) {
   return __uint_as_float((B < 3 ? x << (23 - 8 * B) : x >> 1) & 0x7f800000u);
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+// 16 bytes to shared memory, or zeros; and this thread's arrival once its copies have landed
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 // an 8 x 8 matrix of 16-bit values, transposed
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -140,8 +140,9 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+template <int THREADS>
 __device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
   uint32_t v;
@@ -153,18 +154,18 @@ __device__ __forceinline__ void st_shared_f32(uint32_t a, float x) {
 }
 // Byte of 16-byte chunk c of row `row` in a stage's tensor of D columns of E bytes: boxes of 128
 // bytes a row (bf16: 64 columns, stacked; MXFP8 at 128), or 64 bytes a row.
-template <int D, int E, int kKeys>
+template <int D, int E, int ROWS>
 __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
-  if constexpr (D * E >= 128) return (c >> 3) * (kKeys * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+  if constexpr (D * E >= 128) return (c >> 3) * (ROWS * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
   return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
 }
 
 template <int DQK, int DV, int KIND, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(Layout<DQK, DV, KIND, NT>::kThreads, NT == 1 ? 3 : 2)
 paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedWs w,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   using L = Layout<DQK, DV, KIND, NT>;
-  constexpr int E = L::E, NS = L::NS, kKeys = L::kKeys;
+  constexpr int E = L::E, NS = L::NS, kStage = L::kStage, kKeys = L::kKeys, kConsumers = L::kConsumers;
   constexpr bool MX = KIND == kCacheMx;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -174,8 +175,8 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(full + 8 * s, 1);
-      mbar_init(empty + 8 * s, 1);
+      mbar_init(full + 8 * s, MX ? 33 : 1);  // the TMA loads, and every producer lane's scales
+      mbar_init(empty + 8 * s, 2);
     }
     *abort = 0;
     fence_mbar_init();
@@ -192,14 +193,14 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
-    const int box = min(1 << p.page_shift, kKeys), per = kKeys / box;  // rows of a box, boxes of a stage
+    const int box = min(1 << p.page_shift, kStage), per = kStage / box;  // rows of a box, boxes of a stage
     const int none = (int)((p.pages * p.heads_k) << p.page_shift);    // behind the last row: read as zeros
     bool ok = true;
     while (ok && walk.next(p, t, g)) {
       const int head = g.unit / t.nsub;
       for (int i0 = g.blk0; ok && i0 < g.blk1; i0 += 32 / per) {
         // this lane's box of the next 32: its first row, or one behind the cache where it has no keys
-        const int pos = i0 * kKeys + lane * box;
+        const int pos = i0 * kStage + lane * box;
         int row = none;
         if (pos < g.seq.lk && i0 + lane / per < g.blk1) {
           const int page = paged_page(p, g.b, pos, status);
@@ -213,28 +214,33 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
             break;
           }
           const uint32_t tile = sb + L::TILES + st * L::STAGE, bar = full + 8 * st;
-          if (lane == 0) mbar_expect_tx(bar, L::BYTES);
+          if (lane == 0) mbar_expect_tx(bar, L::KB + L::VB);
           for (int s = 0; s < per; ++s) {
             const int r = __shfl_sync(0xffffffffu, row, i * per + s);
             if (lane == 0) {
 #pragma unroll
               for (int h = 0; h < (DQK * E + 127) / 128; ++h)
-                tma_load_2d(tile + h * kKeys * 128 + s * box * (DQK * E < 128 ? DQK * E : 128), &tm_k, h * (128 / E), r,
+                tma_load_2d(tile + h * kStage * 128 + s * box * (DQK * E < 128 ? DQK * E : 128), &tm_k, h * (128 / E), r,
                             bar);
 #pragma unroll
               for (int h = 0; h < (DV * E + 127) / 128; ++h)
-                tma_load_2d(tile + L::KB + h * kKeys * 128 + s * box * (DV * E < 128 ? DV * E : 128), &tm_v,
+                tma_load_2d(tile + L::KB + h * kStage * 128 + s * box * (DV * E < 128 ? DV * E : 128), &tm_v,
                             h * (128 / E), r, bar);
-              if constexpr (MX) {
-                // no row: scales of zero, from the header
-                const uint32_t sc = sb + L::SCALE0 + st * L::SCALES;
-                const uint8_t* zeros = reinterpret_cast<const uint8_t*>(w.hdr->zeros);
-                bulk_load(sc + s * box * (DQK / 32), r == none ? zeros : p.ks + (int64_t)r * (DQK / 32),
-                          box * (DQK / 32), bar);
-                bulk_load(sc + 128 + s * box * (DV / 32), r == none ? zeros : p.vs + (int64_t)r * (DV / 32),
-                          box * (DV / 32), bar);
-              }
             }
+          }
+          if constexpr (MX) {
+            // the scales, 16 bytes a lane: first the keys', then the values'; zeros for keys that
+            // are not there
+            constexpr int CK = kStage * (DQK / 32) / 16, CV = kStage * (DV / 32) / 16;
+            static_assert(CK + CV <= 32, "a piece a lane");
+            const bool val = lane >= CK;
+            const int c = val ? lane - CK : lane, nb = val ? DV / 32 : DQK / 32, key = c * 16 / nb;
+            const int r = __shfl_sync(0xffffffffu, row, i * per + min(key / box, per - 1));
+            const uint32_t sc = sb + L::SCALE0 + st * L::SCALES;
+            if (lane < CK + CV)
+              copy16(sc + (val ? 256 : 0) + c * 16,
+                     (val ? p.vs : p.ks) + (r == none ? 0 : ((int64_t)r + key % box) * nb), r != none);
+            copies_arrive(bar);
           }
         }
       }
@@ -315,25 +321,32 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
     for (int i = 0; i < NBV; ++i) ref_scale[i] = 0;
 
     for (int blk = g.blk0; blk < g.blk1; ++blk, ++cnt) {
-      if ((int)(cnt % kConsumers) != warp) continue;
+      if ((int)(cnt & 1) != warp >> 1) continue;
       const uint32_t st = cnt % NS;
       if (dead || !mbar_wait(full + 8 * st, (cnt / NS) & 1, abort, status)) {
         dead = true;
         continue;
       }
-      const uint32_t kt = sb + L::TILES + st * L::STAGE, vt = kt + L::KB, sc = sb + L::SCALE0 + st * L::SCALES;
-      const int k0 = blk * kKeys, nk = g.seq.lk - k0;
+      const uint32_t kt = sb + L::TILES + st * L::STAGE, vt = kt + L::KB;
+      const int rb = (warp & 1) * kKeys;  // this warp's rows of the stage
+      const uint32_t sck = sb + L::SCALE0 + st * L::SCALES + rb * NBK, scv = sb + L::SCALE0 + st * L::SCALES + 256 + rb * NBV;
+      const int k0 = blk * kStage + rb, nk = g.seq.lk - k0;
+      if (nk <= 0) {  // the sequence ends in the other half
+        if (lane == 0) mbar_arrive(empty + 8 * st);
+        continue;
+      }
       if (nk < kKeys) {
         // values behind the sequence's end may be anything: as zeros they meet zero weights
         for (int i = lane; i < kKeys * DV * E / 16; i += 32) {
-          const int row = DV * E >= 128 ? (i >> 3) % kKeys : i >> 2;
-          if (row >= nk) st_shared_v4(vt + 16 * i, 0u, 0u, 0u, 0u);
+          constexpr int per = DV * E >= 128 ? 8 : 4;  // pieces of 16 bytes in a row of a box
+          const int row = i / per % kKeys, half = i / (per * kKeys);
+          if (row >= nk) st_shared_v4(vt + half * kStage * 128 + (rb + row) * per * 16 + i % per * 16, 0u, 0u, 0u, 0u);
         }
         if constexpr (MX) {  // and their scales, which have to be numbers: the first key's
-          const uint32_t first = NBV == 4 ? ld_shared_u32(sc + 128) : ld_shared_u32(sc + 128) & 0xffffu;
+          const uint32_t first = NBV == 4 ? ld_shared_u32(scv) : ld_shared_u32(scv) & 0xffffu;
           if (lane >= nk) {
-            if constexpr (NBV == 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sc + 128 + lane * 4), "r"(first) : "memory");
-            else asm volatile("st.shared.u16 [%0], %1;" ::"r"(sc + 128 + lane * 2), "h"((uint16_t)first) : "memory");
+            if constexpr (NBV == 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(scv + lane * 4), "r"(first) : "memory");
+            else asm volatile("st.shared.u16 [%0], %1;" ::"r"(scv + lane * 2), "h"((uint16_t)first) : "memory");
           }
         }
         fence_proxy_async_smem();  // the stage's next loads come through the async proxy
@@ -349,23 +362,30 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
         for (int nt = 0; nt < NT; ++nt) s[ks][nt][0] = s[ks][nt][1] = s[ks][nt][2] = s[ks][nt][3] = 0.f;
         if constexpr (!MX) {
 #pragma unroll
-          for (int k = 0; k < DQK / 16; ++k) {
-            uint32_t a[4];
-            ldsm4(a, kt + chunk_at<DQK, E, kKeys>(ks * 16 + (mi & 1) * 8 + mr, 2 * k + (mi >> 1)));
+          for (int k4 = 0; k4 < DQK / 16; k4 += 4) {  // four loads on their way
+            uint32_t a[4][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_16816_bf16(s[ks][nt], a, qb[nt][k][0], qb[nt][k][1]);
+            for (int k = 0; k < 4; ++k)
+              ldsm4(a[k], kt + chunk_at<DQK, E, kStage>(rb + ks * 16 + (mi & 1) * 8 + mr, 2 * (k4 + k) + (mi >> 1)));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_16816_bf16(s[ks][nt], a[k], qb[nt][k4 + k][0], qb[nt][k4 + k][1]);
           }
         } else {
           uint32_t sk[2];  // scales of keys kq, kq + 8
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int key = ks * 16 + kq + 8 * i;
-            if constexpr (NBK == 4) sk[i] = ld_shared_u32(sc + key * 4);
-            else sk[i] = ld_shared_u32(sc + (key & ~1) * 2) >> (16 * (key & 1));
+            if constexpr (NBK == 4) sk[i] = ld_shared_u32(sck + key * 4);
+            else sk[i] = ld_shared_u32(sck + (key & ~1) * 2) >> (16 * (key & 1));
           }
+          uint32_t kb[NBK][4];  // the group's codes, all on their way before the first is needed
+#pragma unroll
+          for (int c2 = 0; c2 < NBK; ++c2)
+            ldsm4(kb[c2], kt + chunk_at<DQK, E, kStage>(rb + ks * 16 + (mi & 1) * 8 + mr, 2 * c2 + (mi >> 1)));
           auto block = [&](int c2, float f0, float f1) {  // a block: two chunks of 16 columns
-            uint32_t b[4];
-            ldsm4(b, kt + chunk_at<DQK, E, kKeys>(ks * 16 + (mi & 1) * 8 + mr, 2 * c2 + (mi >> 1)));
+            const uint32_t (&b)[4] = kb[c2];
             uint32_t a[2][4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -394,44 +414,52 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
         }
       }
       // ---- weights
-      bool moved = false;
-      float mn[NT][2], ref[NT][2];
+      // A row's reference moves, with its sum and output, only when a score passes it by 2^8: then
+      // alone the lanes exchange their maxima.
+      bool need = false;
+      float top[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int seen = min(limit[nt][e], g.seq.lk) - k0;  // keys of this stage the row sees
-          float top = -INFINITY;
+          top[nt][e] = -INFINITY;
 #pragma unroll
           for (int ks = 0; ks < G16; ++ks)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float& v = s[ks][nt][2 * h + e];
               v = ks * 16 + 8 * h + kq < seen ? v * cs[nt][e] : -INFINITY;
-              top = fmaxf(top, v);
+              top[nt][e] = fmaxf(top[nt][e], v);
             }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          mn[nt][e] = fmaxf(m[nt][e], top);
-          ref[nt][e] = mn[nt][e] == -INFINITY ? 0.f : mn[nt][e];
-          moved |= mn[nt][e] != m[nt][e];
+          need |= top[nt][e] > m[nt][e] + kRescaleLog2;  // m = -inf: any key
         }
-      if (__any_sync(0xffffffffu, moved)) {
+      if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float a = ex2(m[nt][e] - ref[nt][e]);  // m = -inf: 0
-            l[nt][e] *= a;
+            float x = top[nt][e];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            if (x > m[nt][e] + kRescaleLog2) {
+              const float a = ex2(m[nt][e] - x);  // m = -inf: 0
+              l[nt][e] *= a;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              o[nt][i][e] *= a;
-              o[nt][i][2 + e] *= a;
+              for (int i = 0; i < MT; ++i) {
+                o[nt][i][e] *= a;
+                o[nt][i][2 + e] *= a;
+              }
+              m[nt][e] = x;
             }
-            m[nt][e] = mn[nt][e];
           }
       }
+      float ref[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) ref[nt][e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
 #pragma unroll
       for (int ks = 0; ks < G16; ++ks)
 #pragma unroll
@@ -445,27 +473,36 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
       // mixed) or, against fp16 codes, to fp16.
       bool wide = false;  // MXFP8: a scale far under its block's reference
       if constexpr (MX) {
-        const uint32_t mine = NBV == 4 ? ld_shared_u32(sc + 128 + lane * 4)
-                                       : (ld_shared_u32(sc + 128 + (lane & ~1) * 2) >> (16 * (lane & 1))) & 0xffffu;
+        const uint32_t mine = NBV == 4 ? ld_shared_u32(scv + lane * 4)
+                                       : (ld_shared_u32(scv + (lane & ~1) * 2) >> (16 * (lane & 1))) & 0xffffu;
         const uint32_t fac = sb + L::FAC + warp * NBV * 64;
+        bool out = false;  // a scale above its reference, or far under it
+#pragma unroll
+        for (int i = 0; i < NBV; ++i) out |= (uint32_t)(ref_scale[i] - (int)((mine >> (8 * i)) & 255)) > 9u;
+        if (__any_sync(0xffffffffu, out)) {
+#pragma unroll
+          for (int i = 0; i < NBV; ++i) {
+            const int e = min((mine >> (8 * i)) & 255, 254u);
+            const int most = __reduce_max_sync(0xffffffffu, e), least = __reduce_min_sync(0xffffffffu, e);
+            if (most > ref_scale[i]) {  // O of the block goes to the new units, with a step to spare
+              const int to = min(most + 1, 254);
+              const float f = ref_scale[i] == 0 ? 1.f : exp2i(max(ref_scale[i] - to, -126));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  o[nt][2 * i][k] *= f;
+                  o[nt][2 * i + 1][k] *= f;
+                }
+              ref_scale[i] = to;
+            }
+            wide |= least < ref_scale[i] - 9;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < NBV; ++i) {
-          const int e = min((mine >> (8 * i)) & 255, 254u);
-          const int top = __reduce_max_sync(0xffffffffu, e), low = __reduce_min_sync(0xffffffffu, e);
-          if (top > ref_scale[i]) {  // O of the block goes to the new units
-            const float f = ref_scale[i] == 0 ? 1.f : exp2i(max(ref_scale[i] - top, -126));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                o[nt][2 * i][k] *= f;
-                o[nt][2 * i + 1][k] *= f;
-              }
-            ref_scale[i] = top;
-          }
-          wide |= low < ref_scale[i] - 8;
-          // the key's scale over the reference, 2^-8 to 1 as a half
-          const uint16_t h = (uint16_t)((e - ref_scale[i] + 15) << 10);
+          // the key's scale over the reference, 2^-9 to 1 as a half
+          const uint16_t h = (uint16_t)(((int)((mine >> (8 * i)) & 255) - ref_scale[i] + 15) << 10);
           asm volatile("st.shared.u16 [%0], %1;" ::"r"(fac + (i * 32 + lane) * 2), "h"(h) : "memory");
         }
         __syncwarp();
@@ -485,19 +522,30 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
       for (int ks = 0; ks < G16; ++ks) {
         if constexpr (!MX) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint32_t a[4];
-            ldsm4t(a, vt + chunk_at<DV, E, kKeys>(ks * 16 + (mi >> 1) * 8 + mr, 2 * mt + (mi & 1)));
+          for (int m4 = 0; m4 < MT; m4 += 4) {
+            uint32_t a[4][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_16816_bf16(o[nt][mt], a, pb[ks][nt][0], pb[ks][nt][1]);
+            for (int mt = 0; mt < 4; ++mt)
+              ldsm4t(a[mt], vt + chunk_at<DV, E, kStage>(rb + ks * 16 + (mi >> 1) * 8 + mr, 2 * (m4 + mt) + (mi & 1)));
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_16816_bf16(o[nt][m4 + mt], a[mt], pb[ks][nt][0], pb[ks][nt][1]);
           }
         } else if (!wide) {
           const uint32_t fac = sb + L::FAC + warp * NBV * 64 + (ks * 16 + 2 * q) * 2;
+          uint32_t vb[NBV][4], fv[NBV][2];
+#pragma unroll
+          for (int cp = 0; cp < NBV; ++cp) {
+            ldsm4t(vb[cp], vt + chunk_at<DV, E, kStage>(rb + ks * 16 + (mi & 1) * 8 + mr, 2 * cp + (mi >> 1)));
+            fv[cp][0] = ld_shared_u32(fac + cp * 64);
+            fv[cp][1] = ld_shared_u32(fac + cp * 64 + 16);
+          }
 #pragma unroll
           for (int cp = 0; cp < NBV; ++cp) {  // two chunks of 16 columns: one block
-            uint32_t b[4], pw[NT][2];
-            ldsm4t(b, vt + chunk_at<DV, E, kKeys>(ks * 16 + (mi & 1) * 8 + mr, 2 * cp + (mi >> 1)));
-            const uint32_t f0 = ld_shared_u32(fac + cp * 64), f1 = ld_shared_u32(fac + cp * 64 + 16);
+            const uint32_t (&b)[4] = vb[cp];
+            const uint32_t f0 = fv[cp][0], f1 = fv[cp][1];
+            uint32_t pw[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               pw[nt][0] = hmul2(pb[ks][nt][0], f0);
@@ -518,7 +566,7 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
 #pragma unroll
           for (int cp = 0; cp < NBV; ++cp) {
             uint32_t b[4];
-            ldsm4t(b, vt + chunk_at<DV, E, kKeys>(ks * 16 + (mi & 1) * 8 + mr, 2 * cp + (mi >> 1)));
+            ldsm4t(b, vt + chunk_at<DV, E, kStage>(rb + ks * 16 + (mi & 1) * 8 + mr, 2 * cp + (mi >> 1)));
             // 2^(127 - reference), of which 2^-127 is no normal number, and its product with the
             // scale 2^127 is exact all the same
             const float unit = ref_scale[cp] == 254 ? __uint_as_float(0x00400000u) : exp2i(127 - ref_scale[cp]);
@@ -526,8 +574,8 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int key = ks * 16 + 2 * q + (i & 1) + 8 * (i >> 1);
-              const uint32_t x = NBV == 4 ? ld_shared_u32(sc + 128 + key * 4)
-                                          : ld_shared_u32(sc + 128 + (key & ~1) * 2) >> (16 * (key & 1));
+              const uint32_t x = NBV == 4 ? ld_shared_u32(scv + key * 4)
+                                          : ld_shared_u32(scv + (key & ~1) * 2) >> (16 * (key & 1));
               f[i] = unit * __uint_as_float(((x >> (8 * cp)) & 255u) << 23);
             }
 #pragma unroll
@@ -566,7 +614,7 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
           st_shared_f32(at + 4, l[nt][e]);
         }
       }
-    consumers_sync();
+    consumers_sync<32 * kConsumers>();
     const float* mls = (const float*)(smem_raw + (ml - smem_u32(smem_raw)));
     auto joined = [&](int r, float& M, float& Ls) {
       M = -INFINITY;
@@ -615,7 +663,7 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
             const int c = 16 * i + (MX ? 2 * kq + (e >> 1) : kq + 8 * (e >> 1));
             st_shared_f32(mine + (r * L::JOIN_LD + c) * 4, o[nt][2 * rd + i][e]);
           }
-      consumers_sync();
+      consumers_sync<32 * kConsumers>();
       float x[CW];
 #pragma unroll
       for (int c = 0; c < CW; ++c) x[c] = 0.f;
@@ -637,7 +685,7 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
               pack_bf16(x[c] * inv, x[c + 1] * inv);
         }
       }
-      consumers_sync();
+      consumers_sync<32 * kConsumers>();
     }
     if (tid % PER == 0) {
       if (g.slot >= 0) {
@@ -656,15 +704,15 @@ template <int DQK, int DV, int KIND, int NT>
 cudaError_t launch_t(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s) {
   using L = Layout<DQK, DV, KIND, NT>;
   auto kern = paged_rows16_kernel<DQK, DV, KIND, NT>;
-  cudaError_t e = kernel_setup((const void*)kern, kThreads, L::SMEM);
+  cudaError_t e = kernel_setup((const void*)kern, L::kThreads, L::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t rows = (p.pages * p.heads_k) << p.page_shift;
-  const int box = (1 << p.page_shift) < L::kKeys ? (1 << p.page_shift) : L::kKeys;
+  const int box = (1 << p.page_shift) < L::kStage ? (1 << p.page_shift) : L::kStage;
   CUtensorMap mk, mv;
   if (!make_rows_map(&mk, p.kc, L::E, rows, DQK, DQK * L::E < 128 ? DQK : 128 / L::E, box) ||
       !make_rows_map(&mv, p.vc, L::E, rows, DV, DV * L::E < 128 ? DV : 128 / L::E, box))
     return cudaErrorInvalidValue;
-  kern<<<ctas, kThreads, L::SMEM, s>>>(p, t, w, mk, mv);
+  kern<<<ctas, L::kThreads, L::SMEM, s>>>(p, t, w, mk, mv);
   return cudaGetLastError();
 }
 template <int DQK, int DV, int KIND>

@@ -70,8 +70,7 @@ struct __align__(16) PagedPos {
 struct PagedHeader {
   int status;
   int n_ctas;  // CTAs the work is cut for
-  int pad[2];
-  int zeros[60];  // stays zero: scales of keys that are not there
+  int pad[62];
 };
 static_assert(sizeof(PagedHeader) == 256, "workspace header");
 
@@ -87,7 +86,7 @@ struct TileShape {
 constexpr int kMaxPagedCtas = 640, kMaxTcCtas = 160;
 // Keys of a block of the 16-row kernel.
 constexpr int paged_rows16_keys(int dim_qk, int dim_v, int kind) {
-  return kind == kCacheBf16 && dim_qk + dim_v > 128 ? 16 : 32;
+  return kind == kCacheBf16 && dim_qk + dim_v > 128 ? 32 : 64;
 }
 
 struct PagedWs {
