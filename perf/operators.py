@@ -305,8 +305,9 @@ def _own(s):
     if case["op"] == "paged":
         return list(jfa.jfa_paged_fwd(s["q"], cache, s["table"], s["offs"], s["lens"], ws=s["ws"]))
     if case["dir"] == "read":
-        return list(jfa.jfa_cache_read(cache, s["table"], s["offs"], s["lens"], sum(_lengths(case)[0]), dtype=_dtype(case),
-                                       ws=s["ws"]))
+        if "total" not in s:  # the program knows how many rows it asks for
+            s["total"] = sum(_lengths(case)[0])
+        return list(jfa.jfa_cache_read(cache, s["table"], s["offs"], s["lens"], s["total"], dtype=_dtype(case), ws=s["ws"]))
     jfa.jfa_cache_write(s["k"], s["v"], cache, s["table"], s["offs"], s["lens"], ws=s["ws"])
     return _written(s)
 
