@@ -140,6 +140,23 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// The producer warp runs converged and one elected lane issues (from inside a branch of one lane
+// an issue costs more).
+__device__ __forceinline__ void expect_elected(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n.reg .pred e;\n.reg .b64 st;\nelect.sync _|e, 0xffffffff;\n"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void load_elected(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(
+          dst),
+      "l"((uint64_t)map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
 template <int THREADS>
 __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
@@ -214,19 +231,18 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
             break;
           }
           const uint32_t tile = sb + L::TILES + st * L::STAGE, bar = full + 8 * st;
-          if (lane == 0) mbar_expect_tx(bar, L::KB + L::VB);
+          __syncwarp();
+          expect_elected(bar, L::KB + L::VB);
           for (int s = 0; s < per; ++s) {
             const int r = __shfl_sync(0xffffffffu, row, i * per + s);
-            if (lane == 0) {
 #pragma unroll
-              for (int h = 0; h < (DQK * E + 127) / 128; ++h)
-                tma_load_2d(tile + h * kStage * 128 + s * box * (DQK * E < 128 ? DQK * E : 128), &tm_k, h * (128 / E), r,
-                            bar);
+            for (int h = 0; h < (DQK * E + 127) / 128; ++h)
+              load_elected(tile + h * kStage * 128 + s * box * (DQK * E < 128 ? DQK * E : 128), &tm_k, h * (128 / E), r,
+                           bar);
 #pragma unroll
-              for (int h = 0; h < (DV * E + 127) / 128; ++h)
-                tma_load_2d(tile + L::KB + h * kStage * 128 + s * box * (DV * E < 128 ? DV * E : 128), &tm_v,
-                            h * (128 / E), r, bar);
-            }
+            for (int h = 0; h < (DV * E + 127) / 128; ++h)
+              load_elected(tile + L::KB + h * kStage * 128 + s * box * (DV * E < 128 ? DV * E : 128), &tm_v,
+                           h * (128 / E), r, bar);
           }
           if constexpr (MX) {
             // the scales, 16 bytes a lane: first the keys', then the values'; zeros for keys that
