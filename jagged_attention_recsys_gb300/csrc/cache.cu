@@ -12,7 +12,8 @@
 // lanes first look up a token each (sequence, position, page: a chain of dependent loads that
 // would otherwise be paid token by token), then the warp goes through them.  A lane takes 16
 // columns (two lanes share a block's maximum by one shuffle), consecutive over the token's heads,
-// with up to two pieces of the keys and two of the values in flight.
+// with a piece of the keys and one of the values in flight; 32 warps an SM do the rest (two pieces
+// each and 24 warps: 157 us for 118 K tokens of 8 heads of 128, so 142).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -24,6 +25,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtas = 4;  // of an SM
 
 // W columns of a row as they lie in memory
 template <typename T, int W>
@@ -70,6 +72,18 @@ struct Raw {
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < N; ++i) q[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  // 16 codes times their scale
+  __device__ __forceinline__ void set_mx(const uint4& c, float f) {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    float x[W];
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j) {
+      const float2 y = e4m3_values((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+      x[2 * j] = y.x * f;
+      x[2 * j + 1] = y.y * f;
+    }
+    set(x);
   }
 };
 
@@ -137,11 +151,10 @@ __device__ __forceinline__ void write_mx(const Raw<T, 16>& raw, uint8_t* codes, 
 }
 
 template <typename T, int KIND, bool WRITE>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, kCtas)
 cache_kernel(const __grid_constant__ Paged p, T* k_out, T* v_out, PagedHeader* hdr, int run, int parts, int planned) {
   constexpr bool MX = KIND == kCacheMx;
   constexpr int W = MX ? 16 : 8;
-  constexpr int U = W * sizeof(T) > 32 ? 1 : 2;  // pieces of each tensor in flight
   // a plan that found the batch invalid: nothing is computed (page errors do not stop the call,
   // so the check does not depend on what other CTAs have met so far)
   if (planned && *(volatile int*)&hdr->status == (int)JFA_ERR_BAD_OFFSETS) return;
@@ -178,76 +191,52 @@ cache_kernel(const __grid_constant__ Paged p, T* k_out, T* v_out, PagedHeader* h
       const int64_t t = t0 + i, r0 = __shfl_sync(0xffffffffu, row, i);
       const bool has = r0 >= 0;
       if (WRITE && !has) continue;
+      // the token's rows of head 0, a head's step from there on, and the token's own rows
+      constexpr int E = MX ? 1 : (int)sizeof(T);
+      uint8_t *kc = (uint8_t*)p.kc + r0 * p.dim_qk * E, *vc = (uint8_t*)p.vc + r0 * p.dim_v * E;
+      uint8_t *ks = p.ks + r0 * (p.dim_qk >> 5), *vs = p.vs + r0 * (p.dim_v >> 5);
+      const uint32_t hk = (uint32_t)p.dim_qk * E << p.page_shift, hv = (uint32_t)p.dim_v * E << p.page_shift;
+      const uint32_t hks = (uint32_t)(p.dim_qk >> 5) << p.page_shift, hvs = (uint32_t)(p.dim_v >> 5) << p.page_shift;
+      const T *kin = (const T*)p.k + t * p.sk, *vin = (const T*)p.v + t * p.sv;
+      T *kout = k_out + t * ck * W, *vout = v_out + t * cv * W;
       Piece<W> pk(k0 + lane, perk), pv(v0 + lane, perv);
-      for (int step = 0; k0 + 32 * step < k1 || v0 + 32 * step < v1; step += U) {
-        Raw<T, W> rk[U], rv[U];
-        uint4 code_k[MX ? U : 1], code_v[MX ? U : 1];
-        float fk[MX ? U : 1], fv[MX ? U : 1];
-        const Piece<W> sk = pk, sv = pv;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t rowk = r0 + ((int64_t)pk.head << p.page_shift), rowv = r0 + ((int64_t)pv.head << p.page_shift);
-          const bool okk = pk.c < k1, okv = pv.c < v1;
-          if constexpr (WRITE) {
-            rk[u].zero();
-            rv[u].zero();
-            if (okk) rk[u].load((const T*)p.k + t * p.sk + (int64_t)pk.c * W);
-            if (okv) rv[u].load((const T*)p.v + t * p.sv + (int64_t)pv.c * W);
-          } else if constexpr (MX) {
-            code_k[u] = code_v[u] = make_uint4(0u, 0u, 0u, 0u);
-            fk[u] = fv[u] = 0.f;
+      for (; pk.c - lane < k1 || pv.c - lane < v1; pk.next(perk, dhk, dck), pv.next(perv, dhv, dcv)) {
+        const bool okk = pk.c < k1, okv = pv.c < v1;
+        uint8_t *ck_at = kc + (uint64_t)pk.head * hk + pk.col * W * E, *cv_at = vc + (uint64_t)pv.head * hv + pv.col * W * E;
+        uint8_t *sk_at = ks + (uint64_t)pk.head * hks + (pk.col >> 1), *sv_at = vs + (uint64_t)pv.head * hvs + (pv.col >> 1);
+        Raw<T, W> rk, rv;
+        rk.zero();
+        rv.zero();
+        if constexpr (WRITE) {
+          if (okk) rk.load(kin + (uint32_t)pk.c * W);
+          if (okv) rv.load(vin + (uint32_t)pv.c * W);
+          if constexpr (MX) {
+            write_mx<T>(rk, ck_at, sk_at, pk.col, okk);
+            write_mx<T>(rv, cv_at, sv_at, pv.col, okv);
+          } else {
+            if (okk) rk.store((T*)ck_at);
+            if (okv) rv.store((T*)cv_at);
+          }
+        } else {
+          if constexpr (MX) {
+            uint4 code_k = make_uint4(0u, 0u, 0u, 0u), code_v = code_k;
+            float fk = 0.f, fv = 0.f;
             if (okk && has) {
-              code_k[u] = __ldcs(reinterpret_cast<const uint4*>((const uint8_t*)p.kc + rowk * p.dim_qk) + pk.col);
-              fk[u] = __uint_as_float((uint32_t)__ldg(p.ks + rowk * (p.dim_qk >> 5) + (pk.col >> 1)) << 23);
+              code_k = __ldcs(reinterpret_cast<const uint4*>(ck_at));
+              fk = __uint_as_float((uint32_t)__ldg(sk_at) << 23);
             }
             if (okv && has) {
-              code_v[u] = __ldcs(reinterpret_cast<const uint4*>((const uint8_t*)p.vc + rowv * p.dim_v) + pv.col);
-              fv[u] = __uint_as_float((uint32_t)__ldg(p.vs + rowv * (p.dim_v >> 5) + (pv.col >> 1)) << 23);
+              code_v = __ldcs(reinterpret_cast<const uint4*>(cv_at));
+              fv = __uint_as_float((uint32_t)__ldg(sv_at) << 23);
             }
+            rk.set_mx(code_k, fk);
+            rv.set_mx(code_v, fv);
           } else {
-            rk[u].zero();
-            rv[u].zero();
-            if (okk && has) rk[u].load((const T*)p.kc + rowk * p.dim_qk + pk.col * W);
-            if (okv && has) rv[u].load((const T*)p.vc + rowv * p.dim_v + pv.col * W);
+            if (okk && has) rk.load((const T*)ck_at);
+            if (okv && has) rv.load((const T*)cv_at);
           }
-          pk.next(perk, dhk, dck);
-          pv.next(perv, dhv, dcv);
-        }
-        pk = sk;
-        pv = sv;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t rowk = r0 + ((int64_t)pk.head << p.page_shift), rowv = r0 + ((int64_t)pv.head << p.page_shift);
-          const bool okk = pk.c < k1, okv = pv.c < v1;
-          if constexpr (WRITE && MX) {
-            write_mx<T>(rk[u], (uint8_t*)p.kc + rowk * p.dim_qk + pk.col * W,
-                        p.ks + rowk * (p.dim_qk >> 5) + (pk.col >> 1), pk.col, okk);
-            write_mx<T>(rv[u], (uint8_t*)p.vc + rowv * p.dim_v + pv.col * W,
-                        p.vs + rowv * (p.dim_v >> 5) + (pv.col >> 1), pv.col, okv);
-          } else if constexpr (WRITE) {
-            if (okk) rk[u].store((T*)p.kc + rowk * p.dim_qk + pk.col * W);
-            if (okv) rv[u].store((T*)p.vc + rowv * p.dim_v + pv.col * W);
-          } else {
-            if constexpr (MX) {
-              auto values = [](const uint4& c, float f, Raw<T, W>& out) {
-                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-                float x[W];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const float2 y = e4m3_values((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
-                  x[2 * j] = y.x * f;
-                  x[2 * j + 1] = y.y * f;
-                }
-                out.set(x);
-              };
-              values(code_k[u], fk[u], rk[u]);
-              values(code_v[u], fv[u], rv[u]);
-            }
-            if (okk) rk[u].store(k_out + t * ck * W + (int64_t)pk.c * W);
-            if (okv) rv[u].store(v_out + t * cv * W + (int64_t)pv.c * W);
-          }
-          pk.next(perk, dhk, dck);
-          pv.next(perv, dhv, dcv);
+          if (okk) rk.store(kout + (uint32_t)pk.c * W);
+          if (okv) rv.store(vout + (uint32_t)pv.c * W);
         }
       }
     }
@@ -256,17 +245,18 @@ cache_kernel(const __grid_constant__ Paged p, T* k_out, T* v_out, PagedHeader* h
 
 template <typename T, int KIND, bool WRITE>
 cudaError_t launch_t(const Paged& p, void* k, void* v, PagedHeader* hdr, int planned, cudaStream_t s) {
-  // Runs of tokens to about two a warp of a full GPU; with fewer tokens than warps, several
-  // warps a token instead (a serving step of 256 tokens would leave most SMs without work).
+  // Runs of up to 32 tokens, as long as lets every warp of a full GPU take the same number of them
+  // (2.03 runs a warp cost three rounds); with fewer tokens than warps, several warps a token
+  // instead (a serving step of 256 tokens would leave most SMs without work).
   constexpr int W = KIND == kCacheMx ? 16 : 8;
-  const int64_t warps = (int64_t)num_sms() * kWarps * 3;
-  int64_t run = p.total_q / (2 * warps);
-  run = run < 1 ? 1 : run > 32 ? 32 : run;
+  const int64_t warps = (int64_t)num_sms() * kWarps * kCtas;
+  const int64_t rounds = (p.total_q + 32 * warps - 1) / (32 * warps);
+  const int64_t run = (p.total_q + rounds * warps - 1) / (rounds * warps);
   const int most = (p.heads_k * ((p.dim_qk > p.dim_v ? p.dim_qk : p.dim_v) / W) + 31) / 32;
   int64_t parts = run > 1 ? 1 : (warps + p.total_q - 1) / p.total_q;
   if (parts > most) parts = most;
   int64_t grid = ((p.total_q + run - 1) / run * parts + kWarps - 1) / kWarps;
-  const int64_t cap = (int64_t)num_sms() * 3;
+  const int64_t cap = (int64_t)num_sms() * kCtas;
   if (grid > cap) grid = cap;
   cache_kernel<T, KIND, WRITE><<<(unsigned)grid, kThreads, 0, s>>>(p, (T*)k, (T*)v, hdr, (int)run, (int)parts, planned);
   return cudaGetLastError();

@@ -337,13 +337,14 @@ __device__ __forceinline__ void write_partial(const Slot16& acc, const Slot& sl,
   __syncthreads();
 }
 
+// One row of each tensor in flight a lane and three CTAs an SM: more warps hide more here than more
+// rows a warp (two rows at two CTAs: 445 us for 65539 tokens of 40 heads of 128, so 389 us).
 template <typename T, int LAYOUT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
 norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs p, const FastShape g, float* part_ws) {
   extern __shared__ float red[];
   __shared__ __align__(16) float tables[kWarps][2 * kMaxPairs];
   __shared__ __align__(16) float weights[2][kMaxNormDim];
-  constexpr int U = Raw16<T>::kBatch / 2;  // two tensors in flight
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < 2 * p.dim; i += kThreads) {
     const float* w = p.side[i >= p.dim].w;
@@ -362,70 +363,67 @@ norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs p, const FastShape g, 
     const NormRopeSide& sd = p.side[side];
     if (sd.heads == 0) continue;
     const int steps = (sd.heads + per - 1) / per;
-    Slot16 acc, w;
+    Slot16 acc;
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc.a[j] = acc.b[j] = make_float2(0.f, 0.f);
-    weights16<LAYOUT>(w, weights[side], sl);
     for (int64_t task = (int64_t)blockIdx.x * kWarps + warp; task < tasks; task += nw) {
       const int64_t t = task / g.parts;
       const int part = (int)(task - t * g.parts);
       const int s0 = (int)((int64_t)steps * part / g.parts), s1 = (int)((int64_t)steps * (part + 1) / g.parts);
       bool fresh = p.rot > 0;
-      for (int sb = s0; sb < s1; sb += U) {
-        Raw16<T> rx[U], rd[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int h = (sb + u) * per + sub;
-          if (sb + u < s1 && h < sd.heads && lane_ok) {
-            const int64_t o = (int64_t)h * p.dim;
-            const T* dy = (const T*)sd.dy + t * sd.sdy + o;
-            rd[u].load(dy + sl.a, dy + sl.b);
-            if (p.norm) {
-              const T* x = (const T*)sd.x + t * sd.sx + o;
-              rx[u].load(x + sl.a, x + sl.b);
-            }
-          } else {
-            rd[u].zero();
-            rx[u].zero();
+      for (int step = s0; step < s1; ++step) {
+        const int h = step * per + sub;
+        const bool ok = h < sd.heads && lane_ok;
+        Raw16<T> rx, rd;
+        rd.zero();
+        rx.zero();
+        if (ok) {
+          const int64_t o = (int64_t)h * p.dim;
+          const T* dy = (const T*)sd.dy + t * sd.sdy + o;
+          rd.load(dy + sl.a, dy + sl.b);
+          if (p.norm) {
+            const T* x = (const T*)sd.x + t * sd.sx + o;
+            rx.load(x + sl.a, x + sl.b);
           }
         }
-        if (fresh) {
+        if (fresh) {  // under the first row's loads
           turns.table(tb, p, __ldg(p.pos + t), lane);
           fresh = false;
         }
+        Slot16 d;
+        rd.template get<LAYOUT>(d);
+        if (sl.rot) turn16<true>(d, tb, sl.pair0);
+        if (p.norm) {
+          Slot16 v, w;
+          rx.template get<LAYOUT>(v);
+          weights16<LAYOUT>(w, weights[side], sl);
+          float2 ss = make_float2(0.f, 0.f), ux = ss;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (sb + u >= s1) break;
-          const int h = (sb + u) * per + sub;
-          Slot16 d;
-          rd[u].template get<LAYOUT>(d);
-          if (sl.rot) turn16<true>(d, tb, sl.pair0);
-          if (p.norm) {
-            Slot16 v;
-            rx[u].template get<LAYOUT>(v);
-            float2 ss = make_float2(0.f, 0.f), ux = ss;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              ss = tc::ffma2(v.a[j], v.a[j], ss);
-              ss = tc::ffma2(v.b[j], v.b[j], ss);
-              ux = tc::ffma2(tc::fmul2(d.a[j], w.a[j]), v.a[j], ux);
-              ux = tc::ffma2(tc::fmul2(d.b[j], w.b[j]), v.b[j], ux);
-            }
-            const float r = rsqrtf(fmaf(group_sum(ss.x + ss.y, g.group), p.inv_dim, p.eps));
-            const float k = group_sum(ux.x + ux.y, g.group) * p.inv_dim * r * r;
-            const float2 rr = make_float2(r, r), kn = make_float2(-k, -k);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              acc.a[j] = tc::ffma2(d.a[j], tc::fmul2(v.a[j], rr), acc.a[j]);
-              acc.b[j] = tc::ffma2(d.b[j], tc::fmul2(v.b[j], rr), acc.b[j]);
-              d.a[j] = tc::fmul2(rr, tc::ffma2(v.a[j], kn, tc::fmul2(d.a[j], w.a[j])));
-              d.b[j] = tc::fmul2(rr, tc::ffma2(v.b[j], kn, tc::fmul2(d.b[j], w.b[j])));
-            }
+          for (int j = 0; j < 4; ++j) {
+            ss = tc::ffma2(v.a[j], v.a[j], ss);
+            ss = tc::ffma2(v.b[j], v.b[j], ss);
+            ux = tc::ffma2(tc::fmul2(d.a[j], w.a[j]), v.a[j], ux);
+            ux = tc::ffma2(tc::fmul2(d.b[j], w.b[j]), v.b[j], ux);
           }
-          if (h < sd.heads && lane_ok) {
-            T* dx = (T*)sd.out + t * sd.sout + (int64_t)h * p.dim;
-            Raw16<T>::template store<LAYOUT>(dx + sl.a, dx + sl.b, d);
+          float s2 = ss.x + ss.y, su = ux.x + ux.y;
+          for (int m = g.group >> 1; m > 0; m >>= 1) {  // side by side: one latency
+            s2 += __shfl_xor_sync(0xffffffffu, s2, m);
+            su += __shfl_xor_sync(0xffffffffu, su, m);
           }
+          const float r = rsqrtf(fmaf(s2, p.inv_dim, p.eps));
+          const float k = su * p.inv_dim * r * r;
+          const float2 rr = make_float2(r, r), kn = make_float2(-k, -k);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc.a[j] = tc::ffma2(d.a[j], tc::fmul2(v.a[j], rr), acc.a[j]);
+            acc.b[j] = tc::ffma2(d.b[j], tc::fmul2(v.b[j], rr), acc.b[j]);
+            d.a[j] = tc::fmul2(rr, tc::ffma2(v.a[j], kn, tc::fmul2(d.a[j], w.a[j])));
+            d.b[j] = tc::fmul2(rr, tc::ffma2(v.b[j], kn, tc::fmul2(d.b[j], w.b[j])));
+          }
+        }
+        if (ok) {
+          T* dx = (T*)sd.out + t * sd.sout + (int64_t)h * p.dim;
+          Raw16<T>::template store<LAYOUT>(dx + sl.a, dx + sl.b, d);
         }
       }
     }
@@ -619,7 +617,7 @@ cudaError_t bwd_t(const NormRopeArgs& a, float* part, cudaStream_t s) {
   FastShape g;
   int grid;
   if (fast_shape(a, sizeof(T), &g)) {
-    grid = grid_for(a.tokens * g.parts, 2, kNormRopeParts);
+    grid = grid_for(a.tokens * g.parts, 3, kNormRopeParts);
     const size_t smem = sizeof(float) * kWarps * a.dim;
     if (a.layout == JFA_ROPE_HALVES)
       norm_rope_bwd_kernel<T, JFA_ROPE_HALVES><<<grid, kThreads, smem, s>>>(a, g, part);
