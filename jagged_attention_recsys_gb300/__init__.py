@@ -502,12 +502,17 @@ def jfa_block_bwd(q, k, v, o, lse, dout, offs, *, scale=None, causal=False, dq=N
 
 
 # ----------------------------------------------------------------------------- shared checks
+# The handle alone: building a torch Stream around it costs 2.5 us a call.
+_current_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on(device, stream):
     """The raw stream of a call whose tensors live on ``device``, which must be current."""
     if device.index != torch.cuda.current_device():
         raise ValueError("tensors are on %s, which is not the current device" % device)
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_raw_stream(device.index)
     if stream.device != device:
         raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device, device))
     return stream.cuda_stream

@@ -13,7 +13,10 @@
 //
 // The cost of the tiles in front of tile t of a sequence is a closed form (an arithmetic
 // series under the causal mask), so the plan needs one scan over the sequences and one binary
-// search per CTA, and no list of tiles.
+// search per CTA, and no list of tiles.  Batches of at most kPlanInCta sequences need no launch
+// for it unless the caller asks for a plan: each CTA scans the lengths itself (1 us of loads and
+// shuffles) and the join gathers the CTAs' statuses.  A step of four users over short caches
+// takes 24 us a call instead of 33 by that and lighter argument handling.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -30,30 +33,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSmemSeqs = 4096;  // scan kept in shared memory up to this batch
 
-struct SeqCost {
-  int64_t off, lk, tiles, s, over;
-  int causal;
-  // cost of the tiles in front of tile t, t <= tiles - 1
-  __device__ int64_t before(int64_t t) const {
-    if (!causal) return t * (over + lk);
-    // tile u sees max(0, off + (u + 1) s) keys
-    int64_t u0 = off < 0 ? (-off) / s : 0;  // tiles that see nothing
-    if (u0 > t) u0 = t;
-    return t * over + (t - u0) * off + s * ((t * (t + 1) - u0 * (u0 + 1)) / 2);
-  }
-  __device__ int64_t total() const { return tiles == 0 ? 0 : before(tiles - 1) + over + lk; }
-};
-__device__ SeqCost seq_cost(const Paged& p, const TileShape& t, int64_t lq, int64_t lk) {
-  SeqCost c;
-  c.off = lk - lq;
-  c.lk = lk;
-  c.s = t.tokens;
-  c.tiles = (lq + t.tokens - 1) / t.tokens;
-  c.over = t.overhead;
-  c.causal = p.causal;
-  return c;
-}
-
 __global__ void __launch_bounds__(kPlanThreads)
 paged_plan_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, const PagedWs w) {
   extern __shared__ int64_t smem_cum[];
@@ -65,20 +44,16 @@ paged_plan_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
   int64_t* cum = B <= kPlanSmemSeqs ? smem_cum : w.cum;
   if (tid == 0) {
     carry_s = 0;
-    bad_s = p.offs[0] != 0 || p.offs[B] != p.total_q;
+    bad_s = B == 0 && p.offs[0] != 0;
     cum[0] = 0;
   }
   __syncthreads();
-  const int64_t units = (int64_t)p.heads_k * t.nsub;
   for (int64_t base = 0; base < B; base += kPlanThreads) {
     const int64_t b = base + tid;
-    int64_t x = 0;
-    if (b < B) {
-      const int64_t a = p.offs[b], e = p.offs[b + 1], lk = p.lens[b];
-      if (a < 0 || e < a || e > p.total_q || lk < 0 || lk > ((int64_t)p.width << p.page_shift))
-        bad_s = 1;
-      else
-        x = units * seq_cost(p, t, e - a, lk).total();
+    int64_t x = b < B ? checked_cost(p, t, b) : 0;
+    if (x < 0) {
+      bad_s = 1;
+      x = 0;
     }
     for (int m = 1; m < 32; m <<= 1) {
       const int64_t y = __shfl_up_sync(0xffffffffu, x, m);
@@ -108,42 +83,7 @@ paged_plan_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
     w.hdr->status = bad ? JFA_ERR_BAD_OFFSETS : JFA_OK;
     w.hdr->n_ctas = ctas;
   }
-  // little work goes to fewer CTAs, so that a share is worth its tile's fixed cost
-  const int64_t n = max((int64_t)1, min((int64_t)ctas, W / t.share));
-  for (int c = tid; c <= ctas; c += kPlanThreads) {
-    PagedPos r{(int)B, 0, 0, 0};  // the end; a bad batch begins there
-    const int64_t x = W / n * c + W % n * c / n;
-    if (!bad && c < n && x < W) {
-      int64_t lo = 0, hi = B - 1;
-      while (lo < hi) {  // the first b with cum[b + 1] > x
-        const int64_t m = (lo + hi) >> 1;
-        if (cum[m + 1] > x) hi = m;
-        else lo = m + 1;
-      }
-      const SeqCost sc = seq_cost(p, t, p.offs[lo + 1] - p.offs[lo], p.lens[lo]);
-      const int64_t S = sc.total(), y = x - cum[lo];
-      const int64_t unit = y / S, z = y - unit * S;
-      int64_t tl = 0, th = sc.tiles - 1;
-      while (tl < th) {  // the last tile with before(tile) <= z
-        const int64_t m = (tl + th + 1) >> 1;
-        if (sc.before(m) <= z) tl = m;
-        else th = m - 1;
-      }
-      const int64_t vis = tl == sc.tiles - 1 || !sc.causal ? sc.lk : max((int64_t)0, sc.off + (tl + 1) * sc.s);
-      const int64_t nb = (vis + t.keys - 1) / t.keys;
-      const int64_t d = z - sc.before(tl) - sc.over;
-      int64_t blk = d <= 0 ? 0 : (d + t.keys / 2) / t.keys;
-      r.b = (int)lo;
-      r.unit = (int)unit;
-      r.tile = (int)tl;
-      r.blk = (int)blk;
-      if (blk > 0 && blk >= nb) {  // the cut falls on the tile's end
-        r.tile = (int)tl + 1;
-        r.blk = 0;
-      }
-    }
-    w.pos[c] = r;
-  }
+  for (int c = tid; c <= ctas; c += kPlanThreads) w.pos[c] = paged_cut(p, t, ctas, c, cum, W, bad);
 }
 
 // ------------------------------------------------------------------- the CUDA-core kernel
@@ -174,7 +114,7 @@ __device__ __forceinline__ float cache_value(const void* codes, const uint8_t* s
 template <typename T, int KIND>
 __global__ void __launch_bounds__(kSimtThreads)
 paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedWs w) {
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   const int dq = p.dim_qk, dv = p.dim_v, ldq = dq + 1, ldv = dv + 1;
   float* Q = sm;                  // [16][dq + 1]
   float* K = Q + kRows * ldq;     // [32][dq + 1]
@@ -182,8 +122,10 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
   float* S = V + kKeys * ldv;     // [16][33]
   __shared__ int64_t row_of[kKeys];
   const int tid = threadIdx.x, r = tid >> 3, sub = tid & 7;
+  __shared__ PagedPos share[2];
+  int* status = paged_share(p, t, w, share, sm);
   PagedWalk walk;
-  walk.init(w.pos, blockIdx.x);
+  walk.init(share);
   PagedSegment g;
   while (walk.next(p, t, g)) {
     const int head_k = g.unit / t.nsub, gs0 = (g.unit % t.nsub) * t.gsub;
@@ -209,7 +151,7 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
       if (tid < kKeys) {
         int64_t row = -1;
         if (tid < nk) {
-          const int page = paged_page(p, g.b, k0 + tid, &w.hdr->status);
+          const int page = paged_page(p, g.b, k0 + tid, status);
           if (page >= 0) row = paged_row(p, page, head_k, k0 + tid);
         }
         row_of[tid] = row;
@@ -293,8 +235,15 @@ template <typename T>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, const PagedWs w) {
   const int c = blockIdx.x, lane = threadIdx.x & 31;
+  if (w.ctas > 0 && c == 0 && blockIdx.y == 0 && threadIdx.x < 32) {  // the CTAs' errors: the call's
+    int st = 0;
+    for (int i = lane; i < w.ctas; i += 32) st = max(st, w.cta_status[i]);
+    st = __reduce_max_sync(0xffffffffu, st);
+    if (lane == 0) w.hdr->status = st;
+  }
   const PagedPos end = w.pos[c + 1];
-  if (end.blk == 0) return;  // no tile is cut here
+  // no tile is cut here, or the plan is another batch's
+  if (end.blk == 0 || end.b >= p.batch) return;
   const PagedPos at = w.pos[c];
   auto same = [&](const PagedPos& x) { return x.b == end.b && x.unit == end.unit && x.tile == end.tile; };
   if (same(at) && at.blk > 0) return;  // the tile begins in an earlier CTA's share
@@ -339,7 +288,8 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
 template <typename T, int KIND>
 cudaError_t simt_t(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s) {
   auto kern = paged_simt_kernel<T, KIND>;
-  const size_t smem = sizeof(float) * ((kRows + kKeys) * (p.dim_qk + 1) + kKeys * (p.dim_v + 1) + kRows * 33);
+  size_t smem = sizeof(float) * ((kRows + kKeys) * (p.dim_qk + 1) + kKeys * (p.dim_v + 1) + kRows * 33);
+  if (smem < kPlanScratch) smem = kPlanScratch;
   constexpr size_t most = sizeof(float) * ((kRows + kKeys) * 129 + kKeys * 129 + kRows * 33);
   cudaError_t e = kernel_setup((const void*)kern, kSimtThreads, most);
   if (e != cudaSuccess) return e;
@@ -404,6 +354,8 @@ size_t paged_layout(const Paged& p, void* base, PagedWs* out) {
   off = up256(off + sizeof(PagedPos) * (kMaxPagedCtas + 2));
   w.cum = (int64_t*)(b + off);
   off = up256(off + sizeof(int64_t) * (size_t)(p.batch + 1));
+  w.cta_status = (int*)(b + off);
+  off = up256(off + sizeof(int) * kMaxPagedCtas);
   constexpr size_t rows = 2 * (kMaxPagedCtas * 16 > kMaxTcCtas * 256 ? kMaxPagedCtas * 16 : kMaxTcCtas * 256);
   w.part_ml = (float*)(b + off);
   off = up256(off + sizeof(float) * 2 * rows);

@@ -33,6 +33,131 @@ __device__ __forceinline__ int tile_keys(const Paged& p, const TileShape& t, con
   return last < 0 ? 0 : (int)last;
 }
 
+// ------------------------------------------------------------------- cutting the work
+struct SeqCost {
+  int64_t off, lk, tiles, s, over;
+  int causal;
+  // cost of the tiles in front of tile t, t <= tiles - 1
+  __device__ int64_t before(int64_t t) const {
+    if (!causal) return t * (over + lk);
+    // tile u sees max(0, off + (u + 1) s) keys
+    int64_t u0 = off < 0 ? (-off) / s : 0;  // tiles that see nothing
+    if (u0 > t) u0 = t;
+    return t * over + (t - u0) * off + s * ((t * (t + 1) - u0 * (u0 + 1)) / 2);
+  }
+  __device__ int64_t total() const { return tiles == 0 ? 0 : before(tiles - 1) + over + lk; }
+};
+__device__ __forceinline__ SeqCost seq_cost(const Paged& p, const TileShape& t, int64_t lq, int64_t lk) {
+  SeqCost c;
+  c.off = lk - lq;
+  c.lk = lk;
+  c.s = t.tokens;
+  c.tiles = (lq + t.tokens - 1) / t.tokens;
+  c.over = t.overhead;
+  c.causal = p.causal;
+  return c;
+}
+
+// Cost of sequence b in all its units, or -1: the arrays do not describe a batch.
+__device__ __forceinline__ int64_t checked_cost(const Paged& p, const TileShape& t, int64_t b) {
+  const int64_t a = __ldg(p.offs + b), e = __ldg(p.offs + b + 1), lk = __ldg(p.lens + b);
+  if (a < 0 || e < a || e > p.total_q || lk < 0 || lk > ((int64_t)p.width << p.page_shift) || (b == 0 && a != 0) ||
+      (b == p.batch - 1 && e != p.total_q))
+    return -1;
+  return (int64_t)p.heads_k * t.nsub * seq_cost(p, t, e - a, lk).total();
+}
+
+// Where CTA c of `ctas` begins (c = ctas: the end); cum[b]: cost of the sequences before b, in all
+// W = cum[B].  Little work goes to fewer CTAs, so that a share is worth its tile's fixed cost.
+__device__ __forceinline__ PagedPos paged_cut(const Paged& p, const TileShape& t, int ctas, int c, const int64_t* cum,
+                                              int64_t W, bool bad) {
+  const int64_t n = max((int64_t)1, min((int64_t)ctas, W / t.share));
+  PagedPos r{(int)p.batch, 0, 0, 0};  // the end; a bad batch begins there
+  const int64_t x = W / n * c + W % n * c / n;
+  if (bad || c >= n || x >= W) return r;
+  int64_t lo = 0, hi = p.batch - 1;
+  while (lo < hi) {  // the first b with cum[b + 1] > x
+    const int64_t m = (lo + hi) >> 1;
+    if (cum[m + 1] > x) hi = m;
+    else lo = m + 1;
+  }
+  const SeqCost sc = seq_cost(p, t, __ldg(p.offs + lo + 1) - __ldg(p.offs + lo), __ldg(p.lens + lo));
+  const int64_t S = sc.total(), y = x - cum[lo];
+  const int64_t unit = y / S, z = y - unit * S;
+  int64_t tl = 0, th = sc.tiles - 1;
+  while (tl < th) {  // the last tile with before(tile) <= z
+    const int64_t m = (tl + th + 1) >> 1;
+    if (sc.before(m) <= z) tl = m;
+    else th = m - 1;
+  }
+  const int64_t vis = tl == sc.tiles - 1 || !sc.causal ? sc.lk : max((int64_t)0, sc.off + (tl + 1) * sc.s);
+  const int64_t nb = (vis + t.keys - 1) / t.keys;
+  const int64_t d = z - sc.before(tl) - sc.over;
+  const int64_t blk = d <= 0 ? 0 : (d + t.keys / 2) / t.keys;
+  r.b = (int)lo;
+  r.unit = (int)unit;
+  r.tile = (int)tl;
+  r.blk = (int)blk;
+  if (blk > 0 && blk >= nb) {  // the cut falls on the tile's end
+    r.tile = (int)tl + 1;
+    r.blk = 0;
+  }
+  return r;
+}
+
+// A CTA's share, [pos[0], pos[1]), in shared memory.  With w.ctas > 0 there is no plan (a batch of
+// at most kPlanInCta sequences): every CTA scans the batch by itself, in `scratch` (at least
+// kPlanScratch bytes), and leaves its cut and its status in the workspace for the join.  All
+// threads of the CTA call it (at least 128), ahead of any other use of scratch.  Returns
+// where the CTA records errors.
+__device__ __forceinline__ int* paged_share(const Paged& p, const TileShape& t, const PagedWs& w, PagedPos* pos,
+                                            void* scratch) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
+  if (w.ctas == 0) {
+    if (tid < 2) pos[tid] = w.pos[c + tid];
+    __syncthreads();
+    return &w.hdr->status;
+  }
+  constexpr int kThreads = 128, kEach = kPlanInCta / kThreads;  // threads that scan, sequences of each
+  int64_t* cum = (int64_t*)scratch;      // [kPlanInCta + 1]
+  int64_t* sums = cum + kPlanInCta + 1;  // [kThreads / 32]
+  int64_t cost[kEach], x = 0;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int b = tid * kEach + i;
+    cost[i] = tid < kThreads && b < p.batch ? checked_cost(p, t, b) : 0;
+    bad |= cost[i] < 0;
+    x += cost[i];
+  }
+  bad = __syncthreads_or(bad) != 0;
+  int64_t before = x;
+  if (tid < kThreads) {
+    for (int m = 1; m < 32; m <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, before, m);
+      if (lane >= m) before += y;
+    }
+    if (lane == 31) sums[warp] = before;
+    before -= x;
+  }
+  __syncthreads();
+  if (tid < kThreads) {
+    for (int i = 0; i < warp; ++i) before += sums[i];
+    if (tid == 0) cum[0] = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) cum[tid * kEach + i + 1] = before += cost[i];
+  }
+  __syncthreads();
+  if (tid < 2) {
+    pos[tid] = paged_cut(p, t, w.ctas, c + tid, cum, cum[p.batch], bad);
+    if (tid == 0 || c == w.ctas - 1) w.pos[c + tid] = pos[tid];
+    if (tid == 0) w.cta_status[c] = bad ? JFA_ERR_BAD_OFFSETS : JFA_OK;
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // scratch may be TMA's from here on
+  __syncthreads();
+  return w.cta_status + c;
+}
+
 // Walks the segments of a CTA's share: [blk0, blk1) of a tile's nb key blocks.
 struct PagedSegment {
   int b, unit, tile, blk0, blk1, nb;
@@ -43,17 +168,16 @@ struct PagedWalk {
   PagedPos at, end;
   PagedSeq seq;
   bool fresh;
-  __device__ __forceinline__ void init(const PagedPos* pos, int cta) {
-    const int4* q = reinterpret_cast<const int4*>(pos + cta);
-    const int4 a = __ldg(q), e = __ldg(q + 1);
-    at = PagedPos{a.x, a.y, a.z, a.w};
-    end = PagedPos{e.x, e.y, e.z, e.w};
+  __device__ __forceinline__ void init(const PagedPos* share) {  // [begin, end)
+    at = share[0];
+    end = share[1];
     fresh = true;
   }
   __device__ __forceinline__ bool next(const Paged& p, const TileShape& t, PagedSegment& s) {
     const int units = p.heads_k * t.nsub;
     for (;;) {
-      if (at.b > end.b || at.b >= p.batch) return false;
+      // (what a plan of another batch may hold stays inside the arrays of this one)
+      if (at.b > end.b || at.b >= p.batch || at.unit >= units) return false;
       if (fresh) {
         seq = paged_seq(p, t, at.b);
         fresh = false;
@@ -77,8 +201,8 @@ struct PagedWalk {
       s.tile = at.tile;
       s.seq = seq;
       s.nb = (tile_keys(p, t, seq, at.tile) + t.keys - 1) / t.keys;
-      s.blk0 = at.blk;
-      s.blk1 = same ? end.blk : s.nb;
+      s.blk0 = min(at.blk, s.nb);
+      s.blk1 = same ? min(end.blk, s.nb) : s.nb;
       s.slot = s.blk0 > 0 ? 0 : s.blk1 < s.nb ? 1 : -1;
       ++at.tile;
       at.blk = 0;

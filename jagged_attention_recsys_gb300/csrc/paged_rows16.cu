@@ -188,7 +188,9 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
   const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t full = sb, empty = sb + 8 * NS;
   volatile int* abort = (volatile int*)(smem_raw + (sb - smem_u32(smem_raw)) + 16 * NS);
-  int* status = &w.hdr->status;
+  // in the stages' place, before any load
+  PagedPos* share = reinterpret_cast<PagedPos*>(smem_raw + (sb - smem_u32(smem_raw)) + L::ML - 32);
+  int* status = paged_share(p, t, w, share, smem_raw + (sb - smem_u32(smem_raw)) + L::TILES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -200,7 +202,7 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
   }
   __syncthreads();
   PagedWalk walk;
-  walk.init(w.pos, blockIdx.x);
+  walk.init(share);
   PagedSegment g;
   uint32_t cnt = 0;  // stages so far
 

@@ -69,7 +69,7 @@ enum : uint32_t {
   B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PFULL = 6, B_OFULL = 8, B_OEMPTY = 10, B_XCH = 12, B_DRAIN = 13,
   B_FULL = 15, B_EMPTY = 23, B_RFULL = 31, B_REMPTY = 35, B_VTAIL = 39, B_TURN = 47, B_COUNT = 49
 };
-static_assert(8 * B_COUNT + 8 <= 1024, "front");
+static_assert(8 * B_COUNT + 8 <= 1024 - 32, "front: barriers, then the share");
 constexpr uint32_t T_S = 0, T_O = 256;
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -137,7 +137,8 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sb = (raw + 1023u) & ~1023u;
   uint8_t* const sp = smem_raw + (sb - raw);
-  int* status = &w.hdr->status;
+  PagedPos* share = reinterpret_cast<PagedPos*>(sp + L::XCH - 32);
+  int* status = paged_share(p, t, w, share, sp + L::TILE0);  // in the queries' place, before any load
   auto bar = [&](uint32_t i) { return sb + 8u * i; };
   uint32_t* tmem_slot = (uint32_t*)(sp + 8 * B_COUNT);
   volatile int* abort = (volatile int*)(sp + 8 * B_COUNT + 4);
@@ -180,7 +181,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
   if (warp == kLoader) {
     // ---------------------------------------------------------------- loads
     PagedWalk walk;
-    walk.init(w.pos, blockIdx.x);
+    walk.init(share);
     PagedSegment g;
     if (lane == 0) {
       tma_prefetch_desc(&tm_q);
@@ -263,7 +264,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
   } else if (warp == kIssuerA || warp == kIssuerB) {
     // ---------------------------------------------------------------- products of one stream
     PagedWalk walk;
-    walk.init(w.pos, blockIdx.x);
+    walk.init(share);
     PagedSegment g;
     constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, 0, 0), idesc_o = idesc_bf16(128, DV, 0, 1);
     const int x = warp == kIssuerB;
@@ -352,7 +353,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
     // ---------------------------------------------------------------- ends of sequences
     if constexpr (!MX) {
       PagedWalk walk;
-      walk.init(w.pos, blockIdx.x);
+      walk.init(share);
       PagedSegment g;
       uint32_t it = 0, phase = 0;  // phase: a bit a stage
       bool ok = true;
@@ -379,7 +380,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
     // ---------------------------------------------------------------- softmax and epilogue
     more_registers<MX ? 168 : 208>();
     PagedWalk walk;
-    walk.init(w.pos, blockIdx.x);
+    walk.init(share);
     PagedSegment g;
     const int x = warp >> 2;
     const int r = 32 * (warp & 3) + lane;  // TMEM lane: row of the MMA tile
@@ -544,7 +545,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
     few_registers<40>();
     if constexpr (MX) {
       PagedWalk walk;
-      walk.init(w.pos, blockIdx.x);
+      walk.init(share);
       PagedSegment g;
       const int row = threadIdx.x & 127, part = (threadIdx.x - 384) >> 7;  // key of the block, half of its columns
       uint32_t it = 0;

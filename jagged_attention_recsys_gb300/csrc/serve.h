@@ -89,7 +89,14 @@ constexpr int paged_rows16_keys(int dim_qk, int dim_v, int kind) {
   return kind == kCacheBf16 && dim_qk + dim_v > 128 ? 32 : 64;
 }
 
+// Batches that every CTA of the attention scans by itself, so that an unplanned call needs no plan
+// launch (4 us of the 15 that a step of four users takes); and the scratch it takes.
+constexpr int kPlanInCta = 512;
+constexpr int kPlanScratch = 8 * (kPlanInCta + 1 + 4);
+
 struct PagedWs {
+  int ctas;         // 0: pos holds a plan; else the number of CTAs, which cut the work themselves
+  int* cta_status;  // [n_ctas] errors of CTAs without a plan, for the join
   PagedHeader* hdr;
   PagedPos* pos;   // [n_ctas + 1]
   int64_t* cum;    // [B + 1] cost of the sequences before b

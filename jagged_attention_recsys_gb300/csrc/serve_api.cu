@@ -320,10 +320,13 @@ jfa_status jfa_paged_fwd(const jfa_paged_params* p, const void* q, const void* k
   r.lse = lse;
   cudaStream_t s = (cudaStream_t)stream;
   const int kernel = paged_kernel(r, p->dtype);
-  if (!(p->flags & JFA_PLANNED) && (st = plan_paged(r, kernel, w, s)) != JFA_OK) return st;
+  const int ctas = paged_ctas(r, kernel);
+  if (!(p->flags & JFA_PLANNED)) {
+    if (p->total_q > 0 && p->batch <= kPlanInCta) w.ctas = ctas;
+    else if ((st = plan_paged(r, kernel, w, s)) != JFA_OK) return st;
+  }
   if (p->total_q == 0) return JFA_OK;
   const TileShape shape = paged_shape(r, kernel);
-  const int ctas = paged_ctas(r, kernel);
   Timed t(JFA_KERNEL_PAGED, s);
   st = cu(kernel == kPagedTc       ? launch_paged_tc(r, shape, ctas, w, s)
           : kernel == kPagedRows16 ? launch_paged_rows16(r, shape, ctas, w, s)
