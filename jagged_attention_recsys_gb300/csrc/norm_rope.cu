@@ -21,7 +21,7 @@
 //    CTA adds its lanes in a fixed order and writes one partial, a second kernel adds the
 //    partials in order: no atomics, the same bits every time on one GPU.
 // Rows that do not divide into slots (dim or rotated columns not multiples of 16, pointers
-// or strides not multiples of 16 bytes) take the *_any kernels: one warp a row, single
+// or strides not multiples of an access, 16 bytes in bf16 and 32 in fp32) take the *_any kernels: one warp a row, single
 // values.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -93,15 +93,25 @@ struct Raw16<__nv_bfloat16> {
     __stcs(reinterpret_cast<uint4*>(pb), make_uint4(w[4], w[5], w[6], w[7]));
   }
 };
+// 32 bytes in one access: a lane's two 16-byte halves would be half a sector each.
+__device__ __forceinline__ void load32(float4* q, const float* x) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(q[0].x), "=f"(q[0].y), "=f"(q[0].z), "=f"(q[0].w), "=f"(q[1].x), "=f"(q[1].y), "=f"(q[1].z),
+                 "=f"(q[1].w)
+               : "l"(x));
+}
+__device__ __forceinline__ void store32(float* x, const float4* q) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(x), "f"(q[0].x), "f"(q[0].y),
+               "f"(q[0].z), "f"(q[0].w), "f"(q[1].x), "f"(q[1].y), "f"(q[1].z), "f"(q[1].w)
+               : "memory");
+}
 template <>
 struct Raw16<float> {
   static constexpr int kBatch = 2;
   float4 q[4];
   __device__ void load(const float* pa, const float* pb) {
-    q[0] = __ldcs(reinterpret_cast<const float4*>(pa));
-    q[1] = __ldcs(reinterpret_cast<const float4*>(pa) + 1);
-    q[2] = __ldcs(reinterpret_cast<const float4*>(pb));
-    q[3] = __ldcs(reinterpret_cast<const float4*>(pb) + 1);
+    load32(q, pa);
+    load32(q + 2, pb);
   }
   __device__ void zero() { q[0] = q[1] = q[2] = q[3] = make_float4(0.f, 0.f, 0.f, 0.f); }
   template <int LAYOUT>
@@ -131,10 +141,8 @@ struct Raw16<float> {
         w[j] = make_float4(s.a[j].x, s.b[j].x, s.a[j].y, s.b[j].y);
       }
     }
-    __stcs(reinterpret_cast<float4*>(pa), w[0]);
-    __stcs(reinterpret_cast<float4*>(pa) + 1, w[1]);
-    __stcs(reinterpret_cast<float4*>(pb), w[2]);
-    __stcs(reinterpret_cast<float4*>(pb) + 1, w[3]);
+    store32(pa, w);
+    store32(pb, w + 2);
   }
 };
 
@@ -569,11 +577,12 @@ norm_rope_dw_kernel(const float* __restrict__ part, int parts, int dim, float* d
 }
 
 bool fast_shape(const NormRopeArgs& a, size_t e, FastShape* g) {
+  const size_t unit = 8 * e;  // bytes of an access
   if (a.dim % V != 0 || a.rot % V != 0) return false;
   for (const NormRopeSide& s : a.side) {
     if (s.heads == 0) continue;
-    if (((uintptr_t)s.x | (uintptr_t)s.dy | (uintptr_t)s.out) & 15) return false;
-    if ((s.sx * e) % 16 || (s.sdy * e) % 16 || (s.sout * e) % 16) return false;
+    if (((uintptr_t)s.x | (uintptr_t)s.dy | (uintptr_t)s.out) & (unit - 1)) return false;
+    if ((s.sx * e) % unit || (s.sdy * e) % unit || (s.sout * e) % unit) return false;
   }
   g->slots = a.dim / V;
   g->group = 1;
