@@ -12,8 +12,9 @@
 // lanes first look up a token each (sequence, position, page: a chain of dependent loads that
 // would otherwise be paid token by token), then the warp goes through them.  A lane takes 16
 // columns (two lanes share a block's maximum by one shuffle), consecutive over the token's heads,
-// with a piece of the keys and one of the values in flight; 32 warps an SM do the rest (two pieces
-// each and 24 warps: 157 us for 118 K tokens of 8 heads of 128, so 142).
+// with a piece of the keys and one of the values in flight; 24 (write) or 32 warps an SM do the
+// rest (two pieces each: 157 us for a write of 118 K tokens of 8 heads of 128, so 145).  Measured,
+// bf16 rows to MXFP8 pages and to bf16 ones: 145 us, 5.1 TB/s; back: 63 us, 4.4 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -25,7 +26,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtas = 4;  // of an SM
+// CTAs of an SM: a write's conversion to MXFP8 spills at four (154 us, so 145); a read wants the
+// loads in flight (three: 68 us, so 63)
+template <bool WRITE>
+constexpr int kCtas = WRITE ? 3 : 4;
 
 // W columns of a row as they lie in memory
 template <typename T, int W>
@@ -151,7 +155,7 @@ __device__ __forceinline__ void write_mx(const Raw<T, 16>& raw, uint8_t* codes, 
 }
 
 template <typename T, int KIND, bool WRITE>
-__global__ void __launch_bounds__(kThreads, kCtas)
+__global__ void __launch_bounds__(kThreads, kCtas<WRITE>)
 cache_kernel(const __grid_constant__ Paged p, T* k_out, T* v_out, PagedHeader* hdr, int run, int parts, int planned) {
   constexpr bool MX = KIND == kCacheMx;
   constexpr int W = MX ? 16 : 8;
@@ -249,14 +253,14 @@ cudaError_t launch_t(const Paged& p, void* k, void* v, PagedHeader* hdr, int pla
   // (2.03 runs a warp cost three rounds); with fewer tokens than warps, several warps a token
   // instead (a serving step of 256 tokens would leave most SMs without work).
   constexpr int W = KIND == kCacheMx ? 16 : 8;
-  const int64_t warps = (int64_t)num_sms() * kWarps * kCtas;
+  const int64_t warps = (int64_t)num_sms() * kWarps * kCtas<WRITE>;
   const int64_t rounds = (p.total_q + 32 * warps - 1) / (32 * warps);
   const int64_t run = (p.total_q + rounds * warps - 1) / (rounds * warps);
   const int most = (p.heads_k * ((p.dim_qk > p.dim_v ? p.dim_qk : p.dim_v) / W) + 31) / 32;
   int64_t parts = run > 1 ? 1 : (warps + p.total_q - 1) / p.total_q;
   if (parts > most) parts = most;
   int64_t grid = ((p.total_q + run - 1) / run * parts + kWarps - 1) / kWarps;
-  const int64_t cap = (int64_t)num_sms() * kCtas;
+  const int64_t cap = (int64_t)num_sms() * kCtas<WRITE>;
   if (grid > cap) grid = cap;
   cache_kernel<T, KIND, WRITE><<<(unsigned)grid, kThreads, 0, s>>>(p, (T*)k, (T*)v, hdr, (int)run, (int)parts, planned);
   return cudaGetLastError();
