@@ -326,11 +326,12 @@ jfa_status jfa_block_rope_bwd(const jfa_params* p, const void* q, const void* k,
  * (strides stride_dq, stride_dk) those of q, k; dwq, dwk (fp32 [D], or NULL: not wanted)
  * the weights', summed over tokens and heads in a fixed order without atomics (bitwise
  * reproducible on one GPU).  The row's r is recomputed from q, k.  dq may be dyq or q
- * with the same stride.  q, k may be NULL when norm = 0.  No tokens: dwq, dwk are zeroed.
+ * with the same stride.  q, k may be NULL when norm = 0.  Without tokens, or heads of its
+ * tensor, dwq or dwk is zeroed.
  *
  * Values are fp32 or bf16 (dtype), pointers aligned to a value; pointers and strides of
- * whole 16 bytes with dim and rope.dim multiples of 16 take the fast kernels.  dim <= 256
- * and tokens <= 2^31 - 1, else JFA_ERR_UNSUPPORTED.  The forward needs no workspace; the
+ * whole 16 bytes (fp32: 32) with dim and rope.dim multiples of 16 take the fast kernels.
+ * dim <= 256 and tokens <= 2^31 - 1, else JFA_ERR_UNSUPPORTED.  The forward needs no workspace; the
  * backward's (256-byte aligned, jfa_norm_rope_workspace_size; 0 for bad params) is scratch
  * without a status word.  The library finds no errors on the device here.
  */
@@ -406,9 +407,10 @@ jfa_status jfa_norm_rope_bwd(const jfa_norm_rope_params* p, const void* q, const
  * lse [T, Hq] as in jfa_fwd; a row that sees no key gets o = 0, lse = -inf.  Scores,
  * statistics and sums are fp32; on the tensor-core kernels (bf16, dims 64 and 128) the
  * weights are rounded to bf16 (over MXFP8 also fp16) for the product with the values.  The
- * sums run before they are divided by the weights' sum: a row's keys times its largest |v| has
- * to stay below 2^128.  Keys and values of positions that a sequence's other queries see must be finite where a row's own mask
- * hides them.  Results repeat bit for bit on one GPU.
+ * sums run before they are divided by the weights' sum: a row's keys times its largest |v|
+ * has to stay below 2^128.  Keys and values of positions that a sequence's other queries
+ * see must be finite where a row's own mask hides them.  Results repeat bit for bit on one
+ * GPU.
  *
  * Every call cuts its work into equal shares on the device (jfa_paged_plan does it once for
  * several calls, which then pass flags = JFA_PLANNED, the same params but for scale and

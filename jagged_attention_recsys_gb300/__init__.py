@@ -11,6 +11,7 @@ Build the library with ``python -m jagged_attention_recsys_gb300.build``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -507,15 +508,22 @@ _current_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _on(device, stream):
-    """The raw stream of a call whose tensors live on ``device``, which must be current."""
+def _on(device):
+    """The raw current stream of ``device``, which must be the current one."""
     if device.index != torch.cuda.current_device():
         raise ValueError("tensors are on %s, which is not the current device" % device)
-    if stream is None:
-        return _current_raw_stream(device.index)
-    if stream.device != device:
-        raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device, device))
-    return stream.cuda_stream
+    return _current_raw_stream(device.index)
+
+
+def _in_stream(fn):
+    """Calls with a ``stream`` run with it current: what they allocate belongs to it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
 def _rows(name, t, dtype, device, heads=None, dim=None, tokens=None):
@@ -582,6 +590,7 @@ def _out(name, t, like, make=True):
     return t, _rows(name, t, like.dtype, like.device, H, D, T)
 
 
+@_in_stream
 def jfa_norm_rope_fwd(q, k, pos, wq=None, wk=None, *, rope=None, eps=1e-6, norm=True, yq=None,
                       yk=None, stream=None):
     """RMS norm of every head of q [T, Hq, D] and k [T, Hk, D] (either may be None) with the
@@ -592,10 +601,11 @@ def jfa_norm_rope_fwd(q, k, pos, wq=None, wk=None, *, rope=None, eps=1e-6, norm=
     if k is not None:
         yk, p.stride_yk = _out("yk", yk, k)
     _check(lib().jfa_norm_rope_fwd(ctypes.byref(p), _addr(q), _addr(k), _addr(pos), _addr(wq), _addr(wk),
-                                   _addr(yq), _addr(yk), _on(x.device, stream)), "jfa_norm_rope_fwd")
+                                   _addr(yq), _addr(yk), _on(x.device)), "jfa_norm_rope_fwd")
     return yq, yk
 
 
+@_in_stream
 def jfa_norm_rope_bwd(q, k, pos, dyq, dyk, wq=None, wk=None, *, rope=None, eps=1e-6, norm=True,
                       dq=None, dk=None, dwq=None, dwk=None, ws=None, stream=None):
     """Backward of jfa_norm_rope_fwd; returns (dq, dk, dwq, dwk).  The weights' gradients are
@@ -620,7 +630,7 @@ def jfa_norm_rope_bwd(q, k, pos, dyq, dyk, wq=None, wk=None, *, rope=None, eps=1
         ws = torch.empty(max(n, 256), dtype=torch.uint8, device=x.device)
     _check(lib().jfa_norm_rope_bwd(ctypes.byref(p), _addr(q), _addr(k), _addr(pos), _addr(wq), _addr(wk),
                                    _addr(dyq), _addr(dyk), _addr(dq), _addr(dk), _addr(dwq), _addr(dwk),
-                                   _addr(ws), ws.numel(), _on(x.device, stream)), "jfa_norm_rope_bwd")
+                                   _addr(ws), ws.numel(), _on(x.device)), "jfa_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
@@ -704,19 +714,22 @@ def _paged_prep(cache, table, offs, lens, total, dtype, heads_q, scale, causal, 
     return p, ws
 
 
+@_in_stream
 def jfa_cache_write(k, v, cache, table, offs, lens, *, ws=None, stream=None, planned=False):
     """Writes the new tokens' k [T, Hk, Dqk] and v [T, Hk, Dv] into their pages of ``cache``:
     token i of sequence b at position lens[b] - L_b + i.  Returns the workspace, whose status
     word jfa_status_check reads."""
+    stride_k = _rows("k", k, k.dtype, cache.device, cache.heads, cache.dim_qk)
+    stride_v = _rows("v", v, k.dtype, cache.device, cache.heads, cache.dim_v, k.shape[0])
     p, ws = _paged_prep(cache, table, offs, lens, k.shape[0], k.dtype, None, None, True, ws, planned)
-    p.stride_k = _rows("k", k, k.dtype, cache.device, cache.heads, cache.dim_qk)
-    p.stride_v = _rows("v", v, k.dtype, cache.device, cache.heads, cache.dim_v, k.shape[0])
+    p.stride_k, p.stride_v = stride_k, stride_v
     _check(lib().jfa_cache_write(ctypes.byref(p), _addr(k), _addr(v), _addr(offs), _addr(lens), _addr(table),
                                  _addr(cache.k), _addr(cache.v), _addr(cache.k_scale), _addr(cache.v_scale),
-                                 _addr(ws), ws.numel(), _on(cache.device, stream)), "jfa_cache_write")
+                                 _addr(ws), ws.numel(), _on(cache.device)), "jfa_cache_write")
     return ws
 
 
+@_in_stream
 def jfa_cache_read(cache, table, offs, lens, total, *, dtype=torch.bfloat16, k=None, v=None, ws=None,
                    stream=None, planned=False):
     """The last L_b cached rows of every sequence, ``total`` = offs[B] of them, gathered into
@@ -734,28 +747,32 @@ def jfa_cache_read(cache, table, offs, lens, total, *, dtype=torch.bfloat16, k=N
         _plain("v", v, dtype, vshape, dev)
     _check(lib().jfa_cache_read(ctypes.byref(p), _addr(cache.k), _addr(cache.v), _addr(cache.k_scale),
                                 _addr(cache.v_scale), _addr(offs), _addr(lens), _addr(table), _addr(k),
-                                _addr(v), _addr(ws), ws.numel(), _on(dev, stream)), "jfa_cache_read")
+                                _addr(v), _addr(ws), ws.numel(), _on(dev)), "jfa_cache_read")
     return k, v
 
 
+@_in_stream
 def jfa_paged_plan(q, cache, table, offs, lens, *, causal=True, ws=None, stream=None):
     """The shares of work of a step's calls on ``cache`` (same offs and lens), built into
     ``ws`` (allocated if None); returns ``ws`` for calls with ``planned=True``."""
+    stride_q = _rows("q", q, q.dtype, cache.device, None, cache.dim_qk)
     p, ws = _paged_prep(cache, table, offs, lens, q.shape[0], q.dtype, q.shape[1], None, causal, ws, False)
-    p.stride_q = _rows("q", q, q.dtype, cache.device, None, cache.dim_qk)
+    p.stride_q = stride_q
     _check(lib().jfa_paged_plan(ctypes.byref(p), _addr(offs), _addr(lens), _addr(ws), ws.numel(),
-                                _on(cache.device, stream)), "jfa_paged_plan")
+                                _on(cache.device)), "jfa_paged_plan")
     return ws
 
 
+@_in_stream
 def jfa_paged_fwd(q, cache, table, offs, lens, *, scale=None, causal=True, o=None, lse=None, ws=None,
                   stream=None, planned=False):
     """Attention of the new tokens' queries q [T, Hq, Dqk] over their sequences' cached keys
     and values (the new tokens' own among them), Hq a multiple of the cache's heads; returns
     (o [T, Hq, Dv], lse [T, Hq])."""
-    p, ws = _paged_prep(cache, table, offs, lens, q.shape[0], q.dtype, q.shape[1], scale, causal, ws, planned)
     dev = cache.device
-    p.stride_q = _rows("q", q, q.dtype, dev, None, cache.dim_qk)
+    stride_q = _rows("q", q, q.dtype, dev, None, cache.dim_qk)
+    p, ws = _paged_prep(cache, table, offs, lens, q.shape[0], q.dtype, q.shape[1], scale, causal, ws, planned)
+    p.stride_q = stride_q
     T, H = q.shape[0], q.shape[1]
     if o is None:
         o = torch.empty((T, H, cache.dim_v), dtype=q.dtype, device=dev)
@@ -767,5 +784,5 @@ def jfa_paged_fwd(q, cache, table, offs, lens, *, scale=None, causal=True, o=Non
         _plain("lse", lse, torch.float32, (T, H), dev)
     _check(lib().jfa_paged_fwd(ctypes.byref(p), _addr(q), _addr(cache.k), _addr(cache.v), _addr(cache.k_scale),
                                _addr(cache.v_scale), _addr(offs), _addr(lens), _addr(table), _addr(o),
-                               _addr(lse), _addr(ws), ws.numel(), _on(dev, stream)), "jfa_paged_fwd")
+                               _addr(lse), _addr(ws), ws.numel(), _on(dev)), "jfa_paged_fwd")
     return o, lse

@@ -13,8 +13,8 @@
 // would otherwise be paid token by token), then the warp goes through them.  A lane takes 16
 // columns (two lanes share a block's maximum by one shuffle), consecutive over the token's heads,
 // with a piece of the keys and one of the values in flight; 24 (write) or 32 warps an SM do the
-// rest (two pieces each: 157 us for a write of 118 K tokens of 8 heads of 128, so 145).  Measured,
-// bf16 rows to MXFP8 pages and to bf16 ones: 145 us, 5.1 TB/s; back: 63 us, 4.4 TB/s.
+// rest (two pieces each: 157 us for a write of 118 K tokens of 8 heads of 128, so 145).  Measured
+// from bf16 to MXFP8: that write 145 us, 5.1 TB/s; 61 users read back 63 us, 4.4 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

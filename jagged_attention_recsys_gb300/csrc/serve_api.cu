@@ -237,11 +237,11 @@ jfa_status jfa_norm_rope_bwd(const jfa_norm_rope_params* p, const void* q, const
   if (p->tokens > 0 && p->rope.dim > 0 && !aligned(pos, 8)) return JFA_ERR_INVALID_ARG;
   if (!ws || ((uintptr_t)ws & 255u) != 0 || ws_bytes < norm_rope_ws(p)) return JFA_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
-  if (p->tokens == 0) {  // no token: the weights' gradients are zero
-    if (a.side[0].dw && (st = cu(cudaMemsetAsync(dwq, 0, sizeof(float) * p->dim, s))) != JFA_OK) return st;
-    if (a.side[1].dw && (st = cu(cudaMemsetAsync(dwk, 0, sizeof(float) * p->dim, s))) != JFA_OK) return st;
-    return JFA_OK;
-  }
+  // no row: the weights' gradients are zero
+  const size_t bytes = sizeof(float) * p->dim;
+  if (dwq && (p->tokens == 0 || p->heads_q == 0) && (st = cu(cudaMemsetAsync(dwq, 0, bytes, s))) != JFA_OK) return st;
+  if (dwk && (p->tokens == 0 || p->heads_k == 0) && (st = cu(cudaMemsetAsync(dwk, 0, bytes, s))) != JFA_OK) return st;
+  if (p->tokens == 0) return JFA_OK;
   norm_rope_common(p, pos, &a);
   Timed t(JFA_KERNEL_NORM_ROPE, s);
   return cu(launch_norm_rope_bwd(a, p->dtype, (float*)ws, s));
