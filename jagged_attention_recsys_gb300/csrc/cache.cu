@@ -10,11 +10,13 @@
 // Bound: HBM (bytes in plus bytes out; nothing to compute).  A warp takes a run of up to 32
 // consecutive tokens, or part of a token's heads where there are fewer tokens than warps: its
 // lanes first look up a token each (sequence, position, page: a chain of dependent loads that
-// would otherwise be paid token by token), then the warp goes through them.  A lane takes 16
-// columns (two lanes share a block's maximum by one shuffle), consecutive over the token's heads,
-// with a piece of the keys and one of the values in flight; 24 (write) or 32 warps an SM do the
-// rest (two pieces each: 157 us for a write of 118 K tokens of 8 heads of 128, so 145).  Measured
-// from bf16 to MXFP8: that write 145 us, 5.1 TB/s; 61 users read back 63 us, 4.4 TB/s.
+// would otherwise be paid token by token).  A lane then takes a piece of 16 columns of all heads'
+// through all the run's tokens (two lanes share a block's maximum by one shuffle): its place in a
+// token's rows is worked out once a run, not once a token, which took two thirds of the
+// instructions (145 us and 63 us for the two figures below).
+// In flight: four tokens of a lane in 24 warps for a write, two in 32 for a read.
+// Measured, bf16 and MXFP8: 118 K tokens of 8 heads of 128 written in 132 us, 5.6 TB/s; 61 users
+// of 8 heads of 128 and 64 read back in 54 us, 5.2 TB/s; 83% and 77% of the copy rate.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -26,8 +28,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// CTAs of an SM: a write's conversion to MXFP8 spills at four (154 us, so 145); a read wants the
-// loads in flight (three: 68 us, so 63)
+// CTAs of an SM: a write with two (143 us) or a read with three (59 us) has less in flight, a read
+// with five (61 us) too few registers
 template <bool WRITE>
 constexpr int kCtas = WRITE ? 3 : 4;
 
@@ -43,6 +45,10 @@ struct Raw {
   __device__ __forceinline__ void store(T* y) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(y)[i] = q[i];
+  }
+  __device__ __forceinline__ void store_past(T* y) const {  // past the L2: rows read back are read once
+#pragma unroll
+    for (int i = 0; i < N; ++i) __stcs(reinterpret_cast<uint4*>(y) + i, q[i]);
   }
   __device__ __forceinline__ void get(float (&v)[W]) const {
 #pragma unroll
@@ -118,22 +124,6 @@ __device__ __forceinline__ int token_position(const Paged& p, int64_t t, int b, 
   return pos < 0 ? -1 : (int)pos;
 }
 
-// Pieces of W columns of one token's tensor: a lane's next piece is 32 further on.
-template <int W>
-struct Piece {
-  int c, head, col;  // index, head, piece of the head
-  __device__ __forceinline__ Piece(int c0, int per) : c(c0), head(c0 / per), col(c0 - c0 / per * per) {}
-  __device__ __forceinline__ void next(int per, int dh, int dc) {  // dh, dc: 32 / per and 32 % per
-    c += 32;
-    head += dh;
-    col += dc;
-    if (col >= per) {
-      col -= per;
-      ++head;
-    }
-  }
-};
-
 // 16 columns as MXFP8.  All lanes call it (a block is two lanes'); `ok` says which have a row.
 template <typename T>
 __device__ __forceinline__ void write_mx(const Raw<T, 16>& raw, uint8_t* codes, uint8_t* scale, int col, bool ok) {
@@ -151,6 +141,77 @@ __device__ __forceinline__ void write_mx(const Raw<T, 16>& raw, uint8_t* codes, 
   if (ok) {
     *reinterpret_cast<uint4*>(codes) = make_uint4(c[0], c[1], c[2], c[3]);
     if ((col & 1) == 0) *scale = (uint8_t)(e + 127);
+  }
+}
+
+// One of a token's tensors in the cache: n tokens from the one at `x` on, `stride` apart, whose
+// rows of head 0 the warp's lanes hold.  A lane takes a piece of W columns, c of all heads', through
+// all the tokens, U of them in flight: where a piece lies in a token's rows is worked out once.
+template <typename T, int KIND, bool WRITE>
+__device__ __forceinline__ void move_rows(T* x, int64_t stride, uint8_t* cache, uint8_t* scales, int dim,
+                                          int page_shift, int c0, int c1, int64_t row, int n, int lane) {
+  constexpr bool MX = KIND == kCacheMx;
+  constexpr int W = MX ? 16 : 8, E = MX ? 1 : (int)sizeof(T), U = !WRITE || (MX && sizeof(T) == 4) ? 2 : 4;
+  const int per = dim / W;
+  const uint32_t row_bytes = (uint32_t)dim * E, row_scales = (uint32_t)dim >> 5;
+  for (int c = c0 + lane; c - lane < c1; c += 32) {
+    const bool ok = c < c1;
+    const int head = c / per, col = c - head * per;
+    uint8_t* at0 = cache + ((uint64_t)(row_bytes * (uint32_t)head) << page_shift) + col * W * E;
+    uint8_t* sc0 = scales + ((uint64_t)(row_scales * (uint32_t)head) << page_shift) + (col >> 1);
+    T* y = x + (int64_t)c * W;
+    for (int i = 0; i < n; i += U) {
+      int64_t r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        r[u] = __shfl_sync(0xffffffffu, row, (i + u) & 31);
+        if (i + u >= n) r[u] = -1;
+      }
+      if constexpr (WRITE) {
+        Raw<T, W> raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (ok && r[u] >= 0) raw[u].load(y + (i + u) * stride);
+          else raw[u].zero();
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const bool live = ok && r[u] >= 0;
+          if constexpr (MX)
+            write_mx<T>(raw[u], at0 + r[u] * row_bytes, sc0 + r[u] * row_scales, col, live);
+          else if (live)
+            raw[u].store((T*)(at0 + r[u] * row_bytes));
+        }
+      } else if constexpr (MX) {
+        uint4 code[U];
+        float f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          code[u] = make_uint4(0u, 0u, 0u, 0u);
+          f[u] = 0.f;
+          if (ok && r[u] >= 0) {
+            code[u] = __ldcs(reinterpret_cast<const uint4*>(at0 + r[u] * row_bytes));
+            f[u] = __uint_as_float((uint32_t)__ldg(sc0 + r[u] * row_scales) << 23);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          Raw<T, W> raw;
+          raw.set_mx(code[u], f[u]);
+          if (ok && i + u < n) raw.store_past(y + (i + u) * stride);
+        }
+      } else {
+        Raw<T, W> raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          raw[u].zero();
+          if (ok && r[u] >= 0) raw[u].load((const T*)(at0 + r[u] * row_bytes));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (ok && i + u < n) raw[u].store_past(y + (i + u) * stride);
+      }
+    }
   }
 }
 
@@ -173,7 +234,6 @@ cache_kernel(const __grid_constant__ Paged p, T* k_out, T* v_out, PagedHeader* h
   const int lane = threadIdx.x & 31;
   const int perk = p.dim_qk / W, perv = p.dim_v / W;  // pieces of a head
   const int ck = p.heads_k * perk, cv = p.heads_k * perv;
-  const int dhk = 32 / perk, dck = 32 - dhk * perk, dhv = 32 / perv, dcv = 32 - dhv * perv;
   const int64_t runs = (p.total_q + run - 1) / run;
   const int64_t tasks = runs * parts, nw = (int64_t)gridDim.x * kWarps;
   for (int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); task < tasks; task += nw) {
@@ -191,59 +251,10 @@ cache_kernel(const __grid_constant__ Paged p, T* k_out, T* v_out, PagedHeader* h
     // a part is a stretch of whole groups of 32 pieces
     auto cut = [&](int m, int i) { return min(m, (int)((int64_t)((m + 31) / 32) * i / parts) * 32); };
     const int k0 = cut(ck, part), k1 = cut(ck, part + 1), v0 = cut(cv, part), v1 = cut(cv, part + 1);
-    for (int i = 0; i < n; ++i) {
-      const int64_t t = t0 + i, r0 = __shfl_sync(0xffffffffu, row, i);
-      const bool has = r0 >= 0;
-      if (WRITE && !has) continue;
-      // the token's rows of head 0, a head's step from there on, and the token's own rows
-      constexpr int E = MX ? 1 : (int)sizeof(T);
-      uint8_t *kc = (uint8_t*)p.kc + r0 * p.dim_qk * E, *vc = (uint8_t*)p.vc + r0 * p.dim_v * E;
-      uint8_t *ks = p.ks + r0 * (p.dim_qk >> 5), *vs = p.vs + r0 * (p.dim_v >> 5);
-      const uint32_t hk = (uint32_t)p.dim_qk * E << p.page_shift, hv = (uint32_t)p.dim_v * E << p.page_shift;
-      const uint32_t hks = (uint32_t)(p.dim_qk >> 5) << p.page_shift, hvs = (uint32_t)(p.dim_v >> 5) << p.page_shift;
-      const T *kin = (const T*)p.k + t * p.sk, *vin = (const T*)p.v + t * p.sv;
-      T *kout = k_out + t * ck * W, *vout = v_out + t * cv * W;
-      Piece<W> pk(k0 + lane, perk), pv(v0 + lane, perv);
-      for (; pk.c - lane < k1 || pv.c - lane < v1; pk.next(perk, dhk, dck), pv.next(perv, dhv, dcv)) {
-        const bool okk = pk.c < k1, okv = pv.c < v1;
-        uint8_t *ck_at = kc + (uint64_t)pk.head * hk + pk.col * W * E, *cv_at = vc + (uint64_t)pv.head * hv + pv.col * W * E;
-        uint8_t *sk_at = ks + (uint64_t)pk.head * hks + (pk.col >> 1), *sv_at = vs + (uint64_t)pv.head * hvs + (pv.col >> 1);
-        Raw<T, W> rk, rv;
-        rk.zero();
-        rv.zero();
-        if constexpr (WRITE) {
-          if (okk) rk.load(kin + (uint32_t)pk.c * W);
-          if (okv) rv.load(vin + (uint32_t)pv.c * W);
-          if constexpr (MX) {
-            write_mx<T>(rk, ck_at, sk_at, pk.col, okk);
-            write_mx<T>(rv, cv_at, sv_at, pv.col, okv);
-          } else {
-            if (okk) rk.store((T*)ck_at);
-            if (okv) rv.store((T*)cv_at);
-          }
-        } else {
-          if constexpr (MX) {
-            uint4 code_k = make_uint4(0u, 0u, 0u, 0u), code_v = code_k;
-            float fk = 0.f, fv = 0.f;
-            if (okk && has) {
-              code_k = __ldcs(reinterpret_cast<const uint4*>(ck_at));
-              fk = __uint_as_float((uint32_t)__ldg(sk_at) << 23);
-            }
-            if (okv && has) {
-              code_v = __ldcs(reinterpret_cast<const uint4*>(cv_at));
-              fv = __uint_as_float((uint32_t)__ldg(sv_at) << 23);
-            }
-            rk.set_mx(code_k, fk);
-            rv.set_mx(code_v, fv);
-          } else {
-            if (okk && has) rk.load((const T*)ck_at);
-            if (okv && has) rv.load((const T*)cv_at);
-          }
-          if (okk) rk.store(kout + (uint32_t)pk.c * W);
-          if (okv) rv.store(vout + (uint32_t)pv.c * W);
-        }
-      }
-    }
+    move_rows<T, KIND, WRITE>(WRITE ? (T*)p.k + t0 * p.sk : k_out + t0 * ck * W, WRITE ? p.sk : (int64_t)ck * W,
+                              (uint8_t*)p.kc, p.ks, p.dim_qk, p.page_shift, k0, k1, row, n, lane);
+    move_rows<T, KIND, WRITE>(WRITE ? (T*)p.v + t0 * p.sv : v_out + t0 * cv * W, WRITE ? p.sv : (int64_t)cv * W,
+                              (uint8_t*)p.vc, p.vs, p.dim_v, p.page_shift, v0, v1, row, n, lane);
   }
 }
 
