@@ -331,8 +331,8 @@ jfa_status jfa_block_rope_bwd(const jfa_params* p, const void* q, const void* k,
  *
  * Values are fp32 or bf16 (dtype), pointers aligned to a value; pointers and strides of
  * whole 16 bytes (fp32: 32) with dim and rope.dim multiples of 16 take the fast kernels.
- * dim <= 256 and tokens <= 2^31 - 1, else JFA_ERR_UNSUPPORTED.  The forward needs no workspace; the
- * backward's (256-byte aligned, jfa_norm_rope_workspace_size; 0 for bad params) is scratch
+ * dim <= 256 and tokens <= 2^31 - 1, else JFA_ERR_UNSUPPORTED.  The forward needs no
+ * workspace; the backward's (256-byte aligned, jfa_norm_rope_workspace_size; 0 for bad params) is scratch
  * without a status word.  The library finds no errors on the device here.
  */
 enum { JFA_ROPE_HALVES = 0, JFA_ROPE_PAIRS = 1 };
@@ -419,8 +419,8 @@ jfa_status jfa_norm_rope_bwd(const jfa_norm_rope_params* p, const void* q, const
  * calls that may run concurrently.
  *
  * Limits (JFA_ERR_UNSUPPORTED): dims multiples of 8 (MXFP8: 32), at most 256, in
- * jfa_paged_fwd 128; cache_dtype the values' type or JFA_MXFP8; max_pages * page_size,
- * total_q, batch and pages at most 2^31 - 1.  k, v, q and the caches are 16-byte aligned
+ * jfa_paged_fwd 128; cache_dtype the values' type or JFA_MXFP8; max_pages * page_size and
+ * total_q at most 2^31 - 256, batch and pages 2^31 - 1.  k, v, q and the caches are 16-byte aligned
  * with strides of whole 16 bytes.
  */
 typedef struct {

@@ -20,9 +20,9 @@
 //  * Weight gradients: every lane sums its 16 columns in registers over all its rows, the
 //    CTA adds its lanes in a fixed order and writes one partial, a second kernel adds the
 //    partials in order: no atomics, the same bits every time on one GPU.
-// Rows that do not divide into slots (dim or rotated columns not multiples of 16, pointers
-// or strides not multiples of an access, 16 bytes in bf16 and 32 in fp32) take the *_any kernels: one warp a row, single
-// values.
+// Rows that do not divide into slots (dim or rotated columns not multiples of 16, pointers or
+// strides not multiples of an access, 16 bytes in bf16 and 32 in fp32) take the *_any kernels:
+// one warp a row, single values.
 // Measured: 131 K tokens of 32 + 8 heads of 128, bf16: 415 us, 6.5 TB/s, 95% of the copy rate (four
 // rows of a lane in flight, three CTAs an SM; four CTAs: 483 us).  20 K tokens of 8 + 8 heads of
 // 80 in fp32, where 5 of 8 lanes have values: 43 us, 4.7 TB/s (three rows in flight: 57 us).

@@ -6,9 +6,10 @@
 // and B of the same key head, rows = consecutive tokens by the group's heads, so a key block
 // loaded once serves 256 rows.  A and B are two streams of steps, one per block of 128 keys:
 //   S = Q K^T -> softmax -> P -> O += P V,
-// so that the softmax of one stream runs under the products of the other.  Where B has no rows (a chunk of at most 128 rows, the
-// last tile of an odd number) the streams share A's queries and take the key blocks in turn,
-// and A joins both outputs: two loads and two softmaxes in flight instead of one.
+// so that the softmax of one stream runs under the products of the other.  Where B has no rows
+// (a chunk of at most 128 rows, the last tile of an odd number) the streams share A's queries
+// and take the key blocks in turn, and A joins both outputs: two loads and two softmaxes in
+// flight instead of one.
 // Warps (a softmax thread owns a row: no exchange of row statistics):
 //   0-3, 4-7  softmax of A and B, and their epilogues
 //   8, 10     issue the MMAs of A and of B.  An issue holds its thread for most of the MMA's own
@@ -25,6 +26,14 @@
 // its commit PV has completed: O may then be rescaled without a further wait.
 // The row maximum is kept lazily: O and the sum are rescaled only when it grows by more
 // than 2^8.
+// Measured: 8 prompts of 1024 to 4096 tokens, 32 heads on 8 of 128, causal, bf16: 428 us, 1070
+// TFLOP/s; 13 chunks of up to 512 tokens over caches of up to 16384, 32 heads on 4, MXFP8: 463 us,
+// 970 TFLOP/s.  Of a block's time of about 3,000 cycles for both streams the products take 2,048;
+// a stream's softmax (1,330) and its own two products (1,024) follow one another, since its S
+// and P share their columns of TMEM, and both streams' tiles fill the 512.  The epilogues take
+// 7,700 cycles a tile, 10% of the prompts' time.  Slower: the weights handed over in halves
+// (443 us), two threads a row (495), the exponentials begun against an older maximum (496), a
+// rolled softmax that reads TMEM twice (445).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>

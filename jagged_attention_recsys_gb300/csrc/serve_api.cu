@@ -104,8 +104,10 @@ jfa_status check_paged(const jfa_paged_params* p) {
   if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1)) != 0) return JFA_ERR_UNSUPPORTED;
   const int unit = p->cache_dtype == JFA_MXFP8 ? 32 : 8;
   if (p->dim_qk % unit || p->dim_v % unit || p->dim_qk > 256 || p->dim_v > 256) return JFA_ERR_UNSUPPORTED;
-  if (p->total_q > INT32_MAX || p->batch > INT32_MAX || p->pages > INT32_MAX ||
-      (int64_t)p->max_pages * p->page_size > INT32_MAX || p->heads_q > 65536 || p->heads_k > 65536)
+  // the kernels round positions and tokens up to whole tiles in 32 bits
+  constexpr int64_t kMost = (int64_t)INT32_MAX - 255;
+  if (p->total_q > kMost || p->batch > INT32_MAX || p->pages > INT32_MAX ||
+      (int64_t)p->max_pages * p->page_size > kMost || p->heads_q > 65536 || p->heads_k > 65536)
     return JFA_ERR_UNSUPPORTED;
   return JFA_OK;
 }

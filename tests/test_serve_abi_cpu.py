@@ -137,5 +137,13 @@ def test_paged_refusals(L):
     assert L.jfa_paged_workspace_size(None) == 0
 
 
+def test_positions_that_tiles_would_carry_past_32_bits(L):
+    """A tile's end is worked out in 32 bits: the last 255 values are refused."""
+    for f in (paged, write, read, plan):
+        assert f(L, G(page_size=16, max_pages=(1 << 27) - 15)) == UNSUP
+        assert f(L, G(total_q=(1 << 31) - 255, batch=1)) == UNSUP
+    assert L.jfa_paged_workspace_size(ctypes.byref(G(page_size=16, max_pages=(1 << 27) - 16, total_q=(1 << 31) - 256))) > 0
+
+
 def test_status_names_bad_pages(L):
     assert "page" in jfa.status_string(jfa.JFA_ERR_BAD_PAGES)
