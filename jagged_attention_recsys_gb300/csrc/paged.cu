@@ -307,10 +307,13 @@ int paged_kernel(const Paged& p, int dtype) {
   const bool dims = (p.dim_qk == 64 || p.dim_qk == 128) && (p.dim_v == 64 || p.dim_v == 128);
   const int64_t rows = (p.pages * p.heads_k) << p.page_shift;
   if (dtype != JFA_BF16 || !dims || p.pages == 0 || p.total_q == 0 || rows >= INT32_MAX) return kPagedSimt;
-  // Rows that share a key head, over the sequences with new tokens at most: up to 16 go to one
-  // mma.sync tile, more to tcgen05's 128-row tiles (groups larger than one would split them).
+  // Rows that share a key head, a sequence on average: few go to mma.sync tiles of at most 16, more
+  // to tcgen05's 128-row tiles (groups larger than one would split them).  Measured, 64 users of
+  // 2048 keys, 8 key heads of 128, us, few-row kernel against tcgen05: bf16 pages 16 rows 115 to
+  // 121, 24 rows 195 to 121; MXFP8, where tcgen05 waits for the tiles in bf16, 16 rows 84 to 156,
+  // 32 rows 141 to 162, 48 rows 191 to 164.
   const int64_t rows_per_seq = p.total_q * p.group / p.batch;
-  return rows_per_seq <= 16 || p.group > 128 ? kPagedRows16 : kPagedTc;
+  return rows_per_seq <= (p.kind == kCacheMx ? 32 : 16) || p.group > 128 ? kPagedRows16 : kPagedTc;
 }
 
 TileShape paged_shape(const Paged& p, int kernel) {
@@ -325,7 +328,8 @@ TileShape paged_shape(const Paged& p, int kernel) {
     t.share = 512;
     return t;
   }
-  // the 16-row kernel's tiles of 8 rows where a sequence's rows of a key head fit them
+  // the few-row kernel's tiles of 8 rows where a sequence's rows of a key head fit them (the users
+  // above, 8 rows: bf16 109 us to 115 in tiles of 16, MXFP8 72 to 82)
   const int most = kernel == kPagedRows16 && p.group <= 8 && p.total_q * p.group <= 8 * p.batch ? 8 : kRows;
   t.gsub = p.group < most ? p.group : most;
   t.nsub = (p.group + t.gsub - 1) / t.gsub;
