@@ -506,11 +506,12 @@ def jfa_block_bwd(q, k, v, o, lse, dout, offs, *, scale=None, causal=False, dq=N
 # The handle alone: building a torch Stream around it costs 2.5 us a call.
 _current_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on(device):
     """The raw current stream of ``device``, which must be the current one."""
-    if device.index != torch.cuda.current_device():
+    if device.index != _current_device():
         raise ValueError("tensors are on %s, which is not the current device" % device)
     return _current_raw_stream(device.index)
 
@@ -567,26 +568,34 @@ def _norm_rope_params(q, k, pos, wq, wk, eps, rope, norm):
         raise ValueError("q and k must be [tokens, heads, dim] CUDA tensors")
     if not norm and (wq is not None or wk is not None):
         raise ValueError("norm=False takes no weights")
-    T, _, D = x.shape
-    p = jfa_norm_rope_params(tokens=T, dim=D, dtype=_dtype_code(x.dtype), norm=int(bool(norm)), eps=eps)
+    (T, _, D), dtype, dev = x.shape, x.dtype, x.device
+    sq = hq = sk = hk = 0
+    if rope is not None:
+        _plain("pos", pos, torch.int64, (T,), dev)
+    if q is not None:
+        sq, hq = _rows("q", q, dtype, dev, None, D, T), q.shape[1]
+    if k is not None:
+        sk, hk = _rows("k", k, dtype, dev, None, D, T), k.shape[1]
+    if wq is not None:
+        _plain("wq", wq, torch.float32, (D,), dev)
+    if wk is not None:
+        _plain("wk", wk, torch.float32, (D,), dev)
+    p = jfa_norm_rope_params(T, sq, sk, 0, 0, 0, 0, hq, hk, D, _dtype_code(dtype), 1 if norm else 0, eps)
     if rope is not None:
         p.rope = rope
-        _plain("pos", pos, torch.int64, (T,), x.device)
-    if q is not None:
-        p.stride_q, p.heads_q = _rows("q", q, x.dtype, x.device, None, D, T), q.shape[1]
-    if k is not None:
-        p.stride_k, p.heads_k = _rows("k", k, x.dtype, x.device, None, D, T), k.shape[1]
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is not None:
-            _plain(name, w, torch.float32, (D,), x.device)
     return p, x
+
+
+def _rows_like(t):
+    """An empty contiguous tensor of the rows of ``t`` (the copied options cost less than given ones)."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _out(name, t, like, make=True):
     """A tensor of the rows of ``like`` and its stride between tokens; made if None."""
     T, H, D = like.shape
     if t is None and make:
-        return torch.empty((T, H, D), dtype=like.dtype, device=like.device), H * D
+        return _rows_like(like), H * D
     return t, _rows(name, t, like.dtype, like.device, H, D, T)
 
 
@@ -775,7 +784,7 @@ def jfa_paged_fwd(q, cache, table, offs, lens, *, scale=None, causal=True, o=Non
     p.stride_q = stride_q
     T, H = q.shape[0], q.shape[1]
     if o is None:
-        o = torch.empty((T, H, cache.dim_v), dtype=q.dtype, device=dev)
+        o = _rows_like(q) if cache.dim_v == cache.dim_qk else torch.empty((T, H, cache.dim_v), dtype=q.dtype, device=dev)
     else:
         _plain("o", o, q.dtype, (T, H, cache.dim_v), dev)
     if lse is None:
