@@ -28,12 +28,11 @@
 // than 2^8.
 // Measured: 8 prompts of 1024 to 4096 tokens, 32 heads on 8 of 128, causal, bf16: 428 us, 1070
 // TFLOP/s; 13 chunks of up to 512 tokens over caches of up to 16384, 32 heads on 4, MXFP8: 463 us,
-// 970 TFLOP/s.  Of a block's time of about 3,000 cycles for both streams the products take 2,048;
-// a stream's softmax (1,330) and its own two products (1,024) follow one another, since its S
-// and P share their columns of TMEM, and both streams' tiles fill the 512.  The epilogues take
-// 7,700 cycles a tile, 10% of the prompts' time.  Slower: the weights handed over in halves
-// (443 us), two threads a row (495), the exponentials begun against an older maximum (496), a
-// rolled softmax that reads TMEM twice (445).
+// 970 TFLOP/s.  The prompts without any softmax take 335 us, with its TMEM loads and stores 343:
+// a stream's softmax and its products follow one another, since its S and P share their columns
+// of TMEM, and both streams' tiles fill the 512.  Not faster: the weights handed over in halves
+// (433 us), two threads a row (495; they share a scheduler), the exponentials begun against an
+// older maximum (496), a rolled softmax that reads TMEM twice (445).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
