@@ -524,8 +524,10 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
         }
 #pragma unroll
         for (int i = 0; i < NBV; ++i) {
-          // the key's scale over the reference, 2^-9 to 1 as a half
-          const uint16_t h = (uint16_t)(((int)((mine >> (8 * i)) & 255) - ref_scale[i] + 15) << 10);
+          // the key's scale over the reference, 2^-9 to 1 as a half; a scale of 0 makes zeros, so that O
+          // is zero until a block has a reference
+          const int e = (mine >> (8 * i)) & 255;
+          const uint16_t h = e == 0 ? 0 : (uint16_t)((e - ref_scale[i] + 15) << 10);
           asm volatile("st.shared.u16 [%0], %1;" ::"r"(fac + (i * 32 + lane) * 2), "h"(h) : "memory");
         }
         __syncwarp();
