@@ -21,14 +21,16 @@
 // at most 2^-39 of it), so the scores are fp16 products of codes, one block of 32 columns at a
 // time, and a block's scale multiplies its fp32 sum.  For the output the scales go to the
 // weights: a block of columns has a reference scale, the largest it met (O is kept in its
-// units), and the weights, rounded to fp16, times scale / reference, at most 1, meet fp16 codes
-// (2^-12 of a product of at least 2^-14, absolutely 2^-25 below).  A stage with a scale under
-// 2^-9 of its reference takes its values to bf16 instead (exact) and rounds the weights alone,
-// so that keys of small values keep their precision beside keys of large ones.
+// units), and the weights, rounded to fp16, times scale / reference, at most 1, meet fp16 codes.
+// The largest weight is kept at 2^10 to 2^15, so that one of 2^-25 of it still makes a product of
+// 2^-15, which its two roundings to steps of 2^-24 leave within 2^-9.  A stage
+// where a weight times a scale may be less takes its values to bf16 instead (exact) and
+// rounds the weights alone, to bf16: keys of small weights or values keep their precision beside
+// keys of large ones whose values are zero.
 //
 // Measured: one token for each of 256 users, lengths to 4096, 32 heads on 8 of 128, bf16 pages:
 // 317 us, 6.6 TB/s, 97% of the copy rate.  One or two tokens for 96 users, lengths 512 to 16384,
-// 32 heads on 4 (16 rows a tile), MXFP8: 178 us, 4.7 TB/s, 70%; the loads alone take 135 us, the
+// 32 heads on 4 (16 rows a tile), MXFP8: 181 us, 4.6 TB/s, 68%; the loads alone take 135 us, the
 // rest is the consumers' latency: registers allow two CTAs an SM.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -46,7 +48,13 @@ using namespace tc;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleLog2 = 8.0f;
+// A row's reference is kUp (log2) below the score it was set from and moves when one passes that by
+// kRescale.  Over MXFP8 weights stay within 2^15 (a half's largest is 2^16); moved at 2^2 or 2^4 the
+// step in the header takes 188 or 183 us.
+template <int KIND>
+constexpr float kUp = KIND == kCacheMx ? 10.0f : 0.0f;
+template <int KIND>
+constexpr float kRescale = KIND == kCacheMx ? 5.0f : 8.0f;
 
 template <int DQK, int DV, int KIND, int NT>
 struct Layout {
@@ -437,25 +445,30 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
         }
       }
       // ---- weights
-      // A row's reference moves, with its sum and output, only when a score passes it by 2^8: then
-      // alone the lanes exchange their maxima.
+      // A row's reference moves, with its sum and output, only when a score passes it far enough:
+      // then alone the lanes exchange their maxima.
+      constexpr float kMost = kUp<KIND> + kRescale<KIND>;
       bool need = false;
-      float top[NT][2];
+      float top[NT][2], low[NT][2];  // low: MXFP8, of the keys the row sees
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int seen = min(limit[nt][e], g.seq.lk) - k0;  // keys of this stage the row sees
           top[nt][e] = -INFINITY;
+          low[nt][e] = INFINITY;
 #pragma unroll
           for (int ks = 0; ks < G16; ++ks)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float& v = s[ks][nt][2 * h + e];
-              v = ks * 16 + 8 * h + kq < seen ? v * cs[nt][e] : -INFINITY;
+              const bool sees = ks * 16 + 8 * h + kq < seen;
+              v *= cs[nt][e];
+              if constexpr (MX) low[nt][e] = fminf(low[nt][e], sees ? v : INFINITY);
+              v = sees ? v : -INFINITY;
               top[nt][e] = fmaxf(top[nt][e], v);
             }
-          need |= top[nt][e] > m[nt][e] + kRescaleLog2;  // m = -inf: any key
+          need |= top[nt][e] > m[nt][e] + kMost;  // m = -inf: any key
         }
       if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
@@ -466,7 +479,8 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            if (x > m[nt][e] + kRescaleLog2) {
+            if (x > m[nt][e] + kMost) {
+              x -= kUp<KIND>;
               const float a = ex2(m[nt][e] - x);  // m = -inf: 0
               l[nt][e] *= a;
 #pragma unroll
@@ -494,19 +508,26 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
           }
       // The weights as the products' operand: rounded to bf16 (2^-9 of a weight on average, signs
       // mixed) or, against fp16 codes, to fp16.
-      bool wide = false;  // MXFP8: a scale far under its block's reference
+      bool wide = false;  // MXFP8: a product of weight and scale may be too small for fp16
       if constexpr (MX) {
         const uint32_t mine = NBV == 4 ? ld_shared_u32(scv + lane * 4)
                                        : (ld_shared_u32(scv + (lane & ~1) * 2) >> (16 * (lane & 1))) & 0xffffu;
         const uint32_t fac = sb + L::FAC + warp * NBV * 64;
-        bool out = false;  // a scale above its reference, or far under it
+        float deep = -INFINITY;  // how far (log2) a weight lies under 1
 #pragma unroll
-        for (int i = 0; i < NBV; ++i) out |= (uint32_t)(ref_scale[i] - (int)((mine >> (8 * i)) & 255)) > 9u;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) deep = fmaxf(deep, m[nt][e] - low[nt][e]);
+        // a scale above its reference, or one or a weight so small that their product may be
+        bool out = deep > 11.f;
+#pragma unroll
+        for (int i = 0; i < NBV; ++i) out |= (uint32_t)(ref_scale[i] - (int)((mine >> (8 * i)) & 255)) > 4u;
         if (__any_sync(0xffffffffu, out)) {
+          int gap = 0;  // steps (log2) of this key's scales under their references
 #pragma unroll
           for (int i = 0; i < NBV; ++i) {
-            const int e = min((mine >> (8 * i)) & 255, 254u);
-            const int most = __reduce_max_sync(0xffffffffu, e), least = __reduce_min_sync(0xffffffffu, e);
+            const int e = (mine >> (8 * i)) & 255;
+            const int most = __reduce_max_sync(0xffffffffu, min(e, 254));
             if (most > ref_scale[i]) {  // O of the block goes to the new units, with a step to spare
               const int to = min(most + 1, 254);
               const float f = ref_scale[i] == 0 ? 1.f : exp2i(max(ref_scale[i] - to, -126));
@@ -519,12 +540,14 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
                 }
               ref_scale[i] = to;
             }
-            wide |= least < ref_scale[i] - 9;
+            if (e != 0) gap = max(gap, ref_scale[i] - e);
           }
+          gap = __reduce_max_sync(0xffffffffu, gap);
+          wide = gap > 14 || __any_sync(0xffffffffu, deep + (float)gap > 15.f);
         }
 #pragma unroll
         for (int i = 0; i < NBV; ++i) {
-          // the key's scale over the reference, 2^-9 to 1 as a half; a scale of 0 makes zeros, so that O
+          // the key's scale over the reference, 2^-14 to 1 as a half; a scale of 0 makes zeros, so that O
           // is zero until a block has a reference
           const int e = (mine >> (8 * i)) & 255;
           const uint16_t h = e == 0 ? 0 : (uint16_t)((e - ref_scale[i] + 15) << 10);
@@ -633,6 +656,8 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
         l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
         l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
         l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+        l[nt][e] *= exp2i(-(int)kUp<KIND>);  // back to weights of at most about 1
+        m[nt][e] += kUp<KIND>;
         if (kq == 0) {
           const uint32_t at = ml + ((warp * L::R + 8 * nt + 2 * q + e) * 2) * 4;
           st_shared_f32(at, m[nt][e]);
@@ -656,12 +681,12 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
       for (int e = 0; e < 2; ++e) {
         float M, Ls;
         joined(8 * nt + 2 * q + e, M, Ls);
-        const float a = ex2(m[nt][e] - (M == -INFINITY ? 0.f : M));
+        const float a = ex2(m[nt][e] - (M == -INFINITY ? 0.f : M)) * exp2i(-(int)kUp<KIND>);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          const float f = MX && ref_scale[i / 2] > 0 ? a * exp2i(ref_scale[i / 2] - 127) : a;
-          o[nt][i][e] *= f;
-          o[nt][i][2 + e] *= f;
+          const float f = MX && ref_scale[i / 2] > 0 ? exp2i(ref_scale[i / 2] - 127) : 1.f;
+          o[nt][i][e] = o[nt][i][e] * a * f;
+          o[nt][i][2 + e] = o[nt][i][2 + e] * a * f;
         }
       }
     constexpr int CW = L::R / 4, PER = 32 / CW;  // columns a thread adds up in a round, threads of a row

@@ -72,3 +72,41 @@ def test_scales_of_zero_read_as_zeros(kernel, which, zeros):
             if new:
                 got = f64(x)[lo + int(b.new[i]) - new:lo + int(b.new[i])].transpose(1, 0, 2)
                 assert np.array_equal(got, of(i)[:, n - new:].astype(np.float32).astype(np.float64))
+
+
+def scored(b, scores, g):
+    """Keys and queries whose scores (scale 1) are `scores` [pages, hk, page] for all heads, given
+    as values that a code of scale 1 holds; the other columns meet zeros."""
+    b.cache.k.zero_()
+    b.cache.k[..., 0] = scores.to(torch.float8_e4m3fn).view(torch.uint8)
+    set_scales(b, "k", torch.full_like(b.cache.k_scale, 127, dtype=torch.int32))
+    b.cache.k.copy_(torch.where(b.owned, b.cache.k, 0x7f))
+    q = torch.zeros(b.T, b.cache.heads, b.dqk, device="cuda")
+    q[..., 0] = 1
+    return q
+
+
+@kernels
+@pytest.mark.parametrize("gap", [(10, 18), (0, 12), (18, 40), (60, 84), (10, 84)])
+@pytest.mark.parametrize("scales", [(120, 120), (112, 121), (100, 127)])
+def test_small_weights_beside_a_key_of_zero_value(kernel, gap, scales):
+    """One key with nearly all the weight and a value of zero, the others `gap` nats below it: a
+    column is the sum of small weights alone, and keeps its precision relative to that sum."""
+    b, hq = batch(kernel, seed=6)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    # whole and half numbers up to 15 have codes, and multiples of 4 to 60
+    step = 0.5 if gap[1] - gap[0] <= 12 else 4.0
+    top = 8.0 if gap[1] <= 18 else 48.0
+    n = int((gap[1] - gap[0]) / step) + 1
+    low = top - gap[0] - step * torch.randint(0, n, b.cache.k.shape[:3], generator=g, device="cuda")
+    low = low.to(torch.float8_e4m3fn).float()
+    s = torch.randint(scales[0], scales[1] + 1, b.cache.v_scale.shape, generator=g, device="cuda", dtype=torch.int32)
+    for n, row in zip(b.lens_h, b.table_h):
+        if n:  # the sequence's first key
+            low[int(row[0]), :, 0] = top
+            b.cache.v[int(row[0]), :, 0] = 0
+    q = scored(b, low, g)
+    set_scales(b, "v", s)
+    b.k_h = decode(b.cache.k, b.cache.k_scale)
+    q = q[:, :1].expand(-1, hq, -1).to(torch.bfloat16 if b.dtype == "bf16" else torch.float32).contiguous()
+    check_attention(b, hq, q=q, scale=1.0)
