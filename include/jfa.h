@@ -406,7 +406,9 @@ jfa_status jfa_norm_rope_bwd(const jfa_norm_rope_params* p, const void* q, const
  * sequence b sees positions <= lens[b] - L_b + i, else all lens[b].  o [T, Hq, Dv] and
  * lse [T, Hq] as in jfa_fwd; a row that sees no key gets o = 0, lse = -inf.  Scores,
  * statistics and sums are fp32; on the tensor-core kernels (bf16, dims 64 and 128) the
- * weights are rounded to bf16 (over MXFP8 also fp16) for the product with the values.  The
+ * weights are rounded to bf16 (over MXFP8 also fp16, where that is as close) for the product
+ * with the values, and over MXFP8 values of a query row under 2^-31 of its largest may be off by
+ * 2^-39 of that.  A score has to stay in fp32's range before and after its scale.  The
  * sums run before they are divided by the weights' sum: a row's keys times its largest |v|
  * has to stay below 2^128.  Keys and values of positions that a sequence's other queries
  * see must be finite where a row's own mask hides them.  Results repeat bit for bit on one

@@ -19,7 +19,7 @@
 // MXFP8.  Codes are exact in fp16, and a row of bf16 queries times a power of two that brings
 // its largest value to [2^14, 2^15) is exact in fp16 too (values under 2^-31 of the largest lose
 // at most 2^-39 of it), so the scores are fp16 products of codes, one block of 32 columns at a
-// time, and a block's scale multiplies its fp32 sum.  For the output the scales go to the
+// time, and a block's scale times the row's own power of two multiplies its fp32 sum.  For the output the scales go to the
 // weights: a block of columns has a reference scale, the largest it met (O is kept in its
 // units), and the weights, rounded to fp16, times scale / reference, at most 1, meet fp16 codes.
 // The largest weight is kept at 2^10 to 2^15, so that one of 2^-25 of it still makes a product of
@@ -30,7 +30,7 @@
 //
 // Measured: one token for each of 256 users, lengths to 4096, 32 heads on 8 of 128, bf16 pages:
 // 317 us, 6.6 TB/s, 97% of the copy rate.  One or two tokens for 96 users, lengths 512 to 16384,
-// 32 heads on 4 (16 rows a tile), MXFP8: 181 us, 4.6 TB/s, 68%; the loads alone take 135 us, the
+// 32 heads on 4 (16 rows a tile), MXFP8: 183 us, 4.6 TB/s, 68%; the loads alone take 135 us, the
 // rest is the consumers' latency: registers allow two CTAs an SM.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -430,10 +430,17 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
               float x[4];
               mma_16816_f16_zero(x, a[0], qb[nt][2 * c2][0], qb[nt][2 * c2][1]);
               mma_16816_f16(x, a[1], qb[nt][2 * c2 + 1][0], qb[nt][2 * c2 + 1][1]);
-              s[ks][nt][0] = fmaf(x[0], f0, s[ks][nt][0]);
-              s[ks][nt][1] = fmaf(x[1], f0, s[ks][nt][1]);
-              s[ks][nt][2] = fmaf(x[2], f1, s[ks][nt][2]);
-              s[ks][nt][3] = fmaf(x[3], f1, s[ks][nt][3]);
+              // the key's scale and the row's units in one factor: neither product alone leaves fp32
+              // where the score does not
+              const float2 c = make_float2(cs[nt][0], cs[nt][1]);
+              const float2 y0 = ffma2(make_float2(x[0], x[1]), fmul2(make_float2(f0, f0), c),
+                                      make_float2(s[ks][nt][0], s[ks][nt][1]));
+              const float2 y1 = ffma2(make_float2(x[2], x[3]), fmul2(make_float2(f1, f1), c),
+                                      make_float2(s[ks][nt][2], s[ks][nt][3]));
+              s[ks][nt][0] = y0.x;
+              s[ks][nt][1] = y0.y;
+              s[ks][nt][2] = y1.x;
+              s[ks][nt][3] = y1.y;
             }
           };
           block(0, scale_byte<0>(sk[0]), scale_byte<0>(sk[1]));
@@ -463,7 +470,7 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
             for (int h = 0; h < 2; ++h) {
               float& v = s[ks][nt][2 * h + e];
               const bool sees = ks * 16 + 8 * h + kq < seen;
-              v *= cs[nt][e];
+              if constexpr (!MX) v *= cs[nt][e];
               if constexpr (MX) low[nt][e] = fminf(low[nt][e], sees ? v : INFINITY);
               v = sees ? v : -INFINITY;
               top[nt][e] = fmaxf(top[nt][e], v);

@@ -110,3 +110,15 @@ def test_small_weights_beside_a_key_of_zero_value(kernel, gap, scales):
     b.k_h = decode(b.cache.k, b.cache.k_scale)
     q = q[:, :1].expand(-1, hq, -1).to(torch.bfloat16 if b.dtype == "bf16" else torch.float32).contiguous()
     check_attention(b, hq, q=q, scale=1.0)
+
+
+@kernels
+@pytest.mark.parametrize("low,high,size", [(215, 235, -100), (225, 235, -118), (230, 236, -60), (27, 40, 90)])
+def test_keys_of_any_size_against_queries_of_the_other(kernel, low, high, size):
+    """Huge keys and tiny queries, and the other way round: only a score itself may leave fp32."""
+    b, hq = batch(kernel, seed=8)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    set_scales(b, "k", torch.randint(low, high + 1, b.cache.k_scale.shape, generator=g, device="cuda", dtype=torch.int32))
+    q = torch.randn(b.T, hq, b.dqk, generator=g, device="cuda") * 2.0 ** size
+    mid = 2.0 ** -((low + high) // 2 - 127 + size + 10)
+    check_attention(b, hq, q=q.to(torch.bfloat16 if b.dtype == "bf16" else torch.float32), scale=mid)
