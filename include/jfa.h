@@ -416,7 +416,8 @@ jfa_status jfa_norm_rope_bwd(const jfa_norm_rope_params* p, const void* q, const
  *
  * Every call cuts its work into equal shares on the device (jfa_paged_plan does it once for
  * several calls, which then pass flags = JFA_PLANNED, the same params but for scale and
- * strides, the same offs and lens, unchanged, and the same workspace).  The plan serves
+ * strides, the same offs and lens, unchanged, and the same workspace; on another request's plan
+ * a call's outputs are undefined, and nothing outside them is touched).  The plan serves
  * jfa_cache_write, jfa_cache_read and jfa_paged_fwd.  One workspace must not be used by
  * calls that may run concurrently.
  *

@@ -241,24 +241,18 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
     st = __reduce_max_sync(0xffffffffu, st);
     if (lane == 0) w.hdr->status = st;
   }
-  const PagedPos end = w.pos[c + 1];
-  // no tile is cut here, or the plan is another batch's
-  if (end.blk == 0 || end.b >= p.batch) return;
-  const PagedPos at = w.pos[c];
-  auto same = [&](const PagedPos& x) { return x.b == end.b && x.unit == end.unit && x.tile == end.tile; };
-  if (same(at) && at.blk > 0) return;  // the tile begins in an earlier CTA's share
-  const PagedSeq seq = paged_seq(p, t, end.b);
   // the CTAs that hold the tile's parts: c (slot 1), then c + 1 .. last (slot 0)
-  int last = c + 1;
-  while (last + 1 < ctas && same(w.pos[last + 1])) ++last;
+  PagedCutTile cut;
+  if (!cut.find(p, t, w, ctas, c)) return;
+  const PagedSeq& seq = cut.seq;
+  const int last = cut.last;
   for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < t.rows; r += gridDim.y * kJoinWarps) {
-    const int head_k = end.unit / t.nsub, gh = (end.unit % t.nsub) * t.gsub + r % t.gsub;
-    const int tok = end.tile * t.tokens + r / t.gsub;
-    if (tok >= seq.lq || gh >= p.group) continue;
+    int tok, head;
+    if (!cut.row(p, t, r, tok, head)) continue;
     auto slot_row = [&](int i) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * t.rows + r; };
     auto empty = [&](int i) {  // a CTA without work inside the tile
-      const PagedPos a = w.pos[i], e = w.pos[i + 1];
-      return i != c && same(e) && a.blk >= e.blk;
+      const PagedPos a = paged_pos(p, t, w, i), e = paged_pos(p, t, w, i + 1);
+      return i != c && cut.same(e) && a.blk >= e.blk;
     };
     float m = -INFINITY;
     for (int i = c + lane; i <= last; i += 32)
@@ -276,7 +270,7 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
       for (int k = 0; k < 4; ++k)
         if (lane + 32 * k < p.dim_v) acc[k] = fmaf(w.part_o[pr * p.dim_v + lane + 32 * k], f, acc[k]);
     }
-    const int64_t orow = (int64_t)(seq.q0 + tok) * p.heads_q + head_k * p.group + gh;
+    const int64_t orow = (int64_t)(seq.q0 + tok) * p.heads_q + head;
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll
     for (int k = 0; k < 4; ++k)

@@ -19,8 +19,10 @@ struct PagedSeq {
 __device__ __forceinline__ PagedSeq paged_seq(const Paged& p, const TileShape& t, int b) {
   PagedSeq s;
   const int64_t a = __ldg(p.offs + b), e = __ldg(p.offs + b + 1), l = __ldg(p.lens + b);
+  // (what a plan was not made for and is no batch either has no tokens)
+  const bool ok = a >= 0 && e >= a && e <= p.total_q && l >= 0 && l <= ((int64_t)p.width << p.page_shift);
   s.q0 = (int)a;
-  s.lq = (int)(e - a);
+  s.lq = ok ? (int)(e - a) : 0;
   s.lk = (int)l;
   s.off = l - (e - a);
   s.tiles = (s.lq + t.tokens - 1) / t.tokens;
@@ -105,6 +107,15 @@ __device__ __forceinline__ PagedPos paged_cut(const Paged& p, const TileShape& t
   return r;
 }
 
+// Where CTA c's share begins in the workspace's plan.  A plan of another request may name what this one
+// does not have; such a place is the end, so that whatever the plan, only this request's arrays are met.
+__device__ __forceinline__ PagedPos paged_pos(const Paged& p, const TileShape& t, const PagedWs& w, int c) {
+  const PagedPos x = w.pos[c];
+  if ((x.b | x.unit | x.tile | x.blk) < 0 || x.b >= p.batch || x.unit >= p.heads_k * t.nsub)
+    return PagedPos{(int)p.batch, 0, 0, 0};
+  return x;
+}
+
 // A CTA's share, [pos[0], pos[1]), in shared memory.  With w.ctas > 0 there is no plan (a batch of
 // at most kPlanInCta sequences): every CTA scans the batch by itself, in `scratch` (at least
 // kPlanScratch bytes), and leaves its cut and its status in the workspace for the join.  All
@@ -114,7 +125,7 @@ __device__ __forceinline__ int* paged_share(const Paged& p, const TileShape& t, 
                                             void* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
   if (w.ctas == 0) {
-    if (tid < 2) pos[tid] = w.pos[c + tid];
+    if (tid < 2) pos[tid] = paged_pos(p, t, w, c + tid);
     __syncthreads();
     return &w.hdr->status;
   }
@@ -176,8 +187,7 @@ struct PagedWalk {
   __device__ __forceinline__ bool next(const Paged& p, const TileShape& t, PagedSegment& s) {
     const int units = p.heads_k * t.nsub;
     for (;;) {
-      // (what a plan of another batch may hold stays inside the arrays of this one)
-      if (at.b > end.b || at.b >= p.batch || at.unit >= units) return false;
+      if (at.b > end.b || at.b >= p.batch) return false;
       if (fresh) {
         seq = paged_seq(p, t, at.b);
         fresh = false;
@@ -208,6 +218,36 @@ struct PagedWalk {
       at.blk = 0;
       return true;
     }
+  }
+};
+
+// The tile that the cut at CTA c's end falls into, where its parts begin with CTA c's last one; they
+// go to CTA `last`.
+struct PagedCutTile {
+  PagedPos end;
+  PagedSeq seq;
+  int last;
+  __device__ __forceinline__ bool same(const PagedPos& x) const {
+    return x.b == end.b && x.unit == end.unit && x.tile == end.tile;
+  }
+  // False: no tile is cut here, or it begins in an earlier CTA's share, or the plan is another request's.
+  __device__ __forceinline__ bool find(const Paged& p, const TileShape& t, const PagedWs& w, int ctas, int c) {
+    end = paged_pos(p, t, w, c + 1);
+    if (end.blk == 0 || end.b >= p.batch || c + 1 == ctas) return false;
+    const PagedPos at = paged_pos(p, t, w, c);
+    if (same(at) && at.blk > 0) return false;
+    seq = paged_seq(p, t, end.b);
+    if (end.tile >= seq.tiles) return false;
+    last = c + 1;
+    while (last + 1 < ctas && same(paged_pos(p, t, w, last + 1))) ++last;
+    return true;
+  }
+  // Token and head of row r; false: it has none.
+  __device__ __forceinline__ bool row(const Paged& p, const TileShape& t, int r, int& tok, int& head) const {
+    const int gh = (end.unit % t.nsub) * t.gsub + r % t.gsub;
+    tok = end.tile * t.tokens + r / t.gsub;
+    head = end.unit / t.nsub * p.group + gh;
+    return tok < seq.lq && gh < p.group;
   }
 };
 
