@@ -501,8 +501,11 @@ jfa_status jfa_profile_read(int kind, int64_t* launches, double* total_ms);
  * bf16 forward launch in the calling thread's current context (jfa_fwd,
  * jfa_cross_fwd, jfa_gdpa_fwd and the calls built on them) starts with its MMA
  * issuer waiting on a barrier that nothing arrives on, before any MMA is
- * issued; the call then reports JFA_ERR_TIMEOUT through jfa_status_check and
- * leaves its outputs incomplete.  Off by default; turn it off again before
+ * issued; in the tensor-core kernels of jfa_paged_fwd one role of the first CTA
+ * waits in the same way (a consumer warp of the few-row kernel, an MMA issuer of
+ * the other) while its copies are in flight, in launches of the whole process.
+ * The call then reports JFA_ERR_TIMEOUT through jfa_status_check and leaves its
+ * outputs incomplete.  Off by default; turn it off again before
  * normal use.  Synchronises the device.
  */
 jfa_status jfa_test_hold(int on);

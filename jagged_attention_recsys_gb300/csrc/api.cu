@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "serve.h"
 #include "tc.h"
 #include "timed.h"
 
@@ -737,7 +738,10 @@ const char* jfa_status_string(jfa_status s) {
   return "unknown status";
 }
 
-jfa_status jfa_test_hold(int on) { return cu(tc_set_test_hold(on)); }
+jfa_status jfa_test_hold(int on) {
+  paged_set_test_hold(on);
+  return cu(tc_set_test_hold(on));
+}
 
 jfa_status jfa_profile_enable(int on) {
   prof().on = on != 0;

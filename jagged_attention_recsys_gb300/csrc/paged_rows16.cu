@@ -199,7 +199,7 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
   constexpr bool MX = KIND == kCacheMx;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t full = sb, empty = sb + 8 * NS;
+  const uint32_t full = sb, empty = sb + 8 * NS, hold = sb + 16 * NS + 8;
   volatile int* abort = (volatile int*)(smem_raw + (sb - smem_u32(smem_raw)) + 16 * NS);
   // in the stages' place, before any load
   PagedPos* share = reinterpret_cast<PagedPos*>(smem_raw + (sb - smem_u32(smem_raw)) + L::ML - 32);
@@ -210,6 +210,7 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
       mbar_init(full + 8 * s, MX ? 33 : 1);  // the TMA loads, and every producer lane's scales
       mbar_init(empty + 8 * s, 2);
     }
+    mbar_init(hold, 1);  // test hook: nothing arrives on it
     *abort = 0;
     fence_mbar_init();
   }
@@ -289,7 +290,7 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
   constexpr int MT = DV / 16;      // output tiles
   constexpr int NBK = DQK / 32, NBV = DV / 32;
   // a consumer that gave up in a wait walks on without computing, so that its barriers still match
-  bool dead = false;
+  bool dead = w.hold && blockIdx.x == 0 && warp == 0 && !mbar_wait(hold, 0, abort, status);
   while (walk.next(p, t, g)) {
     const int head_k = g.unit / t.nsub, gs0 = (g.unit % t.nsub) * t.gsub;
     uint32_t qb[NT][DQK / 16][2];

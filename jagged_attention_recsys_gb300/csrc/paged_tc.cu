@@ -75,7 +75,7 @@ struct Layout {
 };
 enum : uint32_t {
   B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PFULL = 6, B_OFULL = 8, B_OEMPTY = 10, B_XCH = 12, B_DRAIN = 13,
-  B_FULL = 15, B_EMPTY = 23, B_RFULL = 31, B_REMPTY = 35, B_VTAIL = 39, B_TURN = 47, B_COUNT = 49
+  B_FULL = 15, B_EMPTY = 23, B_RFULL = 31, B_REMPTY = 35, B_VTAIL = 39, B_TURN = 47, B_HOLD = 49, B_COUNT = 50
 };
 static_assert(8 * B_COUNT + 8 <= 1024 - 32, "front: barriers, then the share");
 constexpr uint32_t T_S = 0, T_O = 256;
@@ -164,6 +164,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
       mbar_init(bar(B_TURN + x), 1);
     }
     mbar_init(bar(B_XCH), 4);
+    mbar_init(bar(B_HOLD), 1);  // test hook: nothing arrives on it
     for (int s = 0; s < NS; ++s) {
       mbar_init(bar(B_FULL + s), MX ? L::kConverters : 1);
       mbar_init(bar(B_EMPTY + s), 2);  // both issuers
@@ -278,7 +279,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
     const int x = warp == kIssuerB;
     const uint32_t t_s = tmem + T_S + x * 128, t_o = tmem + T_O + x * 128;
     uint32_t it = 0, qa_it = 0, qb_it = 0, p_it = 0, o_it = 0, turn = 0;
-    bool ok = true;
+    bool ok = !(w.hold && blockIdx.x == 0 && x == 0) || mbar_wait(bar(B_HOLD), 0, abort, status);
     while (ok && walk.next(p, t, g)) {
       const Streams s = streams_of(p, t, g);
       if (s.blocks == 0) continue;

@@ -96,6 +96,7 @@ constexpr int kPlanScratch = 8 * (kPlanInCta + 1 + 4);
 
 struct PagedWs {
   int ctas;         // 0: pos holds a plan; else the number of CTAs, which cut the work themselves
+  int hold;         // test hook (jfa_test_hold): one role of CTA 0 waits for what never comes
   int* cta_status;  // [n_ctas] errors of CTAs without a plan, for the join
   PagedHeader* hdr;
   PagedPos* pos;   // [n_ctas + 1]
@@ -110,6 +111,9 @@ int paged_kernel(const Paged& p, int dtype);
 TileShape paged_shape(const Paged& p, int kernel);
 int paged_ctas(const Paged& p, int kernel);
 size_t paged_layout(const Paged& p, void* base, PagedWs* out);
+
+// Whether later attention launches are held (jfa_test_hold).
+void paged_set_test_hold(int on);
 
 cudaError_t launch_cache_write(const Paged& p, int dtype, PagedHeader* hdr, int planned, cudaStream_t s);
 cudaError_t launch_cache_read(const Paged& p, int dtype, void* k, void* v, PagedHeader* hdr, int planned,

@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "serve.h"
 #include "timed.h"
@@ -179,9 +181,12 @@ Paged make_paged(const jfa_paged_params* p, const int64_t* offs, const int64_t* 
   return r;
 }
 
+std::atomic<int> g_paged_hold{0};
+
 jfa_status check_ws(const Paged& p, void* ws, size_t bytes, PagedWs* w) {
   if (!ws || ((uintptr_t)ws & 255u) != 0) return JFA_ERR_WORKSPACE;
   if (bytes < paged_layout(p, ws, w)) return JFA_ERR_WORKSPACE;
+  w->hold = g_paged_hold.load(std::memory_order_relaxed);
   return JFA_OK;
 }
 
@@ -198,6 +203,8 @@ jfa_status plan_paged(const Paged& r, int kernel, const PagedWs& w, cudaStream_t
 }
 
 }  // namespace
+
+void paged_set_test_hold(int on) { g_paged_hold.store(on != 0, std::memory_order_relaxed); }
 }  // namespace jfa
 
 using namespace jfa;
