@@ -389,7 +389,8 @@ jfa_status jfa_norm_rope_bwd(const jfa_norm_rope_params* p, const void* q, const
  * Index arrays live on the device.  jfa_paged_plan and every call without JFA_PLANNED
  * reset the workspace's status word; invalid offs or lens outside [0, max_pages *
  * page_size] give JFA_ERR_BAD_OFFSETS, and a page index outside [0, pages) that a call
- * meets JFA_ERR_BAD_PAGES.  jfa_paged_fwd computes nothing on the former.  Rows behind a
+ * meets JFA_ERR_BAD_PAGES, unless it has the former or JFA_ERR_TIMEOUT to report.  jfa_paged_fwd
+ * computes nothing on the former.  Rows behind a
  * bad page are not written, are read as zeros, and count as zero keys and values.  Nothing
  * outside the buffers is touched.  Pages' rows behind a sequence's length are never
  * read as values (they may hold anything).

@@ -235,11 +235,13 @@ template <typename T>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, const PagedWs w) {
   const int c = blockIdx.x, lane = threadIdx.x & 31;
-  if (w.ctas > 0 && c == 0 && blockIdx.y == 0 && threadIdx.x < 32) {  // the CTAs' errors: the call's
+  if (w.ctas > 0 && c == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
+    // the call's error: a timeout of any CTA, else an invalid batch, else a bad page
+    static_assert(JFA_OK < 1 && 1 < JFA_ERR_BAD_OFFSETS && JFA_ERR_BAD_OFFSETS < JFA_ERR_TIMEOUT, "ranks");
     int st = 0;
-    for (int i = lane; i < w.ctas; i += 32) st = max(st, w.cta_status[i]);
+    for (int i = lane; i < w.ctas; i += 32) st = max(st, w.cta_status[i] == JFA_ERR_BAD_PAGES ? 1 : w.cta_status[i]);
     st = __reduce_max_sync(0xffffffffu, st);
-    if (lane == 0) w.hdr->status = st;
+    if (lane == 0) w.hdr->status = st == 1 ? (int)JFA_ERR_BAD_PAGES : st;
   }
   // the CTAs that hold the tile's parts: c (slot 1), then c + 1 .. last (slot 0)
   PagedCutTile cut;

@@ -251,11 +251,12 @@ struct PagedCutTile {
   }
 };
 
-// Page of a position, or -1 for an index outside the cache (recorded in the status word).
+// Page of a position, or -1 for an index outside the cache (recorded in the status word, where a
+// timeout or an invalid batch stays).
 __device__ __forceinline__ int paged_page(const Paged& p, int b, int pos, int* status) {
   const int page = __ldg(p.table + (int64_t)b * p.width + (pos >> p.page_shift));
   if ((uint32_t)page >= (uint64_t)p.pages) {
-    atomicExch(status, (int)JFA_ERR_BAD_PAGES);
+    atomicCAS(status, (int)JFA_OK, (int)JFA_ERR_BAD_PAGES);
     return -1;
   }
   return page;

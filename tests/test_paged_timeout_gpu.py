@@ -43,3 +43,25 @@ def test_a_wait_that_runs_out(kind, cache, hq, planned):
         jfa.jfa_paged_plan(q, *b.args(), ws=ws)
     check_attention(b, hq, q=q, ws=ws, planned=planned)
     assert jfa.jfa_status_check(ws) == jfa.JFA_OK
+
+
+@pytest.mark.parametrize("planned", [False, True])
+@pytest.mark.parametrize("kind,cache,hq", KERNELS)
+def test_a_timeout_is_reported_ahead_of_bad_pages(kind, cache, hq, planned):
+    """A bad page says that everything else was computed, so an incomplete call must not report one:
+    bad pages in the first CTA's sequence and in others'."""
+    b, ws = held(kind, cache, hq)
+    b.table[0, 3] = -1
+    b.table[1, 5] = b.pages
+    q = torch.randn(b.T, hq, 128, device="cuda").bfloat16()
+    if planned:
+        jfa.jfa_paged_plan(q, *b.args(), ws=ws)
+    jfa.jfa_paged_fwd(q, *b.args(), ws=ws, planned=planned)
+    assert jfa.jfa_status_check(ws) == jfa.JFA_ERR_BAD_PAGES
+    jfa.jfa_test_hold(True)
+    try:
+        jfa.jfa_paged_fwd(q, *b.args(), ws=ws, planned=planned)
+        st = jfa.jfa_status_check(ws)
+    finally:
+        jfa.jfa_test_hold(False)
+    assert st == jfa.JFA_ERR_TIMEOUT, jfa.status_string(st)
