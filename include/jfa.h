@@ -315,8 +315,9 @@ jfa_status jfa_block_rope_bwd(const jfa_params* p, const void* q, const void* k,
  *                    (turns_fast - turns_slow), 0, 1), n_i = orig_len theta_i / 2 pi the
  *                    turns pair i makes over the trained context; the method's
  *                    temperature is the caller's choice of amp.
- * pos is int64 [T] on the device, any values (negative too); the angle is exact to
- * |pos| 2^-64 turns.
+ * pos is int64 [T] on the device, any values (negative too).  Frequencies are worked out in
+ * 64-bit floating point, so an angle is within |pos| 2^-53 turns (7e-10 rad at position 10^6,
+ * 7e-7 at 10^9) besides fp32 rounding.
  *
  * Strides are in elements between tokens; a token's heads are contiguous, [heads, dim].
  * heads_q or heads_k may be 0 (that tensor is then absent).  yq may be q (and yk be k)

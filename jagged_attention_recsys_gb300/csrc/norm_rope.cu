@@ -9,10 +9,10 @@
 // Bound: HBM.  Each value is read once and written once (the backward reads x and dy and
 // recomputes r), about 12 to 21 lane instructions a value against the 21 a value the SMs
 // can issue at the copy bandwidth, so the arithmetic has to stay lean:
-//  * Angles.  The frequencies come as 64-bit binary fractions of a turn.  pos times such a
-//    fraction modulo one turn is the low half of an integer product, exact to |pos| 2^-64
-//    turns (position 10^9: 5e-11), with no 64-bit floating point and no range reduction;
-//    sincospif of the top 32 bits then gives cos and sin to about 1e-7.
+//  * Angles.  The frequencies come as 64-bit binary fractions of a turn, made on the host from
+//    doubles (within 2^-53 turns).  pos times such a fraction modulo one turn is the low half
+//    of an integer product, which loses no more, with no 64-bit floating point and no range
+//    reduction; sincospif of the top 32 bits then gives cos and sin to about 1e-7.
 //  * A row is D/16 lane slots of 16 values (two 16-byte loads in bf16).  A slot holds whole
 //    pairs in both layouts, so the rotation needs no exchange between lanes, and a lane's
 //    slot is the same in every row it touches: its (cos, sin) are computed once a token
