@@ -215,6 +215,23 @@ __device__ __forceinline__ void move_rows(T* x, int64_t stride, uint8_t* cache, 
   }
 }
 
+// The whole batch's description, once per call without a plan, cut over the grid.
+__device__ __forceinline__ void check_batch(const Paged& p, PagedHeader* hdr) {
+  const int64_t most = (int64_t)p.width << p.page_shift;
+  for (int64_t b = (int64_t)blockIdx.x * kThreads + threadIdx.x; b < p.batch; b += (int64_t)gridDim.x * kThreads) {
+    const int64_t lo = __ldg(p.offs + b), hi = __ldg(p.offs + b + 1), len = __ldg(p.lens + b);
+    if (hi < lo || (b == 0 && lo != 0) || (b == p.batch - 1 && hi != p.total_q) || len < 0 || len > most)
+      atomicExch(&hdr->status, (int)JFA_ERR_BAD_OFFSETS);
+  }
+}
+
+// A call without tokens has its batch checked all the same.
+__global__ void __launch_bounds__(kThreads)
+cache_check_kernel(const __grid_constant__ Paged p, PagedHeader* hdr) {
+  if (p.batch == 0 && __ldg(p.offs) != 0) hdr->status = JFA_ERR_BAD_OFFSETS;
+  check_batch(p, hdr);
+}
+
 template <typename T, int KIND, bool WRITE>
 __global__ void __launch_bounds__(kThreads, kCtas<WRITE>)
 cache_kernel(const __grid_constant__ Paged p, T* k_out, T* v_out, PagedHeader* hdr, int run, int parts, int planned) {
@@ -223,14 +240,7 @@ cache_kernel(const __grid_constant__ Paged p, T* k_out, T* v_out, PagedHeader* h
   // a plan that found the batch invalid: nothing is computed (page errors do not stop the call,
   // so the check does not depend on what other CTAs have met so far)
   if (planned && *(volatile int*)&hdr->status == (int)JFA_ERR_BAD_OFFSETS) return;
-  if (!planned) {  // the whole batch's description, once per call
-    const int64_t most = (int64_t)p.width << p.page_shift;
-    for (int64_t b = (int64_t)blockIdx.x * kThreads + threadIdx.x; b < p.batch; b += (int64_t)gridDim.x * kThreads) {
-      const int64_t lo = __ldg(p.offs + b), hi = __ldg(p.offs + b + 1), len = __ldg(p.lens + b);
-      if (hi < lo || (b == 0 && lo != 0) || (b == p.batch - 1 && hi != p.total_q) || len < 0 || len > most)
-        atomicExch(&hdr->status, (int)JFA_ERR_BAD_OFFSETS);
-    }
-  }
+  if (!planned) check_batch(p, hdr);
   const int lane = threadIdx.x & 31;
   const int perk = p.dim_qk / W, perv = p.dim_v / W;  // pieces of a head
   const int ck = p.heads_k * perk, cv = p.heads_k * perv;
@@ -278,7 +288,12 @@ cudaError_t launch_t(const Paged& p, void* k, void* v, PagedHeader* hdr, int pla
 }
 template <bool WRITE>
 cudaError_t launch_kind(const Paged& p, int dtype, void* k, void* v, PagedHeader* hdr, int planned, cudaStream_t s) {
-  if (p.total_q == 0) return cudaSuccess;
+  if (p.total_q == 0) {
+    if (planned) return cudaSuccess;
+    const int64_t need = (p.batch + kThreads - 1) / kThreads, cap = num_sms();
+    cache_check_kernel<<<(unsigned)(need < 1 ? 1 : need < cap ? need : cap), kThreads, 0, s>>>(p, hdr);
+    return cudaGetLastError();
+  }
   if (dtype == JFA_BF16)
     return p.kind == kCacheMx ? launch_t<__nv_bfloat16, kCacheMx, WRITE>(p, k, v, hdr, planned, s)
                               : launch_t<__nv_bfloat16, kCacheBf16, WRITE>(p, k, v, hdr, planned, s);
