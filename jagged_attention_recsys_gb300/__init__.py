@@ -529,7 +529,7 @@ def _in_stream(fn):
 
 def _rows(name, t, dtype, device, heads=None, dim=None, tokens=None):
     """Checks [T, heads, dim] rows with contiguous heads; returns the stride between tokens."""
-    if t.dim() != 3 or t.dtype is not dtype or t.device != device:
+    if t is None or t.dim() != 3 or t.dtype is not dtype or t.device != device:
         raise ValueError("%s must be a [tokens, heads, dim] %s tensor on %s" % (name, dtype, device))
     T, H, D = t.shape
     if heads not in (None, H) or dim not in (None, D) or tokens not in (None, T):
@@ -542,7 +542,7 @@ def _rows(name, t, dtype, device, heads=None, dim=None, tokens=None):
 
 
 def _plain(name, t, dtype, shape, device):
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t is None or t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
                          % (name, dtype, tuple(shape), device))
 
@@ -570,7 +570,7 @@ def _norm_rope_params(q, k, pos, wq, wk, eps, rope, norm):
         raise ValueError("norm=False takes no weights")
     (T, _, D), dtype, dev = x.shape, x.dtype, x.device
     sq = hq = sk = hk = 0
-    if rope is not None:
+    if rope is not None and rope.dim:
         _plain("pos", pos, torch.int64, (T,), dev)
     if q is not None:
         sq, hq = _rows("q", q, dtype, dev, None, D, T), q.shape[1]
