@@ -19,19 +19,21 @@
 // MXFP8.  Codes are exact in fp16, and a row of bf16 queries times a power of two that brings
 // its largest value to [2^14, 2^15) is exact in fp16 too (values under 2^-31 of the largest lose
 // at most 2^-39 of it), so the scores are fp16 products of codes, one block of 32 columns at a
-// time, and a block's scale times the row's own power of two multiplies its fp32 sum.  For the output the scales go to the
-// weights: a block of columns has a reference scale, the largest it met (O is kept in its
-// units), and the weights, rounded to fp16, times scale / reference, at most 1, meet fp16 codes.
-// The largest weight is kept at 2^10 to 2^15, so that one of 2^-25 of it still makes a product of
-// 2^-15, which its two roundings to steps of 2^-24 leave within 2^-9.  A stage
-// where a weight times a scale may be less takes its values to bf16 instead (exact) and
-// rounds the weights alone, to bf16: keys of small weights or values keep their precision beside
-// keys of large ones whose values are zero.
+// time, and a block's scale times the row's own power of two multiplies its fp32 sum.  For the
+// output the scales go to the weights: a block of columns has a reference scale, the largest it met
+// (O is kept in its units), and the weights, rounded to fp16, times scale / reference, at most 1,
+// meet fp16 codes.  The largest weight is kept at 2^10 to 2^15, so that one of 2^-25 of it still makes
+// a product of 2^-15, which its two roundings to steps of 2^-24 leave within 2^-9.  A stage where a
+// weight times a scale may be less takes its values to bf16 instead (exact) and rounds the weights
+// alone, to bf16: keys of small weights or values keep their precision beside keys of large ones
+// whose values are zero.
 //
 // Measured: one token for each of 256 users, lengths to 4096, 32 heads on 8 of 128, bf16 pages:
 // 317 us, 6.6 TB/s, 97% of the copy rate.  One or two tokens for 96 users, lengths 512 to 16384,
 // 32 heads on 4 (16 rows a tile), MXFP8: 183 us, 4.6 TB/s, 68%; the loads alone take 135 us, the
-// rest is the consumers' latency: registers allow two CTAs an SM.
+// rest is the consumers' latency: registers allow two CTAs an SM.  With scores of three times the
+// spread nearly every stage takes its values to bf16: 228 us (weights scaled in bf16 against codes
+// in bf16 instead: 222 us, but 189 us for scores of the usual spread).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -531,23 +533,31 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
 #pragma unroll
         for (int i = 0; i < NBV; ++i) out |= (uint32_t)(ref_scale[i] - (int)((mine >> (8 * i)) & 255)) > 4u;
         if (__any_sync(0xffffffffu, out)) {
+          bool above = false;
+#pragma unroll
+          for (int i = 0; i < NBV; ++i) above |= (int)((mine >> (8 * i)) & 255) > ref_scale[i];
+          if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+            for (int i = 0; i < NBV; ++i) {
+              const int most = __reduce_max_sync(0xffffffffu, min((mine >> (8 * i)) & 255, 254u));
+              if (most > ref_scale[i]) {  // O of the block goes to the new units, with a step to spare
+                const int to = min(most + 1, 254);
+                const float f = ref_scale[i] == 0 ? 1.f : exp2i(max(ref_scale[i] - to, -126));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    o[nt][2 * i][k] *= f;
+                    o[nt][2 * i + 1][k] *= f;
+                  }
+                ref_scale[i] = to;
+              }
+            }
+          }
           int gap = 0;  // steps (log2) of this key's scales under their references
 #pragma unroll
           for (int i = 0; i < NBV; ++i) {
             const int e = (mine >> (8 * i)) & 255;
-            const int most = __reduce_max_sync(0xffffffffu, min(e, 254));
-            if (most > ref_scale[i]) {  // O of the block goes to the new units, with a step to spare
-              const int to = min(most + 1, 254);
-              const float f = ref_scale[i] == 0 ? 1.f : exp2i(max(ref_scale[i] - to, -126));
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  o[nt][2 * i][k] *= f;
-                  o[nt][2 * i + 1][k] *= f;
-                }
-              ref_scale[i] = to;
-            }
             if (e != 0) gap = max(gap, ref_scale[i] - e);
           }
           gap = __reduce_max_sync(0xffffffffu, gap);
