@@ -314,7 +314,9 @@ jfa_status jfa_block_rope_bwd(const jfa_params* p, const void* q, const void* k,
  *   JFA_ROPE_YARN    theta_i (g + (1 - g) / factor), g = clamp((n_i - turns_slow) /
  *                    (turns_fast - turns_slow), 0, 1), n_i = orig_len theta_i / 2 pi the
  *                    turns pair i makes over the trained context; the method's
- *                    temperature is the caller's choice of amp.
+ *                    temperature is the caller's choice of amp.  (The ramp is over turns;
+ *                    a ramp over the pair's index between rounded bounds, which some models
+ *                    were trained with, cannot be expressed, nor a table of frequencies.)
  * pos is int64 [T] on the device, any values (negative too).  Frequencies are worked out in
  * 64-bit floating point, so an angle is within |pos| 2^-53 turns (7e-10 rad at position 10^6,
  * 7e-7 at 10^9) besides fp32 rounding.
@@ -332,6 +334,8 @@ jfa_status jfa_block_rope_bwd(const jfa_params* p, const void* q, const void* k,
  *
  * Values are fp32 or bf16 (dtype), pointers aligned to a value; pointers and strides of
  * whole 16 bytes (fp32: 32) with dim and rope.dim multiples of 16 take the fast kernels.
+ * Sums are fp32: a row's sum of squares has to stay in its range (with larger values y is 0,
+ * and with eps = 0 rows of values under 2^-63 lose precision).
  * dim <= 256 and tokens <= 2^31 - 1, else JFA_ERR_UNSUPPORTED.  The forward needs no
  * workspace; the backward's (256-byte aligned, jfa_norm_rope_workspace_size; 0 for bad params) is scratch
  * without a status word.  The library finds no errors on the device here.
@@ -378,7 +382,7 @@ jfa_status jfa_norm_rope_bwd(const jfa_norm_rope_params* p, const void* q, const
  * (offs int64 [B+1], a jagged layout as elsewhere) are the last ones of their sequences,
  * token i of sequence b at position lens[b] - L_b + i, L_b = offs[b+1] - offs[b].
  * Where L_b > lens[b] the first tokens come before the cache's start: they are not
- * written, read back as zeros, and see no keys.
+ * written, read back as zeros, and see no keys under the causal mask.
  *
  * The cache holds the values' own type, or MXFP8 (cache_dtype JFA_MXFP8): e4m3 codes,
  * one byte a value, with k_scale [pages, Hk, page_size, Dqk / 32] and v_scale likewise,
@@ -400,7 +404,8 @@ jfa_status jfa_norm_rope_bwd(const jfa_norm_rope_params* p, const void* q, const
  * strides stride_k, stride_v; any slice of a projection's output) into their pages.  Two
  * tokens of a call that share a slot leave either's row, in parts.  jfa_cache_read
  * gathers the same tokens' rows back into contiguous k [T, Hk, Dqk], v [T, Hk, Dv]
- * (L_b = lens[b] reads whole sequences); MXFP8 values are exact in fp32 and bf16.
+ * (L_b = lens[b] reads whole sequences); MXFP8 values are exact in fp32, and
+ * in bf16 with scales of at least 3; values past fp32 (scales above 246) become infinite.
  *
  * jfa_paged_fwd: softmax attention of the new tokens' queries q [T, Hq, Dqk] (token
  * stride stride_q) over their sequences' cached keys, from one token a sequence to whole
@@ -425,8 +430,11 @@ jfa_status jfa_norm_rope_bwd(const jfa_norm_rope_params* p, const void* q, const
  *
  * Limits (JFA_ERR_UNSUPPORTED): dims multiples of 8 (MXFP8: 32), at most 256, in
  * jfa_paged_fwd 128; cache_dtype the values' type or JFA_MXFP8; max_pages * page_size and
- * total_q at most 2^31 - 256, batch and pages 2^31 - 1.  k, v, q and the caches are 16-byte aligned
- * with strides of whole 16 bytes.
+ * total_q at most 2^31 - 256, batch and pages 2^31 - 1.  k, v, q, o, lse and the caches are 16-byte
+ * aligned, with strides of whole 16 bytes.  The tensor-core kernels serve bf16 at dims of 64 and
+ * 128; fp32 and other dims take a CUDA-core kernel, some 40 times slower for single tokens and
+ * 200 to 360 times for prompts.  The workspace is
+ * about 22 MB for values of 64 columns and 43 MB for 128, whatever the batch.
  */
 typedef struct {
   int64_t batch;   /* B >= 0 */

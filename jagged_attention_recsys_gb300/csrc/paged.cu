@@ -79,10 +79,7 @@ paged_plan_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
   }
   const int64_t W = carry_s;
   const bool bad = bad_s != 0;
-  if (tid == 0) {
-    w.hdr->status = bad ? JFA_ERR_BAD_OFFSETS : JFA_OK;
-    w.hdr->n_ctas = ctas;
-  }
+  if (tid == 0) w.hdr->status = bad ? JFA_ERR_BAD_OFFSETS : JFA_OK;
   for (int c = tid; c <= ctas; c += kPlanThreads) w.pos[c] = paged_cut(p, t, ctas, c, cum, W, bad);
 }
 

@@ -69,8 +69,7 @@ struct __align__(16) PagedPos {
 // Header of the workspace (offset 0); the first word is the status, as in every workspace.
 struct PagedHeader {
   int status;
-  int n_ctas;  // CTAs the work is cut for
-  int pad[62];
+  int pad[63];
 };
 static_assert(sizeof(PagedHeader) == 256, "workspace header");
 
