@@ -470,6 +470,54 @@ jfa_status jfa_paged_fwd(const jfa_paged_params* p, const void* q, const void* k
                          float* lse, void* ws, size_t ws_bytes, jfa_stream_t stream);
 
 /*
+ * Attention over a sliding window of a paged cache, with sinks: jfa_paged_fwd in which a query at
+ * position x sees, of the keys y <= x, those with x - y < window and those with y < sinks (the
+ * sequence's first, which stay visible).  window >= 1, sinks >= 0, causal = 1 (0:
+ * JFA_ERR_UNSUPPORTED); otherwise arguments, results, limits, workspace and errors are those of
+ * jfa_paged_fwd, and a plan is one for the same window and sinks (jfa_paged_window_plan, never
+ * jfa_paged_plan's).  Work and bytes grow with the window, not with the cache.  Pages that no query
+ * of the call reaches are not looked up: their table entries may be anything, so a program may free
+ * what has left the window.  Keys and values that no query of a sequence's call sees may hold
+ * anything even inside a page that is read; where some of its queries see them, they must be finite.
+ */
+jfa_status jfa_paged_window_plan(const jfa_paged_params* p, int32_t window, int32_t sinks,
+                                 const int64_t* offs, const int64_t* lens, void* ws, size_t ws_bytes,
+                                 jfa_stream_t stream);
+jfa_status jfa_paged_window_fwd(const jfa_paged_params* p, int32_t window, int32_t sinks,
+                                const void* q, const void* k_cache, const void* v_cache,
+                                const uint8_t* k_scale, const uint8_t* v_scale, const int64_t* offs,
+                                const int64_t* lens, const int32_t* table, void* o, float* lse,
+                                void* ws, size_t ws_bytes, jfa_stream_t stream);
+
+/*
+ * Attention of many sequences behind shared prefixes, over one paged cache: candidates scored
+ * against a user's history, continuations of one prompt.  The batch's sequences come in groups:
+ * group g is the sequences group_offs[g] .. group_offs[g + 1] - 1 (int64 [groups + 1], from 0 to
+ * p->batch, non-decreasing), whose tokens all see the group's prefix, the prefix_lens[g] (int64)
+ * positions of the pages prefix_table[g] (int32 [groups, prefix_pages]).  offs, lens and table
+ * describe the sequences' own tokens and cached keys as in jfa_paged_fwd, positions counted from
+ * the first behind the prefix: token i of sequence b sees the whole prefix and its own positions
+ * <= lens[b] - L_b + i (causal = 1; 0: all lens[b]).  lens may be 0: queries that are not cached see
+ * the prefix alone.  A row that sees no key gets o = 0, lse = -inf.
+ *
+ * The prefix is read once for every 256 query rows of its group that share a key head (a group's
+ * average of 16 rows or less: 8 or 16), not once a sequence.  Two passes: the groups' rows over the prefixes,
+ * whose results stay in fp32, and the rows over their own keys, which joins them.
+ *
+ * Types, limits and errors are those of jfa_paged_fwd (prefix_pages * page_size like max_pages *
+ * page_size; invalid group_offs or prefix_lens: JFA_ERR_BAD_OFFSETS, nothing is computed).
+ * JFA_PLANNED: JFA_ERR_UNSUPPORTED.  The workspace is jfa_shared_workspace_size's (256-byte aligned;
+ * 0 for bad params): the one of jfa_paged_fwd and total_q * heads_q * (dim_v + 1) floats.
+ */
+size_t jfa_shared_workspace_size(const jfa_paged_params* p, int64_t groups, int32_t prefix_pages);
+jfa_status jfa_shared_fwd(const jfa_paged_params* p, int64_t groups, int32_t prefix_pages,
+                          const void* q, const void* k_cache, const void* v_cache,
+                          const uint8_t* k_scale, const uint8_t* v_scale, const int64_t* offs,
+                          const int64_t* lens, const int32_t* table, const int64_t* group_offs,
+                          const int64_t* prefix_lens, const int32_t* prefix_table, void* o, float* lse,
+                          void* ws, size_t ws_bytes, jfa_stream_t stream);
+
+/*
  * Synchronises `stream`, then returns the device status word of the last
  * call that used `ws` (JFA_OK, JFA_ERR_BAD_OFFSETS, JFA_ERR_BAD_PAGES or
  * JFA_ERR_TIMEOUT), or JFA_ERR_CUDA if the synchronisation itself failed.

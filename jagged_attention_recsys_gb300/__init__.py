@@ -51,7 +51,8 @@ EXPORTS = ("jfa_workspace_size", "jfa_fwd", "jfa_bwd", "jfa_cross_fwd", "jfa_cro
            "jfa_test_hold", "jfa_block_rope_fwd", "jfa_block_rope_bwd", "jfa_plan",
            "jfa_block_plan", "jfa_norm_rope_workspace_size", "jfa_norm_rope_fwd",
            "jfa_norm_rope_bwd", "jfa_paged_workspace_size", "jfa_cache_write", "jfa_cache_read",
-           "jfa_paged_plan", "jfa_paged_fwd")
+           "jfa_paged_plan", "jfa_paged_fwd", "jfa_paged_window_plan", "jfa_paged_window_fwd",
+           "jfa_shared_workspace_size", "jfa_shared_fwd")
 
 
 class JfaError(RuntimeError):
@@ -171,8 +172,14 @@ def lib():
         L.jfa_cache_read.argtypes = [G] + [vp] * 10 + [sz, vp]
         L.jfa_paged_plan.argtypes = [G, vp, vp, vp, sz, vp]
         L.jfa_paged_fwd.argtypes = [G] + [vp] * 11 + [sz, vp]
+        L.jfa_paged_window_plan.argtypes = [G, i32, i32, vp, vp, vp, sz, vp]
+        L.jfa_paged_window_fwd.argtypes = [G, i32, i32] + [vp] * 11 + [sz, vp]
+        L.jfa_shared_workspace_size.argtypes = [G, ctypes.c_int64, i32]
+        L.jfa_shared_workspace_size.restype = sz
+        L.jfa_shared_fwd.argtypes = [G, ctypes.c_int64, i32] + [vp] * 14 + [sz, vp]
         for f in ("jfa_norm_rope_fwd", "jfa_norm_rope_bwd", "jfa_cache_write", "jfa_cache_read",
-                  "jfa_paged_plan", "jfa_paged_fwd"):
+                  "jfa_paged_plan", "jfa_paged_fwd", "jfa_paged_window_plan", "jfa_paged_window_fwd",
+                  "jfa_shared_fwd"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -703,7 +710,7 @@ def paged_workspace(p: jfa_paged_params, device="cuda") -> torch.Tensor:
                        device=device)
 
 
-def _paged_prep(cache, table, offs, lens, total, dtype, heads_q, scale, causal, ws, planned):
+def _paged_prep(cache, table, offs, lens, total, dtype, heads_q, scale, causal, ws, planned, make=None):
     dev = cache.device
     if offs.dim() != 1 or table.dim() != 2 or offs.numel() < 1:
         raise ValueError("offs must be [B + 1], table [B, max_pages]")
@@ -717,7 +724,7 @@ def _paged_prep(cache, table, offs, lens, total, dtype, heads_q, scale, causal, 
             raise ValueError("a planned call needs the workspace its plan was built in")
         p.flags = JFA_PLANNED
     if ws is None:
-        ws = paged_workspace(p, dev)
+        ws = make(p) if make else paged_workspace(p, dev)
     elif ws.device != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous uint8 tensor on %s" % dev)
     return p, ws
@@ -772,6 +779,19 @@ def jfa_paged_plan(q, cache, table, offs, lens, *, causal=True, ws=None, stream=
     return ws
 
 
+def _paged_outputs(q, cache, o, lse):
+    dev, (T, H, _) = cache.device, q.shape
+    if o is None:
+        o = _rows_like(q) if cache.dim_v == cache.dim_qk else torch.empty((T, H, cache.dim_v), dtype=q.dtype, device=dev)
+    else:
+        _plain("o", o, q.dtype, (T, H, cache.dim_v), dev)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _plain("lse", lse, torch.float32, (T, H), dev)
+    return o, lse
+
+
 @_in_stream
 def jfa_paged_fwd(q, cache, table, offs, lens, *, scale=None, causal=True, o=None, lse=None, ws=None,
                   stream=None, planned=False):
@@ -782,16 +802,79 @@ def jfa_paged_fwd(q, cache, table, offs, lens, *, scale=None, causal=True, o=Non
     stride_q = _rows("q", q, q.dtype, dev, None, cache.dim_qk)
     p, ws = _paged_prep(cache, table, offs, lens, q.shape[0], q.dtype, q.shape[1], scale, causal, ws, planned)
     p.stride_q = stride_q
-    T, H = q.shape[0], q.shape[1]
-    if o is None:
-        o = _rows_like(q) if cache.dim_v == cache.dim_qk else torch.empty((T, H, cache.dim_v), dtype=q.dtype, device=dev)
-    else:
-        _plain("o", o, q.dtype, (T, H, cache.dim_v), dev)
-    if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    else:
-        _plain("lse", lse, torch.float32, (T, H), dev)
+    o, lse = _paged_outputs(q, cache, o, lse)
     _check(lib().jfa_paged_fwd(ctypes.byref(p), _addr(q), _addr(cache.k), _addr(cache.v), _addr(cache.k_scale),
                                _addr(cache.v_scale), _addr(offs), _addr(lens), _addr(table), _addr(o),
                                _addr(lse), _addr(ws), ws.numel(), _on(dev)), "jfa_paged_fwd")
+    return o, lse
+
+
+# ----------------------------------------------------------------------------- windows, shared prefixes
+def _int32(name, x, least):
+    """A window or a number of sinks; what passes 32 bits is as good as the largest."""
+    x = int(x)
+    if x < least:
+        raise ValueError("%s must be at least %d, got %d" % (name, least, x))
+    return min(x, 2 ** 31 - 1)
+
+
+@_in_stream
+def jfa_paged_window_plan(q, cache, table, offs, lens, window, *, sinks=0, ws=None, stream=None):
+    """jfa_paged_plan for the calls of jfa_paged_window_fwd with this window and these sinks."""
+    window, sinks = _int32("window", window, 1), _int32("sinks", sinks, 0)
+    stride_q = _rows("q", q, q.dtype, cache.device, None, cache.dim_qk)
+    p, ws = _paged_prep(cache, table, offs, lens, q.shape[0], q.dtype, q.shape[1], None, True, ws, False)
+    p.stride_q = stride_q
+    _check(lib().jfa_paged_window_plan(ctypes.byref(p), window, sinks, _addr(offs), _addr(lens), _addr(ws), ws.numel(),
+                                       _on(cache.device)), "jfa_paged_window_plan")
+    return ws
+
+
+@_in_stream
+def jfa_paged_window_fwd(q, cache, table, offs, lens, window, *, sinks=0, scale=None, o=None, lse=None, ws=None,
+                         stream=None, planned=False):
+    """jfa_paged_fwd in which a query sees the last ``window`` keys up to its own position and the
+    first ``sinks`` of its sequence; returns (o [T, Hq, Dv], lse [T, Hq])."""
+    window, sinks = _int32("window", window, 1), _int32("sinks", sinks, 0)
+    dev = cache.device
+    stride_q = _rows("q", q, q.dtype, dev, None, cache.dim_qk)
+    p, ws = _paged_prep(cache, table, offs, lens, q.shape[0], q.dtype, q.shape[1], scale, True, ws, planned)
+    p.stride_q = stride_q
+    o, lse = _paged_outputs(q, cache, o, lse)
+    _check(lib().jfa_paged_window_fwd(ctypes.byref(p), window, sinks, _addr(q), _addr(cache.k), _addr(cache.v),
+                                      _addr(cache.k_scale), _addr(cache.v_scale), _addr(offs), _addr(lens), _addr(table),
+                                      _addr(o), _addr(lse), _addr(ws), ws.numel(), _on(dev)), "jfa_paged_window_fwd")
+    return o, lse
+
+
+def shared_workspace(p: jfa_paged_params, groups, prefix_pages, device="cuda") -> torch.Tensor:
+    """A workspace of jfa_shared_fwd for params p (paged_params), ``groups`` groups and prefixes of at most
+    ``prefix_pages`` pages."""
+    n = int(lib().jfa_shared_workspace_size(ctypes.byref(p), int(groups), int(prefix_pages)))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+@_in_stream
+def jfa_shared_fwd(q, cache, table, offs, lens, prefix_table, prefix_lens, groups, *, scale=None, causal=True, o=None,
+                   lse=None, ws=None, stream=None):
+    """Attention of sequences that share cached prefixes.  Group g is the sequences groups[g] ..
+    groups[g + 1] - 1 (int64 [G + 1]); all its tokens see the prefix_lens[g] (int64) positions of the
+    pages prefix_table[g] (int32 [G, max_pages]), and behind them what jfa_paged_fwd shows them of
+    their sequences' own keys; returns (o [T, Hq, Dv], lse [T, Hq])."""
+    dev = cache.device
+    stride_q = _rows("q", q, q.dtype, dev, None, cache.dim_qk)
+    if groups.dim() != 1 or prefix_table.dim() != 2 or groups.numel() < 1:
+        raise ValueError("groups must be [G + 1], prefix_table [G, max_pages]")
+    G, W = groups.numel() - 1, prefix_table.shape[1]
+    _plain("groups", groups, torch.int64, (G + 1,), dev)
+    _plain("prefix_lens", prefix_lens, torch.int64, (G,), dev)
+    _plain("prefix_table", prefix_table, torch.int32, (G, W), dev)
+    p, ws = _paged_prep(cache, table, offs, lens, q.shape[0], q.dtype, q.shape[1], scale, causal, ws, False,
+                        lambda p: shared_workspace(p, G, W, dev))
+    p.stride_q = stride_q
+    o, lse = _paged_outputs(q, cache, o, lse)
+    _check(lib().jfa_shared_fwd(ctypes.byref(p), G, W, _addr(q), _addr(cache.k), _addr(cache.v), _addr(cache.k_scale),
+                                _addr(cache.v_scale), _addr(offs), _addr(lens), _addr(table), _addr(groups),
+                                _addr(prefix_lens), _addr(prefix_table), _addr(o), _addr(lse), _addr(ws), ws.numel(),
+                                _on(dev)), "jfa_shared_fwd")
     return o, lse

@@ -22,6 +22,7 @@
 #include <stdint.h>
 
 #include "paged.cuh"
+#include "paged_join.cuh"
 
 namespace jfa {
 namespace {
@@ -44,7 +45,7 @@ paged_plan_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
   int64_t* cum = B <= kPlanSmemSeqs ? smem_cum : w.cum;
   if (tid == 0) {
     carry_s = 0;
-    bad_s = B == 0 && p.offs[0] != 0;
+    bad_s = (B == 0 && p.offs[0] != 0) || (p.phase == 2 && prior_failed(p));
     cum[0] = 0;
   }
   __syncthreads();
@@ -79,7 +80,7 @@ paged_plan_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
   }
   const int64_t W = carry_s;
   const bool bad = bad_s != 0;
-  if (tid == 0) w.hdr->status = bad ? JFA_ERR_BAD_OFFSETS : JFA_OK;
+  if (tid == 0) w.hdr->status = bad ? (int)JFA_ERR_BAD_OFFSETS : p.phase == 2 ? *(volatile const int*)p.prior_status : (int)JFA_OK;
   for (int c = tid; c <= ctas; c += kPlanThreads) w.pos[c] = paged_cut(p, t, ctas, c, cum, W, bad);
 }
 
@@ -107,6 +108,34 @@ __device__ __forceinline__ float cache_value(const void* codes, const uint8_t* s
   const float f = __uint_as_float((uint32_t)scales[row * (dim >> 5) + (c >> 5)] << 23);
   return e4m3_values(((const uint8_t*)codes)[row * dim + c]).x * f;
 }
+
+// The end of a whole row: normalised to its place, or, of a shared prefix, phase 1's in fp32 and
+// phase 2's joined with it.
+template <typename T>
+struct RowEnd {
+  float own, prior, lse;
+  __device__ __forceinline__ RowEnd(const Paged& p, int64_t row, float m, float l) {
+    if (p.phase == 2) {
+      const PagedJoin j = paged_join_prior(m, l, p.prior_lse[row]);
+      own = j.own;
+      prior = j.prior;
+      lse = j.lse;
+    } else {
+      own = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no key: 0; NaN stays NaN
+      prior = 0.f;
+      lse = l == 0.f ? -INFINITY : p.phase == 1 ? m + log2f(l) : (m + log2f(l)) * kLn2;
+    }
+  }
+  __device__ __forceinline__ void put(const Paged& p, int64_t at, float x) const {
+    x *= own;
+    if (p.phase == 1) p.prior_o[at] = x;
+    else ((T*)p.o)[at] = result<T>(p.phase == 2 ? fmaf(p.prior_o[at], prior, x) : x);
+  }
+  __device__ __forceinline__ void finish(const Paged& p, int64_t row) const {
+    if (p.phase == 1) p.prior_lse[row] = lse;
+    else p.lse[row] = lse;
+  }
+};
 
 template <typename T, int KIND>
 __global__ void __launch_bounds__(kSimtThreads)
@@ -139,22 +168,23 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
     }
     for (int i = tid + t.rows * ldq; i < kRows * ldq; i += kSimtThreads) Q[i] = 0.f;
     const int64_t limit = !row_ok ? 0 : p.causal ? g.seq.off + tok + 1 : g.seq.lk;  // keys the row sees
+    const int64_t from = p.window > 0 ? limit - p.window : 0;  // but for the sinks, none in front of this one
     float m = -INFINITY, l = 0.f, acc[16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) acc[c] = 0.f;
     for (int blk = g.blk0; blk < g.blk1; ++blk) {
-      const int k0 = blk * kKeys, nk = min(kKeys, g.seq.lk - k0);
+      const int k0 = g.span.block(blk) * kKeys, nk = min(kKeys, g.seq.lk - k0);
       __syncthreads();
       if (tid < kKeys) {
         int64_t row = -1;
-        if (tid < nk) {
+        if (tid < nk && paged_sees(p, g.span.low, k0 + tid)) {
           const int page = paged_page(p, g.b, k0 + tid, status);
           if (page >= 0) row = paged_row(p, page, head_k, k0 + tid);
         }
         row_of[tid] = row;
       }
       __syncthreads();
-      // slots behind the sequence's end are never read
+      // slots behind the sequence's end or in front of the window are never read
       for (int i = tid; i < kKeys * dq; i += kSimtThreads) {
         const int j = i / dq, c = i - j * dq;
         K[j * ldq + c] = row_of[j] >= 0 ? cache_value<KIND>(p.kc, p.ks, row_of[j], dq, c) : 0.f;
@@ -170,7 +200,8 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
         const int j = sub + 8 * i;
         float x = 0.f;
         for (int c = 0; c < dq; ++c) x = fmaf(Q[r * ldq + c], K[j * ldq + c], x);
-        s[i] = k0 + j < limit && j < nk ? x * p.scale * kLog2e : -INFINITY;
+        const int at = k0 + j;
+        s[i] = at < limit && j < nk && (at >= from || at < p.sinks) ? x * p.scale * kLog2e : -INFINITY;
         mt = fmaxf(mt, s[i]);
       }
       for (int o = 4; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
@@ -214,11 +245,11 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
       }
     } else if (row_ok) {
       const int64_t orow = (int64_t)(g.seq.q0 + tok) * p.heads_q + head;
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no key: 0; NaN stays NaN
+      RowEnd<T> end(p, orow, m, l);
 #pragma unroll
       for (int c = 0; c < 16; ++c)
-        if (sub + 8 * c < dv) ((T*)p.o)[orow * dv + sub + 8 * c] = result<T>(acc[c] * inv);
-      if (sub == 0) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (sub + 8 * c < dv) end.put(p, orow * dv + sub + 8 * c, acc[c]);
+      if (sub == 0) end.finish(p, orow);
     }
   }
 }
@@ -237,6 +268,7 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
     static_assert(JFA_OK < 1 && 1 < JFA_ERR_BAD_OFFSETS && JFA_ERR_BAD_OFFSETS < JFA_ERR_TIMEOUT, "ranks");
     int st = 0;
     for (int i = lane; i < w.ctas; i += 32) st = max(st, w.cta_status[i] == JFA_ERR_BAD_PAGES ? 1 : w.cta_status[i]);
+    if (p.phase == 2) st = max(st, *p.prior_status == JFA_ERR_BAD_PAGES ? 1 : *p.prior_status);
     st = __reduce_max_sync(0xffffffffu, st);
     if (lane == 0) w.hdr->status = st == 1 ? (int)JFA_ERR_BAD_PAGES : st;
   }
@@ -270,11 +302,11 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
         if (lane + 32 * k < p.dim_v) acc[k] = fmaf(w.part_o[pr * p.dim_v + lane + 32 * k], f, acc[k]);
     }
     const int64_t orow = (int64_t)(seq.q0 + tok) * p.heads_q + head;
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    RowEnd<T> end(p, orow, m, l);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (lane + 32 * k < p.dim_v) ((T*)p.o)[orow * p.dim_v + lane + 32 * k] = result<T>(acc[k] * inv);
-    if (lane == 0) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      if (lane + 32 * k < p.dim_v) end.put(p, orow * p.dim_v + lane + 32 * k, acc[k]);
+    if (lane == 0) end.finish(p, orow);
   }
 }
 
@@ -340,19 +372,23 @@ int paged_ctas(const Paged& p, int kernel) {
   return n < kMaxPagedCtas ? n : kMaxPagedCtas;
 }
 
+// What a request's plan takes: header, places, scan, statuses.
+static size_t plan_layout(int64_t batch, char* b, size_t off, PagedWs* w) {
+  w->hdr = (PagedHeader*)(b + off);
+  off += sizeof(PagedHeader);
+  w->pos = (PagedPos*)(b + off);
+  off = up256(off + sizeof(PagedPos) * (kMaxPagedCtas + 2));
+  w->cum = (int64_t*)(b + off);
+  off = up256(off + sizeof(int64_t) * (size_t)(batch + 1));
+  w->cta_status = (int*)(b + off);
+  return up256(off + sizeof(int) * kMaxPagedCtas);
+}
+
 // Large enough for every kernel that may serve the request.
 size_t paged_layout(const Paged& p, void* base, PagedWs* out) {
   char* b = (char*)base;
-  size_t off = 0;
   PagedWs w{};
-  w.hdr = (PagedHeader*)b;
-  off = 256;
-  w.pos = (PagedPos*)(b + off);
-  off = up256(off + sizeof(PagedPos) * (kMaxPagedCtas + 2));
-  w.cum = (int64_t*)(b + off);
-  off = up256(off + sizeof(int64_t) * (size_t)(p.batch + 1));
-  w.cta_status = (int*)(b + off);
-  off = up256(off + sizeof(int) * kMaxPagedCtas);
+  size_t off = plan_layout(p.batch, b, 0, &w);
   constexpr size_t rows = 2 * (kMaxPagedCtas * 16 > kMaxTcCtas * 256 ? kMaxPagedCtas * 16 : kMaxTcCtas * 256);
   w.part_ml = (float*)(b + off);
   off = up256(off + sizeof(float) * 2 * rows);
@@ -360,6 +396,18 @@ size_t paged_layout(const Paged& p, void* base, PagedWs* out) {
   off = up256(off + sizeof(float) * rows * (size_t)p.dim_v);
   if (out) *out = w;
   return off;
+}
+
+size_t shared_layout(const Paged& prefix, const Paged& own, void* base, PagedWs* first, PagedWs* second, float** prior_o,
+                     float** prior_lse) {
+  char* b = (char*)base;
+  size_t off = paged_layout(own, base, second);
+  *first = *second;
+  off = plan_layout(prefix.batch, b, off, first);
+  *prior_lse = (float*)(b + off);
+  off = up256(off + sizeof(float) * (size_t)own.total_q * own.heads_q);
+  *prior_o = (float*)(b + off);
+  return up256(off + sizeof(float) * (size_t)own.total_q * own.heads_q * own.dim_v);
 }
 
 cudaError_t launch_paged_plan(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s) {

@@ -16,9 +16,20 @@ struct PagedSeq {
   int q0, lq, lk, tiles;
   int64_t off;  // position of its first new token: lk - lq (negative: tokens before the cache)
 };
+// The new tokens [x, y) of sequence b; [-1, -1): its group is not one of the batch's.
+struct PagedBounds {
+  int64_t x, y;
+};
+__device__ __forceinline__ PagedBounds paged_bounds(const Paged& p, int64_t b) {
+  if (!p.groups) return PagedBounds{__ldg(p.offs + b), __ldg(p.offs + b + 1)};
+  const int64_t s = __ldg(p.groups + b), n = __ldg(p.groups + b + 1);
+  if (s < 0 || n < s || n > p.seqs || (b == 0 && s != 0) || (b == p.batch - 1 && n != p.seqs)) return PagedBounds{-1, -1};
+  return PagedBounds{__ldg(p.offs + s), __ldg(p.offs + n)};
+}
 __device__ __forceinline__ PagedSeq paged_seq(const Paged& p, const TileShape& t, int b) {
   PagedSeq s;
-  const int64_t a = __ldg(p.offs + b), e = __ldg(p.offs + b + 1), l = __ldg(p.lens + b);
+  const PagedBounds n = paged_bounds(p, b);
+  const int64_t a = n.x, e = n.y, l = __ldg(p.lens + b);
   // (what a plan was not made for and is no batch either has no tokens)
   const bool ok = a >= 0 && e >= a && e <= p.total_q && l >= 0 && l <= ((int64_t)p.width << p.page_shift);
   s.q0 = (int)a;
@@ -35,19 +46,48 @@ __device__ __forceinline__ int tile_keys(const Paged& p, const TileShape& t, con
   return last < 0 ? 0 : (int)last;
 }
 
+// The blocks of keys that a tile meets, by number: `nb` of them, the first `ns` from the cache's
+// start (they hold the sinks), the others from block `first` on.  Without a window ns = first = 0.
+struct PagedSpan {
+  int nb, ns, first;
+  int low;  // position of the first key of the window of the tile's first row
+  __device__ __forceinline__ int block(int i) const { return i < ns ? i : i - ns + first; }
+};
+// off: position of the sequence's first new token, end: keys that the tile's last row sees
+template <bool WIN = true>
+__device__ __forceinline__ PagedSpan paged_span(const Paged& p, const TileShape& t, int64_t off, int64_t end, int64_t tile) {
+  PagedSpan s;
+  s.nb = (int)((end + t.keys - 1) / t.keys);
+  s.ns = s.first = s.low = 0;
+  if (WIN && p.window > 0) {
+    const int64_t low = off + tile * t.tokens - p.window + 1;
+    s.low = (int)min(max((int64_t)0, low), end);
+    s.first = min(s.low / t.keys, max(s.nb - 1, 0));
+    s.ns = min((int)(((int64_t)p.sinks + t.keys - 1) / t.keys), s.first);
+    s.nb -= s.first - s.ns;
+  }
+  return s;
+}
+// Whether any row of the tile may see the key at position x (that its last row sees)
+__device__ __forceinline__ bool paged_sees(const Paged& p, int low, int x) { return x >= low || x < p.sinks; }
+
 // ------------------------------------------------------------------- cutting the work
 struct SeqCost {
   int64_t off, lk, tiles, s, over;
+  int64_t most;  // keys that a tile meets at most: a window's with its sinks, and part of a block
   int causal;
   // cost of the tiles in front of tile t, t <= tiles - 1
   __device__ int64_t before(int64_t t) const {
     if (!causal) return t * (over + lk);
-    // tile u sees max(0, off + (u + 1) s) keys
+    // tile u sees max(0, off + (u + 1) s) keys, and meets at most `most`
     int64_t u0 = off < 0 ? (-off) / s : 0;  // tiles that see nothing
     if (u0 > t) u0 = t;
-    return t * over + (t - u0) * off + s * ((t * (t + 1) - u0 * (u0 + 1)) / 2);
+    int64_t u1 = most > off ? (most - off) / s : 0;  // tiles that meet all that they see
+    if (u1 > t) u1 = t;
+    if (u1 < u0) u1 = u0;
+    return t * over + (u1 - u0) * off + s * ((u1 * (u1 + 1) - u0 * (u0 + 1)) / 2) + (t - u1) * (u1 < t ? most : 0);
   }
-  __device__ int64_t total() const { return tiles == 0 ? 0 : before(tiles - 1) + over + lk; }
+  __device__ int64_t total() const { return tiles == 0 ? 0 : before(tiles - 1) + over + min(lk, most); }
 };
 __device__ __forceinline__ SeqCost seq_cost(const Paged& p, const TileShape& t, int64_t lq, int64_t lk) {
   SeqCost c;
@@ -56,13 +96,16 @@ __device__ __forceinline__ SeqCost seq_cost(const Paged& p, const TileShape& t, 
   c.s = t.tokens;
   c.tiles = (lq + t.tokens - 1) / t.tokens;
   c.over = t.overhead;
+  c.most = (int64_t)1 << 40;
+  if (p.window > 0) c.most = (int64_t)p.window + t.tokens + t.keys + ((int64_t)p.sinks + t.keys - 1) / t.keys * t.keys;
   c.causal = p.causal;
   return c;
 }
 
 // Cost of sequence b in all its units, or -1: the arrays do not describe a batch.
 __device__ __forceinline__ int64_t checked_cost(const Paged& p, const TileShape& t, int64_t b) {
-  const int64_t a = __ldg(p.offs + b), e = __ldg(p.offs + b + 1), lk = __ldg(p.lens + b);
+  const PagedBounds n = paged_bounds(p, b);
+  const int64_t a = n.x, e = n.y, lk = __ldg(p.lens + b);
   if (a < 0 || e < a || e > p.total_q || lk < 0 || lk > ((int64_t)p.width << p.page_shift) || (b == 0 && a != 0) ||
       (b == p.batch - 1 && e != p.total_q))
     return -1;
@@ -83,7 +126,8 @@ __device__ __forceinline__ PagedPos paged_cut(const Paged& p, const TileShape& t
     if (cum[m + 1] > x) hi = m;
     else lo = m + 1;
   }
-  const SeqCost sc = seq_cost(p, t, __ldg(p.offs + lo + 1) - __ldg(p.offs + lo), __ldg(p.lens + lo));
+  const PagedBounds bounds = paged_bounds(p, lo);
+  const SeqCost sc = seq_cost(p, t, bounds.y - bounds.x, __ldg(p.lens + lo));
   const int64_t S = sc.total(), y = x - cum[lo];
   const int64_t unit = y / S, z = y - unit * S;
   int64_t tl = 0, th = sc.tiles - 1;
@@ -93,7 +137,7 @@ __device__ __forceinline__ PagedPos paged_cut(const Paged& p, const TileShape& t
     else th = m - 1;
   }
   const int64_t vis = tl == sc.tiles - 1 || !sc.causal ? sc.lk : max((int64_t)0, sc.off + (tl + 1) * sc.s);
-  const int64_t nb = (vis + t.keys - 1) / t.keys;
+  const int64_t nb = paged_span(p, t, sc.off, vis, tl).nb;
   const int64_t d = z - sc.before(tl) - sc.over;
   const int64_t blk = d <= 0 ? 0 : (d + t.keys / 2) / t.keys;
   r.b = (int)lo;
@@ -114,6 +158,11 @@ __device__ __forceinline__ PagedPos paged_pos(const Paged& p, const TileShape& t
   if ((x.b | x.unit | x.tile | x.blk) < 0 || x.b >= p.batch || x.unit >= p.heads_k * t.nsub)
     return PagedPos{(int)p.batch, 0, 0, 0};
   return x;
+}
+
+// Whether the first phase found the batch invalid: the second then computes nothing either.
+__device__ __forceinline__ bool prior_failed(const Paged& p) {
+  return *(const volatile int*)p.prior_status == (int)JFA_ERR_BAD_OFFSETS;
 }
 
 // A CTA's share, [pos[0], pos[1]), in shared memory.  With w.ctas > 0 there is no plan (a batch of
@@ -141,6 +190,7 @@ __device__ __forceinline__ int* paged_share(const Paged& p, const TileShape& t, 
     bad |= cost[i] < 0;
     x += cost[i];
   }
+  if (p.phase == 2 && tid == 0) bad |= prior_failed(p);
   bad = __syncthreads_or(bad) != 0;
   int64_t before = x;
   if (tid < kThreads) {
@@ -169,9 +219,10 @@ __device__ __forceinline__ int* paged_share(const Paged& p, const TileShape& t, 
   return w.cta_status + c;
 }
 
-// Walks the segments of a CTA's share: [blk0, blk1) of a tile's nb key blocks.
+// Walks the segments of a CTA's share: [blk0, blk1) of the nb key blocks that a tile meets.
 struct PagedSegment {
   int b, unit, tile, blk0, blk1, nb;
+  PagedSpan span;
   PagedSeq seq;
   int slot;  // partial slot (0 or 1) of the CTA, or -1: the tile is whole
 };
@@ -184,6 +235,8 @@ struct PagedWalk {
     end = share[1];
     fresh = true;
   }
+  // WIN false: of kernels that serve no window
+  template <bool WIN = true>
   __device__ __forceinline__ bool next(const Paged& p, const TileShape& t, PagedSegment& s) {
     const int units = p.heads_k * t.nsub;
     for (;;) {
@@ -210,7 +263,8 @@ struct PagedWalk {
       s.unit = at.unit;
       s.tile = at.tile;
       s.seq = seq;
-      s.nb = (tile_keys(p, t, seq, at.tile) + t.keys - 1) / t.keys;
+      s.span = paged_span<WIN>(p, t, seq.off, tile_keys(p, t, seq, at.tile), at.tile);
+      s.nb = s.span.nb;
       s.blk0 = min(at.blk, s.nb);
       s.blk1 = same ? min(end.blk, s.nb) : s.nb;
       s.slot = s.blk0 > 0 ? 0 : s.blk1 < s.nb ? 1 : -1;

@@ -1,0 +1,10 @@
+// Attention over a paged cache for many query rows, over a shared prefix: both phases (paged_tc.cuh).
+#include "paged_tc.cuh"
+
+namespace jfa {
+
+cudaError_t launch_paged_tc_shared(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s) {
+  return launch_tc<kShared>(p, t, ctas, w, s);
+}
+
+}  // namespace jfa

@@ -41,6 +41,10 @@ constexpr int kNormRopeParts = 1024;  // most partial sums a backward writes
 // ------------------------------------------------------------- paged cache and attention
 enum : int { kCacheF32 = 0, kCacheBf16 = 1, kCacheMx = 2 };
 
+// What a kernel over a paged cache is compiled for: attention of all keys, of a window with sinks, or
+// one of the two phases of a shared prefix.
+enum : int { kAll = 0, kWindow = 1, kShared = 2 };
+
 // One request on a paged cache.
 struct Paged {
   const int64_t* offs;   // [B+1] new tokens
@@ -58,6 +62,17 @@ struct Paged {
   int64_t sq, sk, sv;  // elements between tokens
   void* o;             // [T, heads_q, dim_v]
   float* lse;          // [T, heads_q]
+  // Window: a query at position x sees the keys y <= x with x - y < window, and the first `sinks`.
+  // window = 0: all up to x.
+  int window, sinks;
+  // Shared prefix.  Phase 1: the "sequences" of the request are groups, sequence b the tokens of the
+  // sequences groups[b] .. groups[b + 1] - 1 of `seqs`, and its results are left in prior_o and
+  // prior_lse (log2 units) in fp32.  Phase 2 adds them to its own.
+  int phase;
+  const int64_t* groups;
+  int64_t seqs;
+  float *prior_o, *prior_lse;  // [T, heads_q, dim_v], [T, heads_q]
+  const int* prior_status;     // phase 2: how phase 1 ended
 };
 
 // Where a CTA's share of the attention begins: block `blk` of keys of tile `tile` of unit
@@ -110,6 +125,10 @@ int paged_kernel(const Paged& p, int dtype);
 TileShape paged_shape(const Paged& p, int kernel);
 int paged_ctas(const Paged& p, int kernel);
 size_t paged_layout(const Paged& p, void* base, PagedWs* out);
+// The workspace of attention over a shared prefix: phase 2's, then phase 1's header and plan (its
+// parts lie in phase 2's place, which begins behind it) and its results.
+size_t shared_layout(const Paged& prefix, const Paged& own, void* base, PagedWs* first, PagedWs* second, float** prior_o,
+                     float** prior_lse);
 
 // Whether later attention launches are held (jfa_test_hold).
 void paged_set_test_hold(int on);
@@ -120,8 +139,13 @@ cudaError_t launch_cache_read(const Paged& p, int dtype, void* k, void* v, Paged
 cudaError_t launch_paged_plan(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
 cudaError_t launch_paged_simt(const Paged& p, const TileShape& t, int ctas, int dtype, const PagedWs& w,
                               cudaStream_t s);
+// One translation unit for each of kAll, kWindow, kShared.
 cudaError_t launch_paged_rows16(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
+cudaError_t launch_paged_rows16_window(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
+cudaError_t launch_paged_rows16_shared(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
 cudaError_t launch_paged_tc(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
+cudaError_t launch_paged_tc_window(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
+cudaError_t launch_paged_tc_shared(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
 cudaError_t launch_paged_combine(const Paged& p, const TileShape& t, int ctas, int dtype, const PagedWs& w,
                                  cudaStream_t s);
 

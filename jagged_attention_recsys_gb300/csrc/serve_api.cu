@@ -202,6 +202,76 @@ jfa_status plan_paged(const Paged& r, int kernel, const PagedWs& w, cudaStream_t
   return cu(launch_paged_plan(r, paged_shape(r, kernel), paged_ctas(r, kernel), w, s));
 }
 
+// One pass of the attention over its plan, or the cuts that its CTAs make.
+jfa_status run_paged(const Paged& r, int dtype, int mode, bool planned, PagedWs w, cudaStream_t s) {
+  const int kernel = paged_kernel(r, dtype);
+  const int ctas = paged_ctas(r, kernel);
+  jfa_status st;
+  if (!planned) {
+    if (r.total_q > 0 && r.batch <= kPlanInCta) w.ctas = ctas;
+    else if ((st = plan_paged(r, kernel, w, s)) != JFA_OK) return st;
+  }
+  if (r.total_q == 0) return JFA_OK;
+  const TileShape shape = paged_shape(r, kernel);
+  constexpr decltype(&launch_paged_tc) tc[] = {launch_paged_tc, launch_paged_tc_window, launch_paged_tc_shared};
+  constexpr decltype(&launch_paged_rows16) few[] = {launch_paged_rows16, launch_paged_rows16_window,
+                                                    launch_paged_rows16_shared};
+  Timed t(JFA_KERNEL_PAGED, s);
+  st = cu(kernel == kPagedTc       ? tc[mode](r, shape, ctas, w, s)
+          : kernel == kPagedRows16 ? few[mode](r, shape, ctas, w, s)
+                                   : launch_paged_simt(r, shape, ctas, dtype, w, s));
+  if (st != JFA_OK) return st;
+  return cu(launch_paged_combine(r, shape, ctas, dtype, w, s));
+}
+
+jfa_status check_window(const jfa_paged_params* p, int32_t window, int32_t sinks) {
+  jfa_status st = check_paged_attention(p);
+  if (st != JFA_OK) return st;
+  if (window < 1 || sinks < 0) return JFA_ERR_INVALID_ARG;
+  return p->causal ? JFA_OK : JFA_ERR_UNSUPPORTED;
+}
+// All positions there are need no more than that.
+void set_window(const jfa_paged_params* p, int32_t window, int32_t sinks, Paged* r) {
+  const int most = p->max_pages > 0 ? p->max_pages * p->page_size : 1;
+  r->window = window < most ? window : most;
+  r->sinks = sinks < most ? sinks : most;
+}
+
+// What the calls over a paged cache check of their arguments, and the request they make of them.
+jfa_status paged_request(const jfa_paged_params* p, const void* q, const void* k_cache, const void* v_cache,
+                         const uint8_t* k_scale, const uint8_t* v_scale, const int64_t* offs, const int64_t* lens,
+                         const int32_t* table, void* o, float* lse, Paged* r) {
+  jfa_status st;
+  if ((st = check_index(p, offs, lens, table)) != JFA_OK ||
+      (st = check_cache(p, k_cache, v_cache, k_scale, v_scale)) != JFA_OK ||
+      (st = check_rows(p, q, p->stride_q, (int64_t)p->heads_q * p->dim_qk)) != JFA_OK)
+    return st;
+  if (p->total_q > 0 && (!aligned(o, 16) || !aligned(lse, 16))) return JFA_ERR_INVALID_ARG;
+  *r = make_paged(p, offs, lens, table, k_cache, v_cache, k_scale, v_scale);
+  r->q = q;
+  r->o = o;
+  r->lse = lse;
+  return JFA_OK;
+}
+
+// The prefixes' side of a call: groups in the place of sequences, and no mask.
+jfa_status check_shared(const jfa_paged_params* p, int64_t groups, int32_t prefix_pages) {
+  jfa_status st = check_paged_attention(p);
+  if (st != JFA_OK) return st;
+  if (groups < 0 || prefix_pages < 0 || (groups == 0 && p->batch > 0)) return JFA_ERR_INVALID_ARG;
+  jfa_paged_params g = *p;
+  g.batch = groups;
+  g.max_pages = prefix_pages;
+  if (groups == 0) g.total_q = 0;
+  return check_paged_attention(&g);
+}
+void prefix_request(int64_t groups, int32_t prefix_pages, Paged* r) {
+  r->seqs = r->batch;
+  r->batch = groups;
+  r->width = prefix_pages;
+  r->causal = 0;
+}
+
 }  // namespace
 
 void paged_set_test_hold(int on) { g_paged_hold.store(on != 0, std::memory_order_relaxed); }
@@ -316,32 +386,82 @@ jfa_status jfa_paged_fwd(const jfa_paged_params* p, const void* q, const void* k
                          const int32_t* table, void* o, float* lse, void* ws, size_t ws_bytes, jfa_stream_t stream) {
   jfa_status st = check_paged_attention(p);
   if (st != JFA_OK) return st;
-  if ((st = check_index(p, offs, lens, table)) != JFA_OK ||
-      (st = check_cache(p, k_cache, v_cache, k_scale, v_scale)) != JFA_OK ||
-      (st = check_rows(p, q, p->stride_q, (int64_t)p->heads_q * p->dim_qk)) != JFA_OK)
-    return st;
-  if (p->total_q > 0 && (!aligned(o, 16) || !aligned(lse, 16))) return JFA_ERR_INVALID_ARG;
-  Paged r = make_paged(p, offs, lens, table, k_cache, v_cache, k_scale, v_scale);
+  Paged r;
+  if ((st = paged_request(p, q, k_cache, v_cache, k_scale, v_scale, offs, lens, table, o, lse, &r)) != JFA_OK) return st;
   PagedWs w;
   if ((st = check_ws(r, ws, ws_bytes, &w)) != JFA_OK) return st;
-  r.q = q;
-  r.o = o;
-  r.lse = lse;
-  cudaStream_t s = (cudaStream_t)stream;
-  const int kernel = paged_kernel(r, p->dtype);
-  const int ctas = paged_ctas(r, kernel);
-  if (!(p->flags & JFA_PLANNED)) {
-    if (p->total_q > 0 && p->batch <= kPlanInCta) w.ctas = ctas;
-    else if ((st = plan_paged(r, kernel, w, s)) != JFA_OK) return st;
-  }
-  if (p->total_q == 0) return JFA_OK;
-  const TileShape shape = paged_shape(r, kernel);
-  Timed t(JFA_KERNEL_PAGED, s);
-  st = cu(kernel == kPagedTc       ? launch_paged_tc(r, shape, ctas, w, s)
-          : kernel == kPagedRows16 ? launch_paged_rows16(r, shape, ctas, w, s)
-                                   : launch_paged_simt(r, shape, ctas, p->dtype, w, s));
+  return run_paged(r, p->dtype, kAll, (p->flags & JFA_PLANNED) != 0, w, (cudaStream_t)stream);
+}
+
+jfa_status jfa_paged_window_plan(const jfa_paged_params* p, int32_t window, int32_t sinks, const int64_t* offs,
+                                 const int64_t* lens, void* ws, size_t ws_bytes, jfa_stream_t stream) {
+  jfa_status st = check_window(p, window, sinks);
   if (st != JFA_OK) return st;
-  return cu(launch_paged_combine(r, shape, ctas, p->dtype, w, s));
+  if (!aligned(offs, 8) || (p->batch > 0 && !aligned(lens, 8))) return JFA_ERR_INVALID_ARG;
+  Paged r = make_paged(p, offs, lens, nullptr, nullptr, nullptr, nullptr, nullptr);
+  set_window(p, window, sinks, &r);
+  PagedWs w;
+  if ((st = check_ws(r, ws, ws_bytes, &w)) != JFA_OK) return st;
+  return plan_paged(r, paged_kernel(r, p->dtype), w, (cudaStream_t)stream);
+}
+
+jfa_status jfa_paged_window_fwd(const jfa_paged_params* p, int32_t window, int32_t sinks, const void* q,
+                                const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                                const uint8_t* v_scale, const int64_t* offs, const int64_t* lens, const int32_t* table,
+                                void* o, float* lse, void* ws, size_t ws_bytes, jfa_stream_t stream) {
+  jfa_status st = check_window(p, window, sinks);
+  if (st != JFA_OK) return st;
+  Paged r;
+  if ((st = paged_request(p, q, k_cache, v_cache, k_scale, v_scale, offs, lens, table, o, lse, &r)) != JFA_OK) return st;
+  set_window(p, window, sinks, &r);
+  PagedWs w;
+  if ((st = check_ws(r, ws, ws_bytes, &w)) != JFA_OK) return st;
+  return run_paged(r, p->dtype, kWindow, (p->flags & JFA_PLANNED) != 0, w, (cudaStream_t)stream);
+}
+
+size_t jfa_shared_workspace_size(const jfa_paged_params* p, int64_t groups, int32_t prefix_pages) {
+  if (check_shared(p, groups, prefix_pages) != JFA_OK) return 0;
+  const Paged own = make_paged(p, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+  Paged prefix = own;
+  prefix_request(groups, prefix_pages, &prefix);
+  PagedWs a, b;
+  float *o, *l;
+  return shared_layout(prefix, own, nullptr, &a, &b, &o, &l);
+}
+
+jfa_status jfa_shared_fwd(const jfa_paged_params* p, int64_t groups, int32_t prefix_pages, const void* q,
+                          const void* k_cache, const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                          const int64_t* offs, const int64_t* lens, const int32_t* table, const int64_t* group_offs,
+                          const int64_t* prefix_lens, const int32_t* prefix_table, void* o, float* lse, void* ws,
+                          size_t ws_bytes, jfa_stream_t stream) {
+  jfa_status st = check_shared(p, groups, prefix_pages);
+  if (st != JFA_OK) return st;
+  if (p->flags & JFA_PLANNED) return JFA_ERR_UNSUPPORTED;
+  Paged own;
+  if ((st = paged_request(p, q, k_cache, v_cache, k_scale, v_scale, offs, lens, table, o, lse, &own)) != JFA_OK) return st;
+  if (groups > 0 && (!aligned(group_offs, 8) || !aligned(prefix_lens, 8) || (prefix_pages > 0 && !aligned(prefix_table, 4))))
+    return JFA_ERR_INVALID_ARG;
+  Paged prefix = own;
+  prefix_request(groups, prefix_pages, &prefix);
+  prefix.groups = group_offs;
+  prefix.lens = prefix_lens;
+  prefix.table = prefix_table;
+  if (!ws || ((uintptr_t)ws & 255u) != 0) return JFA_ERR_WORKSPACE;
+  PagedWs first, second;
+  float *prior_o, *prior_lse;
+  if (ws_bytes < shared_layout(prefix, own, ws, &first, &second, &prior_o, &prior_lse)) return JFA_ERR_WORKSPACE;
+  first.hold = second.hold = g_paged_hold.load(std::memory_order_relaxed);
+  prefix.phase = 1;
+  own.phase = 2;
+  prefix.prior_o = own.prior_o = prior_o;
+  prefix.prior_lse = own.prior_lse = prior_lse;
+  own.prior_status = &first.hdr->status;
+  cudaStream_t s = (cudaStream_t)stream;
+  // (no group, no sequence: nothing to find wrong in the prefixes)
+  if ((st = groups > 0 ? run_paged(prefix, p->dtype, kShared, false, first, s)
+                       : cu(cudaMemsetAsync(first.hdr, 0, sizeof(PagedHeader), s))) != JFA_OK)
+    return st;
+  return run_paged(own, p->dtype, kShared, false, second, s);
 }
 
 }  // extern "C"
