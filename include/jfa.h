@@ -162,6 +162,26 @@ jfa_status jfa_bwd(const jfa_params* p, const void* q, const void* k, const void
                    jfa_stream_t stream);
 
 /*
+ * Causal softmax self-attention over a sliding window with sinks: of the keys j <= i, row i sees
+ * those with i - j < window and those with j < sinks (the sequence's first, which stay visible).
+ * window >= 1, sinks >= 0; p->causal = 1 (0: JFA_ERR_UNSUPPORTED).  Arguments, outputs, workspace
+ * and errors are otherwise those of jfa_fwd and jfa_bwd; the work of a row ends with its window, so
+ * that a sequence's grows with its length and not with its square.  Every row sees its own key.
+ * jfa_window_plan builds the lists of both calls for one window and its sinks (JFA_PLANNED, as by
+ * jfa_plan; a plan of another window or of jfa_plan gives wrong results, within the buffers' bounds).
+ * Values of keys that a row's window hides have to be finite and at most 2^120 in size.
+ */
+jfa_status jfa_window_plan(const jfa_params* p, int32_t window, int32_t sinks, const int64_t* offs,
+                           void* ws, size_t ws_bytes, jfa_stream_t stream);
+jfa_status jfa_window_fwd(const jfa_params* p, int32_t window, int32_t sinks, const void* q,
+                          const void* k, const void* v, const int64_t* offs, void* o, float* lse,
+                          void* ws, size_t ws_bytes, jfa_stream_t stream);
+jfa_status jfa_window_bwd(const jfa_params* p, int32_t window, int32_t sinks, const void* q,
+                          const void* k, const void* v, const void* o, const float* lse,
+                          const void* dout, const int64_t* offs, void* dq, void* dk, void* dv,
+                          void* ws, size_t ws_bytes, jfa_stream_t stream);
+
+/*
  * Softmax cross-attention forward with independent query and key offsets and
  * possibly Dv != Dqk (jagged-input bullet: cross and asymmetric-QKV patterns).
  * Causal must be 0.  A sequence with Lk_b == 0 yields o = 0 and lse = -inf.
@@ -468,6 +488,27 @@ jfa_status jfa_paged_fwd(const jfa_paged_params* p, const void* q, const void* k
                          const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
                          const int64_t* offs, const int64_t* lens, const int32_t* table, void* o,
                          float* lse, void* ws, size_t ws_bytes, jfa_stream_t stream);
+
+/*
+ * New tokens appended to a paged cache in one pass: what jfa_norm_rope_fwd makes of the queries q and
+ * the keys k, the queries written to yq, the keys and the values v to their pages as jfa_cache_write
+ * does (that call's arguments, limits, errors, plans and workspace).  norm, eps, wq, wk and rope are
+ * those of jfa_norm_rope_params (rope NULL: no rotation; norm = 0: no weights).  pos (int64 [T]) are
+ * the positions of the rotation; NULL: those in the cache, lens[b] - L_b + i.  q [T, Hq, Dqk] (stride
+ * p->stride_q) may be NULL, and yq then is: only keys and values are appended.  yq may be q with the
+ * same stride.  Keys go to an MXFP8 cache from their fp32 values, without a rounding to `dtype` in
+ * between; in the values' own type they are rounded once, as by the two calls.  yq is written for every
+ * token, those before the cache's start too.  On an invalid batch (JFA_ERR_BAD_OFFSETS) yq and the rows
+ * written are undefined; a planned call on one computes nothing.
+ * q, k, v and yq are 16-byte aligned, with strides of whole 16 bytes; pointers and strides of whole 32
+ * bytes in fp32, with dim_qk and rope.dim multiples of 16 and dim_v of 8, take the fast kernel.
+ */
+jfa_status jfa_rope_append(const jfa_paged_params* p, const jfa_rope* rope, int32_t norm, float eps,
+                           const void* q, const void* k, const void* v, const int64_t* pos,
+                           const float* wq, const float* wk, const int64_t* offs, const int64_t* lens,
+                           const int32_t* table, void* yq, int64_t stride_yq, void* k_cache,
+                           void* v_cache, uint8_t* k_scale, uint8_t* v_scale, void* ws, size_t ws_bytes,
+                           jfa_stream_t stream);
 
 /*
  * Attention over a sliding window of a paged cache, with sinks: jfa_paged_fwd in which a query at

@@ -52,7 +52,8 @@ EXPORTS = ("jfa_workspace_size", "jfa_fwd", "jfa_bwd", "jfa_cross_fwd", "jfa_cro
            "jfa_block_plan", "jfa_norm_rope_workspace_size", "jfa_norm_rope_fwd",
            "jfa_norm_rope_bwd", "jfa_paged_workspace_size", "jfa_cache_write", "jfa_cache_read",
            "jfa_paged_plan", "jfa_paged_fwd", "jfa_paged_window_plan", "jfa_paged_window_fwd",
-           "jfa_shared_workspace_size", "jfa_shared_fwd")
+           "jfa_shared_workspace_size", "jfa_shared_fwd", "jfa_rope_append",
+           "jfa_window_plan", "jfa_window_fwd", "jfa_window_bwd")
 
 
 class JfaError(RuntimeError):
@@ -172,6 +173,11 @@ def lib():
         L.jfa_cache_read.argtypes = [G] + [vp] * 10 + [sz, vp]
         L.jfa_paged_plan.argtypes = [G, vp, vp, vp, sz, vp]
         L.jfa_paged_fwd.argtypes = [G] + [vp] * 11 + [sz, vp]
+        L.jfa_window_plan.argtypes = [P, i32, i32, i64p, vp, sz, vp]
+        L.jfa_window_fwd.argtypes = [P, i32, i32, vp, vp, vp, i64p, vp, fp, vp, sz, vp]
+        L.jfa_window_bwd.argtypes = [P, i32, i32, vp, vp, vp, vp, fp, vp, i64p, vp, vp, vp, vp, sz, vp]
+        L.jfa_rope_append.argtypes = ([G, ctypes.POINTER(_rope), i32, ctypes.c_float] + [vp] * 10 + [ctypes.c_int64]
+                                      + [vp] * 5 + [sz, vp])
         L.jfa_paged_window_plan.argtypes = [G, i32, i32, vp, vp, vp, sz, vp]
         L.jfa_paged_window_fwd.argtypes = [G, i32, i32] + [vp] * 11 + [sz, vp]
         L.jfa_shared_workspace_size.argtypes = [G, ctypes.c_int64, i32]
@@ -179,7 +185,7 @@ def lib():
         L.jfa_shared_fwd.argtypes = [G, ctypes.c_int64, i32] + [vp] * 14 + [sz, vp]
         for f in ("jfa_norm_rope_fwd", "jfa_norm_rope_bwd", "jfa_cache_write", "jfa_cache_read",
                   "jfa_paged_plan", "jfa_paged_fwd", "jfa_paged_window_plan", "jfa_paged_window_fwd",
-                  "jfa_shared_fwd"):
+                  "jfa_shared_fwd", "jfa_rope_append", "jfa_window_plan", "jfa_window_fwd", "jfa_window_bwd"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -809,6 +815,39 @@ def jfa_paged_fwd(q, cache, table, offs, lens, *, scale=None, causal=True, o=Non
     return o, lse
 
 
+@_in_stream
+def jfa_rope_append(q, k, v, cache, table, offs, lens, wq=None, wk=None, *, rope=None, eps=1e-6, norm=True, pos=None,
+                    yq=None, ws=None, stream=None, planned=False):
+    """jfa_norm_rope_fwd of the new tokens' q [T, Hq, Dqk] and k [T, Hk, Dqk] and jfa_cache_write of those keys
+    and v [T, Hk, Dv] in one pass, at positions ``pos`` [T] (None: theirs in the cache); q may be None.
+    Returns (yq, ws)."""
+    dev, dtype = cache.device, k.dtype
+    if not norm and (wq is not None or wk is not None):
+        raise ValueError("norm=False takes no weights")
+    stride_k = _rows("k", k, dtype, dev, cache.heads, cache.dim_qk)
+    T, D = k.shape[0], cache.dim_qk
+    stride_v = _rows("v", v, dtype, dev, cache.heads, cache.dim_v, T)
+    hq = stride_q = stride_yq = None
+    if q is not None:
+        stride_q, hq = _rows("q", q, dtype, dev, None, D, T), q.shape[1]
+        yq, stride_yq = _out("yq", yq, q)
+    elif yq is not None:
+        raise ValueError("yq without q")
+    if pos is not None:
+        _plain("pos", pos, torch.int64, (T,), dev)
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            _plain(name, w, torch.float32, (D,), dev)
+    p, ws = _paged_prep(cache, table, offs, lens, T, dtype, hq, None, True, ws, planned)
+    p.stride_q, p.stride_k, p.stride_v = stride_q or 0, stride_k, stride_v
+    _check(lib().jfa_rope_append(ctypes.byref(p), None if rope is None else ctypes.byref(rope), 1 if norm else 0, eps,
+                                 _addr(q), _addr(k), _addr(v), _addr(pos), _addr(wq), _addr(wk), _addr(offs), _addr(lens),
+                                 _addr(table), _addr(yq), stride_yq or 0, _addr(cache.k), _addr(cache.v),
+                                 _addr(cache.k_scale), _addr(cache.v_scale), _addr(ws), ws.numel(), _on(dev)),
+           "jfa_rope_append")
+    return yq, ws
+
+
 # ----------------------------------------------------------------------------- windows, shared prefixes
 def _int32(name, x, least):
     """A window or a number of sinks; what passes 32 bits is as good as the largest."""
@@ -816,6 +855,69 @@ def _int32(name, x, least):
     if x < least:
         raise ValueError("%s must be at least %d, got %d" % (name, least, x))
     return min(x, 2 ** 31 - 1)
+
+
+def _window_prep(q, k, v, offs, window, sinks, ws, scale, planned):
+    window, sinks = _int32("window", window, 1), _int32("sinks", sinks, 0)
+    if q.dim() != 3 or k.shape != q.shape or v.dim() != 3 or v.shape[:2] != q.shape[:2]:
+        raise ValueError("q, k and v must be [T, H, dim], q and k of one shape")
+    if not (q.dtype == k.dtype == v.dtype) or not (q.device == k.device == v.device == offs.device):
+        raise ValueError("q, k and v must be of one type, on the device of offs")
+    _plain("offs", offs, torch.int64, (offs.numel(),), q.device)
+    p, ws = _prep(q, k, v, offs, None, ws, scale, True, planned)
+    if ws.device != q.device or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous uint8 tensor on %s" % q.device)
+    return p, ws, window, sinks
+
+
+@_in_stream
+def jfa_window_plan(q, k, v, offs, window, *, sinks=0, scale=None, ws=None, stream=None):
+    """The work lists of jfa_window_fwd and jfa_window_bwd on these inputs' shapes and offsets with this
+    window and these sinks, built into ``ws`` (allocated if None); returns ``ws``."""
+    p, ws, window, sinks = _window_prep(q, k, v, offs, window, sinks, ws, scale, False)
+    _check(lib().jfa_window_plan(ctypes.byref(p), window, sinks, _addr(offs), _addr(ws), ws.numel(), _on(q.device)),
+           "jfa_window_plan")
+    return ws
+
+
+@_in_stream
+def jfa_window_fwd(q, k, v, offs, window, *, sinks=0, scale=None, o=None, lse=None, ws=None, stream=None,
+                   planned=False):
+    """Causal softmax self-attention in which row i sees the last ``window`` keys up to its own and the first
+    ``sinks`` of its sequence; returns (o, lse)."""
+    p, ws, window, sinks = _window_prep(q, k, v, offs, window, sinks, ws, scale, planned)
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _plain("o", o, q.dtype, v.shape, q.device)
+    if lse is None:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    else:
+        _plain("lse", lse, torch.float32, q.shape[:2], q.device)
+    _check(lib().jfa_window_fwd(ctypes.byref(p), window, sinks, _addr(q), _addr(k), _addr(v), _addr(offs), _addr(o),
+                                _addr(lse), _addr(ws), ws.numel(), _on(q.device)), "jfa_window_fwd")
+    return o, lse
+
+
+@_in_stream
+def jfa_window_bwd(q, k, v, o, lse, dout, offs, window, *, sinks=0, scale=None, dq=None, dk=None, dv=None, ws=None,
+                   stream=None, planned=False):
+    """Backward of jfa_window_fwd; returns (dq, dk, dv)."""
+    p, ws, window, sinks = _window_prep(q, k, v, offs, window, sinks, ws, scale, planned)
+    _plain("o", o, q.dtype, v.shape, q.device)
+    _plain("lse", lse, torch.float32, q.shape[:2], q.device)
+    _plain("dout", dout, q.dtype, v.shape, q.device)
+    made = []
+    for name, g, x in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if g is None:
+            g = torch.empty_like(x)
+        else:
+            _plain(name, g, q.dtype, x.shape, q.device)
+        made.append(g)
+    _check(lib().jfa_window_bwd(ctypes.byref(p), window, sinks, _addr(q), _addr(k), _addr(v), _addr(o), _addr(lse),
+                                _addr(dout), _addr(offs), _addr(made[0]), _addr(made[1]), _addr(made[2]), _addr(ws),
+                                ws.numel(), _on(q.device)), "jfa_window_bwd")
+    return tuple(made)
 
 
 @_in_stream

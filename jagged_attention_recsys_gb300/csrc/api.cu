@@ -212,6 +212,11 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 enum class Kind { Self, Cross, Gdpa };
 
+// A sliding window with sinks; 0: none.
+struct Window {
+  int window = 0, sinks = 0;
+};
+
 jfa_status check_params(const jfa_params* p, Kind kind) {
   if (!p) return JFA_ERR_INVALID_ARG;
   if (p->batch < 0 || p->total_q < 0 || p->total_k < 0 || p->heads < 1) return JFA_ERR_INVALID_ARG;
@@ -261,6 +266,8 @@ Problem make_problem(const jfa_params* p, const int64_t* oq, const int64_t* ok, 
   r.rope = nullptr;
   r.rope_npos = 0;
   r.block_mask = 0;
+  r.window = 0;
+  r.sinks = 0;
   r.dq_f32 = nullptr;
   return r;
 }
@@ -273,7 +280,7 @@ jfa_status empty_call(const Workspace& w, cudaStream_t s) {
 jfa_status run_fwd(const jfa_params* p, Kind kind, int act, const void* q, const void* k,
                    const void* v, const int64_t* oq, const int64_t* ok, void* o, float* lse,
                    void* ws, size_t ws_bytes, cudaStream_t s, const float2* rope = nullptr,
-                   int rope_npos = 0, int block_mask = 0) {
+                   int rope_npos = 0, int block_mask = 0, Window win = Window{}) {
   jfa_status st = check_params(p, kind);
   if (st != JFA_OK) return st;
   if ((st = check_ptrs({oq, ok})) != JFA_OK) return st;
@@ -289,6 +296,8 @@ jfa_status run_fwd(const jfa_params* p, Kind kind, int act, const void* q, const
   pr.rope = rope;
   pr.rope_npos = rope_npos;
   pr.block_mask = block_mask;
+  pr.window = win.window;
+  pr.sinks = win.sinks;
   const int path = jfa_path_for(p);
   if (!(p->flags & JFA_PLANNED)) {
     SchedConfig sc = path == 1 ? tc_fwd_sched(pr) : kSimtSched;
@@ -298,6 +307,7 @@ jfa_status run_fwd(const jfa_params* p, Kind kind, int act, const void* q, const
     Timed t(JFA_KERNEL_SCHEDULE, s);
     if ((st = cu(launch_schedule(pr, w, sc, s))) != JFA_OK) return st;
   }
+  if (p->total_q == 0 && p->total_k == 0) return JFA_OK;  // sequences without rows: their offsets are checked
   Timed t(JFA_KERNEL_FWD, s);
   if (path == 1) return cu(launch_tc_fwd(pr, q, k, v, o, lse, w, s));
   return cu(launch_simt_fwd(pr, p->dtype, q, k, v, o, lse, w, s));
@@ -307,7 +317,7 @@ jfa_status run_bwd(const jfa_params* p, Kind kind, int act, const void* q, const
                    const void* v, const void* o, const float* lse, const void* dout,
                    const int64_t* oq, const int64_t* ok, void* dq, void* dk, void* dv, void* ws,
                    size_t ws_bytes, cudaStream_t s, const float2* rope = nullptr,
-                   int rope_npos = 0, int block_mask = 0, float* dq_f32 = nullptr) {
+                   int rope_npos = 0, int block_mask = 0, float* dq_f32 = nullptr, Window win = Window{}) {
   jfa_status st = check_params(p, kind);
   if (st != JFA_OK) return st;
   if ((st = check_ptrs({oq, ok})) != JFA_OK) return st;
@@ -323,13 +333,16 @@ jfa_status run_bwd(const jfa_params* p, Kind kind, int act, const void* q, const
   pr.rope = rope;
   pr.rope_npos = rope_npos;
   pr.block_mask = block_mask;
+  pr.window = win.window;
+  pr.sinks = win.sinks;
   pr.dq_f32 = jfa_path_for(p) == 1 ? dq_f32 : nullptr;
   const int path = jfa_path_for(p);
   const bool planned = (p->flags & JFA_PLANNED) != 0;
   // The row terms (softmax only) depend on o, dout and lse alone: they run on a side
   // stream while the scheduler builds the lists, and the caller's stream waits for
   // them before the dK/dV pass.  A planned call builds no lists and runs them in line.
-  SideStream* sd = act == kActSoftmax && !planned ? side_stream() : nullptr;
+  const bool rows = p->total_q > 0 || p->total_k > 0;
+  SideStream* sd = act == kActSoftmax && !planned && rows ? side_stream() : nullptr;
   if (sd && (cudaEventRecord(sd->fork, s) != cudaSuccess ||
              cudaStreamWaitEvent(sd->s, sd->fork, 0) != cudaSuccess))
     return JFA_ERR_CUDA;
@@ -341,6 +354,7 @@ jfa_status run_bwd(const jfa_params* p, Kind kind, int act, const void* q, const
     Timed t(JFA_KERNEL_SCHEDULE, s);
     if ((st = cu(launch_schedule(pr, w, sc, s))) != JFA_OK) return st;
   }
+  if (!rows) return JFA_OK;
   if (act == kActSoftmax) {
     cudaStream_t rs = sd ? sd->s : s;
     {
@@ -370,12 +384,14 @@ jfa_status run_bwd(const jfa_params* p, Kind kind, int act, const void* q, const
 // is the forward's (same tiles and steps on each path), so one build serves the three
 // passes.  self_attention: Lq_b must equal Lk_b.
 jfa_status run_plan(const jfa_params* p, const int64_t* oq, const int64_t* ok, bool self_attention,
-                    void* ws, size_t ws_bytes, cudaStream_t s) {
+                    void* ws, size_t ws_bytes, cudaStream_t s, Window win = Window{}) {
   Workspace w;
   jfa_status st = prepare(p, ws, ws_bytes, &w);
   if (st != JFA_OK) return st;
   if (p->batch == 0) return empty_call(w, s);
   Problem pr = make_problem(p, oq, ok, kActSoftmax);
+  pr.window = win.window;
+  pr.sinks = win.sinks;
   const int path = jfa_path_for(p);
   SchedConfig sc = path == 1 ? tc_bwd_sched(pr) : kSimtSched;
   if (path == 1) {
@@ -387,6 +403,18 @@ jfa_status run_plan(const jfa_params* p, const int64_t* oq, const int64_t* ok, b
   sc.self_attention = self_attention || p->causal;
   Timed t(JFA_KERNEL_SCHEDULE, s);
   return cu(launch_schedule(pr, w, sc, s));
+}
+
+// A window's calls: causal self-attention.  No row needs more than all keys.
+jfa_status check_window(const jfa_params* p, int32_t window, int32_t sinks, Window* w) {
+  jfa_status st = check_params(p, Kind::Self);
+  if (st != JFA_OK) return st;
+  if (window < 1 || sinks < 0) return JFA_ERR_INVALID_ARG;
+  if (!p->causal) return JFA_ERR_UNSUPPORTED;
+  const int most = p->total_q > 1 ? (int)p->total_q : 1;
+  w->window = window < most ? window : most;
+  w->sinks = sinks < most ? sinks : most;
+  return JFA_OK;
 }
 
 // Pooled multi-head attention: the cross-attention workspace, then the query-row offsets
@@ -586,6 +614,35 @@ jfa_status jfa_bwd(const jfa_params* p, const void* q, const void* k, const void
                    jfa_stream_t stream) {
   return run_bwd(p, Kind::Self, kActSoftmax, q, k, v, o, lse, dout, offs, offs, dq, dk, dv, ws,
                  ws_bytes, (cudaStream_t)stream);
+}
+
+jfa_status jfa_window_plan(const jfa_params* p, int32_t window, int32_t sinks, const int64_t* offs, void* ws,
+                           size_t ws_bytes, jfa_stream_t stream) {
+  Window w;
+  jfa_status st = check_window(p, window, sinks, &w);
+  if (st != JFA_OK) return st;
+  if ((st = check_ptrs({offs})) != JFA_OK) return st;
+  return run_plan(p, offs, offs, true, ws, ws_bytes, (cudaStream_t)stream, w);
+}
+
+jfa_status jfa_window_fwd(const jfa_params* p, int32_t window, int32_t sinks, const void* q, const void* k,
+                          const void* v, const int64_t* offs, void* o, float* lse, void* ws, size_t ws_bytes,
+                          jfa_stream_t stream) {
+  Window w;
+  jfa_status st = check_window(p, window, sinks, &w);
+  if (st != JFA_OK) return st;
+  return run_fwd(p, Kind::Self, kActSoftmax, q, k, v, offs, offs, o, lse, ws, ws_bytes, (cudaStream_t)stream, nullptr,
+                 0, 0, w);
+}
+
+jfa_status jfa_window_bwd(const jfa_params* p, int32_t window, int32_t sinks, const void* q, const void* k,
+                          const void* v, const void* o, const float* lse, const void* dout, const int64_t* offs,
+                          void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, jfa_stream_t stream) {
+  Window w;
+  jfa_status st = check_window(p, window, sinks, &w);
+  if (st != JFA_OK) return st;
+  return run_bwd(p, Kind::Self, kActSoftmax, q, k, v, o, lse, dout, offs, offs, dq, dk, dv, ws, ws_bytes,
+                 (cudaStream_t)stream, nullptr, 0, 0, nullptr, w);
 }
 
 jfa_status jfa_cross_fwd(const jfa_params* p, const void* q, const void* k, const void* v,

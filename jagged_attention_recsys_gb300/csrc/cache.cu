@@ -231,6 +231,16 @@ cache_kernel(const __grid_constant__ Paged p, T* k_out, T* v_out, PagedHeader* h
   }
 }
 
+}  // namespace
+
+cudaError_t launch_cache_check(const Paged& p, PagedHeader* hdr, cudaStream_t s) {
+  const int64_t need = (p.batch + kThreads - 1) / kThreads, cap = num_sms();
+  cache_check_kernel<<<(unsigned)(need < 1 ? 1 : need < cap ? need : cap), kThreads, 0, s>>>(p, hdr);
+  return cudaGetLastError();
+}
+
+namespace {
+
 template <typename T, int KIND, bool WRITE>
 cudaError_t launch_t(const Paged& p, void* k, void* v, PagedHeader* hdr, int planned, cudaStream_t s) {
   // Runs of up to 32 tokens, as long as lets every warp of a full GPU take the same number of them
@@ -253,9 +263,7 @@ template <bool WRITE>
 cudaError_t launch_kind(const Paged& p, int dtype, void* k, void* v, PagedHeader* hdr, int planned, cudaStream_t s) {
   if (p.total_q == 0) {
     if (planned) return cudaSuccess;
-    const int64_t need = (p.batch + kThreads - 1) / kThreads, cap = num_sms();
-    cache_check_kernel<<<(unsigned)(need < 1 ? 1 : need < cap ? need : cap), kThreads, 0, s>>>(p, hdr);
-    return cudaGetLastError();
+    return launch_cache_check(p, hdr, s);
   }
   if (dtype == JFA_BF16)
     return p.kind == kCacheMx ? launch_t<__nv_bfloat16, kCacheMx, WRITE>(p, k, v, hdr, planned, s)

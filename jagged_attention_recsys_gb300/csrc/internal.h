@@ -70,10 +70,33 @@ struct Problem {
   // block_mask-row block, counted from its sequence's first row (a power of two that the
   // compute warpgroups' column spans divide; 0: whole sequences).
   int block_mask;
+  // Sliding window with sinks (causal): row i sees the keys j <= i with i - j < window, and those with
+  // j < sinks.  window = 0: every key j <= i.
+  int window, sinks;
   // When set, the tensor-core dQ pass writes its rows in fp32 here instead of bf16 into
   // its dq argument (pooled attention's per-sequence query gradients, summed afterwards).
   float* dq_f32;
 };
+
+// The key blocks of `step` keys that the rows [row0, row0 + rows) of a window meet, by number: the
+// first `ns` hold the sinks, the others go on from block `first`.
+struct WindowBlocks {
+  int ns, first;
+  __host__ __device__ __forceinline__ int block(int i) const { return i < ns ? i : i - ns + first; }
+};
+__host__ __device__ __forceinline__ WindowBlocks window_blocks(int window, int sinks, int row0, int step) {
+  WindowBlocks w;
+  const int low = row0 >= window ? row0 - window + 1 : 0;
+  w.first = low / step;
+  const int ns = sinks / step + (sinks % step != 0 ? 1 : 0);
+  w.ns = ns < w.first ? ns : w.first;
+  return w;
+}
+// One past the last row that sees a key of [key0, key0 + keys).
+__host__ __device__ __forceinline__ int window_rows_end(int window, int sinks, int key0, int keys, int lq) {
+  const int64_t end = (int64_t)key0 + keys - 1 + window;
+  return key0 < sinks || end > lq ? lq : (int)end;
+}
 
 // Carve-up of the caller's workspace.
 struct Workspace {

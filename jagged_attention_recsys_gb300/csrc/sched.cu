@@ -105,21 +105,28 @@ __device__ __forceinline__ int tiles_of(const ListSpec& L, int lq, int lk) {
 }
 
 // Inner steps the kernel runs for tile t of a sequence with lengths (lq, lk).
-__device__ __forceinline__ int cost_of(const ListSpec& L, int causal, int lq, int lk, int t) {
+__device__ __forceinline__ int cost_of(const Problem& p, const ListSpec& L, int causal, int lq, int lk, int t) {
   if (!L.key_major) {
     const int keys = causal ? min(lk, (t + 1) * L.tile) : lk;
-    return cdiv_shift(keys, L.step_shift);
+    const int n = cdiv_shift(keys, L.step_shift);
+    if (p.window == 0) return n;
+    const WindowBlocks w = window_blocks(p.window, p.sinks, t * L.tile, L.step);
+    return n - w.first + w.ns;
   }
+  if (p.window > 0)
+    return max(0, cdiv_shift(window_rows_end(p.window, p.sinks, t * L.tile, L.tile, lq), L.step_shift) -
+                      ((t * L.tile) >> L.step_shift));
   if (!causal) return cdiv_shift(lq, L.step_shift);
   // rows >= the first key of this tile, counted in whole inner steps
   return max(0, cdiv_shift(lq, L.step_shift) - ((t * L.tile) >> L.step_shift));
 }
 
 // Total cost of a sequence's n tiles: closed form where every tile costs the same.
-__device__ __forceinline__ long long total_cost(const ListSpec& L, int causal, int lq, int lk, int n) {
-  if (!causal) return (long long)n * cost_of(L, 0, lq, lk, 0);
+__device__ __forceinline__ long long total_cost(const Problem& p, const ListSpec& L, int causal, int lq, int lk,
+                                                int n) {
+  if (!causal) return (long long)n * cost_of(p, L, 0, lq, lk, 0);
   long long c = 0;
-  for (int t = 0; t < n; ++t) c += cost_of(L, causal, lq, lk, t);
+  for (int t = 0; t < n; ++t) c += cost_of(p, L, causal, lq, lk, t);
   return c;
 }
 
@@ -159,7 +166,7 @@ __device__ void build_list(const Problem& p, const ListSpec& L, const Arrays& A,
   for (int b = tid; b < B; b += kThreads) {
     const int4 s = A.seq[b];
     const int n = tiles_of(L, s.z, s.w);
-    const long long c = total_cost(L, p.causal, s.z, s.w, n);
+    const long long c = total_cost(p, L, p.causal, s.z, s.w, n);
     A.ntile[b] = n;
     const int ci = (int)min(c, (long long)0x7fffffff);
     A.bucket[b] = ci;  // total cost for now
@@ -301,7 +308,7 @@ __device__ void build_list(const Problem& p, const ListSpec& L, const Arrays& A,
       const int b = A.order[lo];
       fs = A.seq[b];
       const int t = tile_at(L, p.causal, A.ntile[b], u - A.first[lo]);
-      fa = make_int4(b, 0, t, cost_of(L, p.causal, fs.z, fs.w, t));
+      fa = make_int4(b, 0, t, cost_of(p, L, p.causal, fs.z, fs.w, t));
     }
     const int n = min(32, u_hi - u0) * H;  // items of this warp's units
     int4* dst = reinterpret_cast<int4*>(list + (int64_t)u0 * H);

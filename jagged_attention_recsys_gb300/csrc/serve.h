@@ -136,6 +136,10 @@ void paged_set_test_hold(int on);
 cudaError_t launch_cache_write(const Paged& p, int dtype, PagedHeader* hdr, int planned, cudaStream_t s);
 cudaError_t launch_cache_read(const Paged& p, int dtype, void* k, void* v, PagedHeader* hdr, int planned,
                               cudaStream_t s);
+// The batch of a call without tokens, checked.
+cudaError_t launch_cache_check(const Paged& p, PagedHeader* hdr, cudaStream_t s);
+// a.side: queries (heads 0: none) and keys; p.v, p.sv: values.
+cudaError_t launch_append(const Paged& p, const NormRopeArgs& a, int dtype, PagedHeader* hdr, int planned, cudaStream_t s);
 cudaError_t launch_paged_plan(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
 cudaError_t launch_paged_simt(const Paged& p, const TileShape& t, int ctas, int dtype, const PagedWs& w,
                               cudaStream_t s);

@@ -352,6 +352,53 @@ jfa_status jfa_cache_write(const jfa_paged_params* p, const void* k, const void*
   return cu(launch_cache_write(r, p->dtype, w.hdr, p->flags & JFA_PLANNED, s));
 }
 
+jfa_status jfa_rope_append(const jfa_paged_params* p, const jfa_rope* rope, int32_t norm, float eps, const void* q,
+                           const void* k, const void* v, const int64_t* pos, const float* wq, const float* wk,
+                           const int64_t* offs, const int64_t* lens, const int32_t* table, void* yq, int64_t stride_yq,
+                           void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale, void* ws, size_t ws_bytes,
+                           jfa_stream_t stream) {
+  jfa_status st = check_paged(p);
+  if (st != JFA_OK) return st;
+  // norm and rotation of the queries and keys, as in jfa_norm_rope_fwd
+  jfa_norm_rope_params n{};
+  n.tokens = p->total_q;
+  n.heads_q = q ? p->heads_q : 0;
+  n.heads_k = p->heads_k;
+  n.dim = p->dim_qk;
+  n.dtype = p->dtype;
+  n.norm = norm;
+  n.eps = eps;
+  if (rope) n.rope = *rope;
+  if ((st = check_norm_rope(&n)) != JFA_OK) return st;
+  if (!q && yq) return JFA_ERR_INVALID_ARG;
+  if ((st = check_index(p, offs, lens, table)) != JFA_OK ||
+      (st = check_cache(p, k_cache, v_cache, k_scale, v_scale)) != JFA_OK ||
+      (st = check_rows(p, k, p->stride_k, (int64_t)p->heads_k * p->dim_qk)) != JFA_OK ||
+      (st = check_rows(p, v, p->stride_v, (int64_t)p->heads_k * p->dim_v)) != JFA_OK)
+    return st;
+  const int64_t row = (int64_t)p->heads_q * p->dim_qk;
+  if (q && ((st = check_rows(p, q, p->stride_q, row)) != JFA_OK || (st = check_rows(p, yq, stride_yq, row)) != JFA_OK))
+    return st;
+  NormRopeArgs a;
+  if ((st = norm_rope_side(&n, n.heads_q, q, p->stride_q, nullptr, 0, false, wq, yq, stride_yq, nullptr, &a.side[0])) !=
+          JFA_OK ||
+      (st = norm_rope_side(&n, n.heads_k, k, p->stride_k, nullptr, 0, false, wk, const_cast<void*>(k), p->stride_k,
+                           nullptr, &a.side[1])) != JFA_OK)  // (their output is the cache)
+    return st;
+  if (pos && !aligned(pos, 8)) return JFA_ERR_INVALID_ARG;
+  norm_rope_common(&n, pos, &a);
+  Paged r = make_paged(p, offs, lens, table, k_cache, v_cache, k_scale, v_scale);
+  PagedWs w;
+  if ((st = check_ws(r, ws, ws_bytes, &w)) != JFA_OK) return st;
+  r.v = v;
+  cudaStream_t s = (cudaStream_t)stream;
+  Timed t(JFA_KERNEL_CACHE, s);
+  if ((st = cache_status(p, w, s)) != JFA_OK) return st;
+  const int planned = p->flags & JFA_PLANNED;
+  if (p->total_q == 0) return planned ? JFA_OK : cu(launch_cache_check(r, w.hdr, s));
+  return cu(launch_append(r, a, p->dtype, w.hdr, planned, s));
+}
+
 jfa_status jfa_cache_read(const jfa_paged_params* p, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
                           const uint8_t* v_scale, const int64_t* offs, const int64_t* lens, const int32_t* table,
                           void* k, void* v, void* ws, size_t ws_bytes, jfa_stream_t stream) {

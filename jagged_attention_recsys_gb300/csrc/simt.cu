@@ -55,6 +55,11 @@ __device__ __forceinline__ float q_factor(const Problem& p) {
   return p.act == kActSoftmax ? p.scale * kLog2e : p.scale;
 }
 
+// Whether row i sees key j <= i under the window.
+__device__ __forceinline__ bool in_window(const Problem& p, int i, int j) {
+  return p.window == 0 || i - j < p.window || j < p.sinks;
+}
+
 template <typename T, int DQ, int DV>
 struct SimtFwdSmem {
   float q[kTileRows][DQ];
@@ -96,7 +101,9 @@ simt_fwd_kernel(Problem p, const T* __restrict__ q, const T* __restrict__ k,
       for (int t = 0; t < DV / 32; ++t) acc[rr][t] = 0.f;
     }
     const int kend = p.causal ? min(Lk, row0 + kTileRows) : Lk;
-    for (int kb = 0; kb < kend; kb += kStep) {
+    const WindowBlocks wb = p.window > 0 ? window_blocks(p.window, p.sinks, row0, kStep) : WindowBlocks{0, 0};
+    for (int step = 0; wb.block(step) * kStep < kend; ++step) {
+      const int kb = wb.block(step) * kStep;
       __syncthreads();
       for (int idx = tid; idx < kStep * DQ; idx += kThreads) {
         int r = idx / DQ, d = idx % DQ;
@@ -114,7 +121,7 @@ simt_fwd_kernel(Problem p, const T* __restrict__ q, const T* __restrict__ k,
         float s = 0.f;
 #pragma unroll 8
         for (int d = 0; d < DQ; ++d) s = fmaf(sm.q[r][d], sm.k[lane][d], s);
-        const bool valid = j < Lk && (!p.causal || j <= i);
+        const bool valid = j < Lk && (!p.causal || j <= i) && in_window(p, i, j);
         s -= valid ? 0.f : kMaskShift;
         float pj;
         if (p.act == kActSoftmax) {
@@ -219,7 +226,9 @@ simt_dq_kernel(Problem p, const T* __restrict__ q, const T* __restrict__ k,
       for (int t = 0; t < DQ / 32; ++t) acc[rr][t] = 0.f;
     }
     const int kend = p.causal ? min(Lk, row0 + kTileRows) : Lk;
-    for (int kb = 0; kb < kend; kb += kStep) {
+    const WindowBlocks wb = p.window > 0 ? window_blocks(p.window, p.sinks, row0, kStep) : WindowBlocks{0, 0};
+    for (int step = 0; wb.block(step) * kStep < kend; ++step) {
+      const int kb = wb.block(step) * kStep;
       __syncthreads();
       for (int idx = tid; idx < kStep * DQ; idx += kThreads) {
         int r = idx / DQ, d = idx % DQ;
@@ -239,7 +248,7 @@ simt_dq_kernel(Problem p, const T* __restrict__ q, const T* __restrict__ k,
         for (int d = 0; d < DQ; ++d) s = fmaf(sm.q[r][d], sm.k[lane][d], s);
 #pragma unroll 8
         for (int d = 0; d < DV; ++d) dp = fmaf(sm.dout[r][d], sm.v[lane][d], dp);
-        const bool valid = i < Lq && j < Lk && (!p.causal || j <= i);
+        const bool valid = i < Lq && j < Lk && (!p.causal || j <= i) && in_window(p, i, j);
         s -= valid ? 0.f : kMaskShift;
         float ds;
         if (softmax) {
@@ -322,7 +331,8 @@ simt_dkdv_kernel(Problem p, const T* __restrict__ q, const T* __restrict__ k,
     }
     // causal: only rows >= key0 can see this tile (start on a step boundary)
     const int qstart = p.causal ? (key0 / kStep) * kStep : 0;
-    for (int qb = qstart; qb < Lq; qb += kStep) {
+    const int qend = p.window > 0 ? window_rows_end(p.window, p.sinks, key0, kTileRows, Lq) : Lq;
+    for (int qb = qstart; qb < qend; qb += kStep) {
       __syncthreads();
       for (int idx = tid; idx < kStep * DQ; idx += kThreads) {
         int r = idx / DQ, d = idx % DQ;
@@ -347,7 +357,7 @@ simt_dkdv_kernel(Problem p, const T* __restrict__ q, const T* __restrict__ k,
         for (int d = 0; d < DQ; ++d) s = fmaf(sm.q[lane][d], sm.k[r][d], s);
 #pragma unroll 8
         for (int d = 0; d < DV; ++d) dp = fmaf(sm.dout[lane][d], sm.v[r][d], dp);
-        const bool valid = i < Lq && j < Lk && (!p.causal || j <= i);
+        const bool valid = i < Lq && j < Lk && (!p.causal || j <= i) && in_window(p, i, j);
         s -= valid ? 0.f : kMaskShift;
         float pi, ds;
         if (softmax) {

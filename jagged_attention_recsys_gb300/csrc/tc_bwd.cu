@@ -270,7 +270,9 @@ __device__ __forceinline__ bool kv_rotate_next(int& rot_next, uint32_t& rot_cnt,
   return true;
 }
 
-template <int DQK, int DV, int ACT, bool CAUSAL, bool ROPE>
+// WIN: a sliding window with sinks (softmax, causal).  A key tile's rows are still one stretch, which
+// ends with the last row whose window reaches the tile (the sinks' tiles: with the sequence).
+template <int DQK, int DV, int ACT, bool CAUSAL, bool ROPE, bool WIN>
 __global__ void __launch_bounds__(KvGroups<ACT>::kThreads, 1)
 tc_dkdv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -710,6 +712,7 @@ tc_dkdv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int lo = CAUSAL ? j - i0 : 0;
         int hi = j < Lk ? Lq - i0 : 0;
         if (p.block_mask > 0 && (j ^ i0) >= p.block_mask) hi = 0;  // another block's queries
+        if (WIN && j >= p.sinks) hi = min(hi, j - i0 + p.window);
         if (lo > 0 || hi < HC) {
 #pragma unroll
           for (int c = 0; c < HC; ++c) sv[c] -= (c >= lo && c < hi) ? 0.f : shift_raw;
@@ -900,7 +903,8 @@ __device__ __forceinline__ bool q_rotate_next(int& rot_next, uint32_t& rot_cnt, 
   return true;
 }
 
-template <int DQK, int DV, int ACT, bool CAUSAL, bool ROPE>
+// WIN: a sliding window with sinks, as in the forward.
+template <int DQK, int DV, int ACT, bool CAUSAL, bool ROPE, bool WIN>
 __global__ void __launch_bounds__(QGroups<ACT>::kThreads, 1)
 tc_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
              const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -1020,6 +1024,7 @@ tc_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         if (n == 0) continue;
         const int h = w.h, row0 = w.tile * TILE;
         const int32_t q0 = w.q0, k0 = w.k0;
+        const WindowBlocks wb = WIN ? window_blocks(p.window, p.sinks, row0, STEP) : WindowBlocks{0, 0};
         const uint32_t qs = q_it % nrow, qph = ((q_it / nrow) & 1) ^ 1;
         if (!mbar_wait(bar(b_rempty + qs), qph, abort, status)) break;
         mbar_expect_tx(bar(b_rfull + qs), row_bytes);
@@ -1035,8 +1040,8 @@ tc_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
           }
           mbar_expect_tx(bar(b_kfull + st), key_bytes);
           for (int a = 0; a < D / 64; ++a)
-            tma_load_2d(sb + key_off + st * key_bytes + a * 16384, tm_key, h * D + a * 64, k0 + j * STEP,
-                        bar(b_kfull + st));
+            tma_load_2d(sb + key_off + st * key_bytes + a * 16384, tm_key, h * D + a * 64,
+                        k0 + wb.block(j) * STEP, bar(b_kfull + st));
         }
       }
       // every load issued has landed before the CTA leaves (also after giving up)
@@ -1305,6 +1310,7 @@ tc_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
       }
       const float inv_len = 1.0f / (float)max(Lq, 1);
       const float2 hl = make_float2(0.5f * inv_len, 0.5f * inv_len);
+      const WindowBlocks wb = WIN ? window_blocks(p.window, p.sinks, row0, STEP) : WindowBlocks{0, 0};
       float2 rsv = make_float2(0.f, 0.f);
       if (ACT == kActSoftmax && row_ok && n > 0) rsv = rowstat[(int64_t)h * p.total_q + q0 + i];
       const float2 nl = make_float2(-rsv.x, -rsv.x), nd = make_float2(-rsv.y, -rsv.y);
@@ -1317,12 +1323,19 @@ tc_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
         for (int c = 0; c < HC / 32; ++c) tmem_ld32(s_tm + 32 * c, sv + 32 * c);
         tmem_wait_ld();
-        const int kb = step * STEP + grp * HC;
+        const int kb = wb.block(step) * STEP + grp * HC;
         int nvalid = Lk - kb;
         if (CAUSAL) nvalid = min(nvalid, i - kb + 1);
         if (p.block_mask > 0 && (kb ^ i) >= p.block_mask) nvalid = 0;  // another block's keys
         if (!row_ok) nvalid = 0;
-        if (nvalid < HC) {
+        if (WIN) {
+          // the row's window, and the sinks
+          const int from = max(i - p.window + 1, 0) - kb, front = p.sinks - kb;
+          if (nvalid < HC || (from > 0 && front < HC)) {
+#pragma unroll
+            for (int c = 0; c < HC; ++c) sv[c] -= c < nvalid && (c >= from || c < front) ? 0.f : shift_raw;
+          }
+        } else if (nvalid < HC) {
 #pragma unroll
           for (int c = 0; c < HC; ++c) sv[c] -= c < nvalid ? 0.f : shift_raw;
         }
@@ -1432,10 +1445,10 @@ bool make_maps(const Problem& p, const void* q, const void* k, const void* v, co
          make_tile_map(&m->k, kk, tk, cq, 64, TILE) && make_tile_map(&m->v, vv, tk, cv, 64, TILE);
 }
 
-template <int DQK, int DV, int ACT, bool CAUSAL, bool ROPE = false>
+template <int DQK, int DV, int ACT, bool CAUSAL, bool ROPE = false, bool WIN = false>
 cudaError_t dkdv_t(const Maps& m, const Problem& p, const float2* rowstat, void* dk, void* dv,
                    const Workspace& ws, cudaStream_t s) {
-  auto kern = tc_dkdv_kernel<DQK, DV, ACT, CAUSAL, ROPE>;
+  auto kern = tc_dkdv_kernel<DQK, DV, ACT, CAUSAL, ROPE, WIN>;
   constexpr uint32_t smem = KvLayout<DQK, DV>::SMEM;
   cudaError_t e = kernel_setup((const void*)kern, KvGroups<ACT>::kThreads, smem);
   if (e != cudaSuccess) return e;
@@ -1444,10 +1457,10 @@ cudaError_t dkdv_t(const Maps& m, const Problem& p, const float2* rowstat, void*
   return cudaGetLastError();
 }
 
-template <int DQK, int DV, int ACT, bool CAUSAL, bool ROPE = false>
+template <int DQK, int DV, int ACT, bool CAUSAL, bool ROPE = false, bool WIN = false>
 cudaError_t dq_t(const Maps& m, const Problem& p, const float2* rowstat, void* dq,
                  const Workspace& ws, cudaStream_t s) {
-  auto kern = tc_dq_kernel<DQK, DV, ACT, CAUSAL, ROPE>;
+  auto kern = tc_dq_kernel<DQK, DV, ACT, CAUSAL, ROPE, WIN>;
   constexpr uint32_t smem = QLayout<DQK, DV>::SMEM;
   cudaError_t e = kernel_setup((const void*)kern, QGroups<ACT>::kThreads, smem);
   if (e != cudaSuccess) return e;
@@ -1466,6 +1479,13 @@ cudaError_t dq_t(const Maps& m, const Problem& p, const float2* rowstat, void* d
       if (p.dim_qk == 64) return c_ ? FN<64, 64, kActSoftmax, true, true>(__VA_ARGS__)        \
                                     : FN<64, 64, kActSoftmax, false, true>(__VA_ARGS__);      \
       return cudaErrorInvalidValue;                                                           \
+    }                                                                                         \
+    if (p.window > 0) { /* a window: causal softmax */                                        \
+      if (!sm_ || !c_) return cudaErrorInvalidValue;                                          \
+      if (p.dim_qk == 128) return p.dim_v == 128 ? FN<128, 128, kActSoftmax, true, false, true>(__VA_ARGS__) \
+                                                 : FN<128, 64, kActSoftmax, true, false, true>(__VA_ARGS__); \
+      return p.dim_v == 128 ? FN<64, 128, kActSoftmax, true, false, true>(__VA_ARGS__)        \
+                            : FN<64, 64, kActSoftmax, true, false, true>(__VA_ARGS__);        \
     }                                                                                         \
     if (p.dim_qk == 128 && p.dim_v == 128) {                                                  \
       if (sm_) return c_ ? FN<128, 128, kActSoftmax, true>(__VA_ARGS__)                       \

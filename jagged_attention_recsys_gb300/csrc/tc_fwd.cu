@@ -145,7 +145,9 @@ __device__ __forceinline__ bool fwd_rotate_next(int& rot_next, uint32_t& rot_cnt
 // MMA is issued and the CTA leaves through its abort path.  Zero unless a test sets it.
 __device__ int g_test_hold = 0;
 
-template <int DQK, int DV, int ACT, bool CAUSAL, bool ROPE>
+// WIN: a sliding window with sinks (softmax, causal); its items' steps are the window's key blocks,
+// the sinks' in front of them.
+template <int DQK, int DV, int ACT, bool CAUSAL, bool ROPE, bool WIN>
 __global__ void __launch_bounds__(FwdRoles<ACT>::kThreads, 1)
 tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const Problem p,
@@ -252,6 +254,7 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       while (ok && (qk ? claimer.claim(w, abort, status) : feed.take(w, false, true, abort, status))) {
         const int n = w.cost;
         if (n == 0) continue;
+        const WindowBlocks wb = WIN ? window_blocks(p.window, p.sinks, w.tile * BM, BN) : WindowBlocks{0, 0};
         if (qk) {
           const uint32_t qs = q_it % L::NQB;
           if (!mbar_wait(bar(B_QEMPTY + qs), ((q_it / L::NQB) & 1) ^ 1, abort, status)) break;
@@ -270,7 +273,7 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
             for (int a = 0; a < DQK / 64; ++a)
               tma_load_2d(sb + L::K_OFF + st * L::K_BYTES + a * 16384, &tm_k, w.h * DQK + a * 64,
-                          w.k0 + j * BN, bar(B_KFULL + st));
+                          w.k0 + wb.block(j) * BN, bar(B_KFULL + st));
           } else {
             const uint32_t st = t_it % NV;
             if (!mbar_wait(bar(B_VEMPTY + st), ((t_it / NV) & 1) ^ 1, abort, status)) { ok = false; break; }
@@ -278,7 +281,7 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
             for (int a = 0; a < DV / 64; ++a)
               tma_load_2d(sb + L::V_OFF + st * L::V_BYTES + a * 16384, &tm_v, w.h * DV + a * 64,
-                          w.k0 + j * BN, bar(B_VFULL + st));
+                          w.k0 + wb.block(j) * BN, bar(B_VFULL + st));
           }
         }
       }
@@ -434,6 +437,7 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       }
       const int i = w.tile * BM + r;
       const float inv_len = 1.0f / (float)max(Lq, 1);
+      const WindowBlocks wb = WIN ? window_blocks(p.window, p.sinks, w.tile * BM, BN) : WindowBlocks{0, 0};
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++p_it) {
         const uint32_t b = p_it & 1;
@@ -443,11 +447,18 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         float sv[HC];
         tmem_ld<HC>(s_tm, sv);
         tmem_wait_ld();
-        const int kb = j * BN + grp * HC;
+        const int kb = wb.block(j) * BN + grp * HC;
         int nvalid = Lk - kb;
         if (CAUSAL) nvalid = min(nvalid, i - kb + 1);
         if (p.block_mask > 0 && (kb ^ i) >= p.block_mask) nvalid = 0;  // another block's keys
-        if (nvalid < HC) {
+        if (WIN) {
+          // the row's window, and the sinks
+          const int from = max(i - p.window + 1, 0) - kb, front = p.sinks - kb;
+          if (nvalid < HC || (from > 0 && front < HC)) {
+#pragma unroll
+            for (int c = 0; c < HC; ++c) sv[c] -= c < nvalid && (c >= from || c < front) ? 0.f : shift_raw;
+          }
+        } else if (nvalid < HC) {
 #pragma unroll
           for (int k = 0; k < HC; ++k) sv[k] -= k < nvalid ? 0.f : shift_raw;
         }
@@ -580,11 +591,11 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   }
 }
 
-template <int DQK, int DV, int ACT, bool CAUSAL, bool ROPE = false>
+template <int DQK, int DV, int ACT, bool CAUSAL, bool ROPE = false, bool WIN = false>
 cudaError_t launch_fwd_t(const Problem& p, const CUtensorMap& mq, const CUtensorMap& mk,
                          const CUtensorMap& mv, void* o, float* lse, const Workspace& ws,
                          cudaStream_t s) {
-  auto kern = tc_fwd_kernel<DQK, DV, ACT, CAUSAL, ROPE>;
+  auto kern = tc_fwd_kernel<DQK, DV, ACT, CAUSAL, ROPE, WIN>;
   constexpr uint32_t smem = FwdLayout<DQK, DV>::SMEM;
   constexpr int threads = FwdRoles<ACT>::kThreads;
   cudaError_t e = kernel_setup((const void*)kern, threads, smem);
@@ -604,6 +615,10 @@ cudaError_t launch_fwd_d(const Problem& p, const CUtensorMap& mq, const CUtensor
                         : launch_fwd_t<DQK, DV, kActSoftmax, false, true>(p, mq, mk, mv, o, lse, ws, s);
     }
     return cudaErrorInvalidValue;
+  }
+  if (p.window > 0) {
+    if (p.act != kActSoftmax || !p.causal) return cudaErrorInvalidValue;
+    return launch_fwd_t<DQK, DV, kActSoftmax, true, false, true>(p, mq, mk, mv, o, lse, ws, s);
   }
   if (p.act == kActSoftmax)
     return p.causal ? launch_fwd_t<DQK, DV, kActSoftmax, true>(p, mq, mk, mv, o, lse, ws, s)
