@@ -501,7 +501,7 @@ jfa_status jfa_paged_fwd(const jfa_paged_params* p, const void* q, const void* k
  * token, those before the cache's start too.  On an invalid batch (JFA_ERR_BAD_OFFSETS) yq and the rows
  * written are undefined; a planned call on one computes nothing.
  * q, k, v and yq are 16-byte aligned, with strides of whole 16 bytes; pointers and strides of whole 32
- * bytes in fp32, with dim_qk and rope.dim multiples of 16 and dim_v of 8, take the fast kernel.
+ * bytes in fp32, with dim_qk, rope.dim and dim_v multiples of 16, take the fast kernel.
  */
 jfa_status jfa_rope_append(const jfa_paged_params* p, const jfa_rope* rope, int32_t norm, float eps,
                            const void* q, const void* k, const void* v, const int64_t* pos,
