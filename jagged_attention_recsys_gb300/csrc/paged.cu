@@ -256,7 +256,9 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
 
 // --------------------------------------------------------------------------- the join
 // A warp a row: the parts of a split tile, rescaled to their common maximum and added in CTA
-// order.  CTA x of the grid serves the tile whose parts begin with CTA x's last one.
+// order.  CTA x of the grid serves the tile whose parts begin with CTA x's last one.  A row a warp, with
+// the parts' places and statistics a lane each and four parts' rows on their way: 16 tiles of 256 rows in
+// ten parts each take JOIN_NEW us, where eight rows a warp and one part after the other took 60.
 constexpr int kJoinWarps = 4;
 
 template <typename T>
@@ -272,34 +274,70 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
     st = __reduce_max_sync(0xffffffffu, st);
     if (lane == 0) w.hdr->status = st == 1 ? (int)JFA_ERR_BAD_PAGES : st;
   }
-  // the CTAs that hold the tile's parts: c (slot 1), then c + 1 .. last (slot 0)
+  // the CTAs that hold the tile's parts: c (slot 1), then c + 1 .. last (slot 0), looked up 32 at a time
   PagedCutTile cut;
-  if (!cut.find(p, t, w, ctas, c)) return;
+  if (!cut.begins(p, t, w, ctas, c)) return;
   const PagedSeq& seq = cut.seq;
-  const int last = cut.last;
+  int last = c + 1;
+  for (;;) {
+    const unsigned on = __ballot_sync(0xffffffffu, cut.goes_on(p, t, w, ctas, last + 1 + lane));
+    if (on != ~0u) {
+      last += __ffs(~on) - 1;
+      break;
+    }
+    last += 32;
+  }
+  auto empty = [&](int i) {  // a CTA without work inside the tile
+    const PagedPos a = paged_pos(p, t, w, i), e = paged_pos(p, t, w, i + 1);
+    return i != c && cut.same(e) && a.blk >= e.blk;
+  };
   for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < t.rows; r += gridDim.y * kJoinWarps) {
     int tok, head;
     if (!cut.row(p, t, r, tok, head)) continue;
     auto slot_row = [&](int i) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * t.rows + r; };
-    auto empty = [&](int i) {  // a CTA without work inside the tile
-      const PagedPos a = paged_pos(p, t, w, i), e = paged_pos(p, t, w, i + 1);
-      return i != c && cut.same(e) && a.blk >= e.blk;
-    };
-    float m = -INFINITY;
-    for (int i = c + lane; i <= last; i += 32)
-      if (!empty(i)) m = fmaxf(m, w.part_ml[2 * slot_row(i)]);
+    // this lane's parts: statistics of the first 32, whose rows' loads then need not wait for them
+    float m = -INFINITY, m0 = -INFINITY, l0 = 0.f;
+    for (int i = c + lane; i <= last; i += 32) {
+      if (empty(i)) continue;
+      const float2 x = *reinterpret_cast<const float2*>(w.part_ml + 2 * slot_row(i));
+      m = fmaxf(m, x.x);
+      if (i == c + lane) {
+        m0 = x.x;
+        l0 = x.y;
+      }
+    }
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float ref = m == -INFINITY ? 0.f : m;
     float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};  // columns lane + 32 i
-    for (int i = c; i <= last; ++i) {
-      if (empty(i)) continue;
-      const int64_t pr = slot_row(i);
-      const float f = exp2f(w.part_ml[2 * pr] - ref);
-      l = fmaf(w.part_ml[2 * pr + 1], f, l);
-      if (w.part_ml[2 * pr] == -INFINITY) continue;  // no keys: the part has no output
+    for (int i0 = c; i0 <= last; i0 += 32) {
+      float mi = m0, li = l0;
+      if (i0 > c) {
+        const bool has = i0 + lane <= last && !empty(i0 + lane);
+        const float2 x = has ? *reinterpret_cast<const float2*>(w.part_ml + 2 * slot_row(i0 + lane)) : make_float2(-INFINITY, 0.f);
+        mi = x.x;
+        li = x.y;
+      }
+      const float fi = exp2f(mi - ref);
+      // a part without keys has no output (nor has an empty CTA): its maximum says so
+      const unsigned full = __ballot_sync(0xffffffffu, mi != -INFINITY);
+      constexpr int U = 4;  // parts whose rows are on their way
+      for (int i = 0; i < 32 && i0 + i <= last; i += U) {
+        float x[U][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (lane + 32 * k < p.dim_v) acc[k] = fmaf(w.part_o[pr * p.dim_v + lane + 32 * k], f, acc[k]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            x[u][k] = (full >> (i + u)) & 1 && lane + 32 * k < p.dim_v
+                          ? w.part_o[slot_row(i0 + i + u) * p.dim_v + lane + 32 * k] : 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float f = __shfl_sync(0xffffffffu, fi, i + u);
+          l = fmaf(__shfl_sync(0xffffffffu, li, i + u), f, l);
+          if (!((full >> (i + u)) & 1)) continue;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[k] = fmaf(x[u][k], f, acc[k]);
+        }
+      }
     }
     const int64_t orow = (int64_t)(seq.q0 + tok) * p.heads_q + head;
     RowEnd<T> end(p, orow, m, l);
@@ -404,6 +442,7 @@ size_t shared_layout(const Paged& prefix, const Paged& own, void* base, PagedWs*
   size_t off = paged_layout(own, base, second);
   *first = *second;
   off = plan_layout(prefix.batch, b, off, first);
+  if (paged_short(own)) first->hdr = second->hdr;
   *prior_lse = (float*)(b + off);
   off = up256(off + sizeof(float) * (size_t)own.total_q * own.heads_q);
   *prior_o = (float*)(b + off);
@@ -426,8 +465,7 @@ cudaError_t launch_paged_simt(const Paged& p, const TileShape& t, int ctas, int 
 
 cudaError_t launch_paged_combine(const Paged& p, const TileShape& t, int ctas, int dtype, const PagedWs& w,
                                  cudaStream_t s) {
-  int gy = (t.rows + kJoinWarps - 1) / kJoinWarps;
-  if (gy > 8) gy = 8;
+  const int gy = (t.rows + kJoinWarps - 1) / kJoinWarps;  // a row a warp
   if (dtype == JFA_BF16)
     paged_join_kernel<__nv_bfloat16><<<dim3(ctas, gy), kJoinWarps * 32, 0, s>>>(p, t, ctas, w);
   else

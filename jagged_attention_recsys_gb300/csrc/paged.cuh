@@ -285,15 +285,22 @@ struct PagedCutTile {
     return x.b == end.b && x.unit == end.unit && x.tile == end.tile;
   }
   // False: no tile is cut here, or it begins in an earlier CTA's share, or the plan is another request's.
-  __device__ __forceinline__ bool find(const Paged& p, const TileShape& t, const PagedWs& w, int ctas, int c) {
+  __device__ __forceinline__ bool begins(const Paged& p, const TileShape& t, const PagedWs& w, int ctas, int c) {
     end = paged_pos(p, t, w, c + 1);
     if (end.blk == 0 || end.b >= p.batch || c + 1 == ctas) return false;
     const PagedPos at = paged_pos(p, t, w, c);
     if (same(at) && at.blk > 0) return false;
     seq = paged_seq(p, t, end.b);
-    if (end.tile >= seq.tiles) return false;
+    return end.tile < seq.tiles;
+  }
+  // Whether CTA i, whose parts would follow CTA i - 1's, has work of the tile (or a share that is empty).
+  __device__ __forceinline__ bool goes_on(const Paged& p, const TileShape& t, const PagedWs& w, int ctas, int i) const {
+    return i < ctas && same(paged_pos(p, t, w, i));
+  }
+  __device__ __forceinline__ bool find(const Paged& p, const TileShape& t, const PagedWs& w, int ctas, int c) {
+    if (!begins(p, t, w, ctas, c)) return false;
     last = c + 1;
-    while (last + 1 < ctas && same(paged_pos(p, t, w, last + 1))) ++last;
+    while (goes_on(p, t, w, ctas, last + 1)) ++last;
     return true;
   }
   // Token and head of row r; false: it has none.

@@ -126,7 +126,8 @@ TileShape paged_shape(const Paged& p, int kernel);
 int paged_ctas(const Paged& p, int kernel);
 size_t paged_layout(const Paged& p, void* base, PagedWs* out);
 // The workspace of attention over a shared prefix: phase 2's, then phase 1's header and plan (its
-// parts lie in phase 2's place, which begins behind it) and its results.
+// parts lie in phase 2's place, which begins behind it) and its results.  Where phase 2 is the short
+// kernel's, both have the first header.
 size_t shared_layout(const Paged& prefix, const Paged& own, void* base, PagedWs* first, PagedWs* second, float** prior_o,
                      float** prior_lse);
 
@@ -150,6 +151,11 @@ cudaError_t launch_paged_rows16_shared(const Paged& p, const TileShape& t, int c
 cudaError_t launch_paged_tc(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
 cudaError_t launch_paged_tc_window(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
 cudaError_t launch_paged_tc_shared(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
+// Phase 2 of a shared prefix where the pages of a sequence have room for few keys.  hdr: phase 1's header,
+// whose status it goes on with.
+constexpr int kShortKeys = 128;
+bool paged_short(const Paged& p);
+cudaError_t launch_paged_short(const Paged& p, int dtype, PagedHeader* hdr, cudaStream_t s);
 cudaError_t launch_paged_combine(const Paged& p, const TileShape& t, int ctas, int dtype, const PagedWs& w,
                                  cudaStream_t s);
 

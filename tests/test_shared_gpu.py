@@ -14,14 +14,19 @@ pytestmark = pytest.mark.gpu
 class Shared(Batch):
     """Sequences in groups: the prefixes are sequences of the same cache, without new tokens."""
 
-    def __init__(self, groups, prefix, new, lens, hk, dqk, dv, page, cache, dtype, seed=0):
+    def __init__(self, groups, prefix, new, lens, hk, dqk, dv, page, cache, dtype, seed=0, wide=False):
         super().__init__(list(new) + [0] * len(prefix), list(lens) + list(prefix), hk, dqk, dv, page, cache, dtype, seed)
         self.G, self.S = len(groups), len(new)
         assert sum(groups) == self.S and len(prefix) == self.G
         self.group_h = np.concatenate([[0], np.cumsum(groups)]).astype(np.int64)
         self.groups = torch.tensor(self.group_h, device="cuda")
         self.prefix_table, self.prefix_lens = self.table[self.S:].contiguous(), self.lens[self.S:].clone()
-        self.own = (self.cache, self.table[:self.S].contiguous(), self.offs[:self.S + 1].clone(), self.lens[:self.S].clone())
+        # a table of few pages takes the kernel for few keys, a wide one the tiled kernels
+        width = self.table.shape[1] if wide else max([-(-int(n) // page) for n in lens] + [0]) + 1
+        if wide and width * page <= 128:
+            width = 128 // page + 1
+        own = torch.nn.functional.pad(self.table[:self.S], (0, max(0, width - self.table.shape[1])), value=-1)
+        self.own = (self.cache, own[:, :width].contiguous(), self.offs[:self.S + 1].clone(), self.lens[:self.S].clone())
 
     def call(self, q, **kw):
         return jfa.jfa_shared_fwd(q, *self.own, self.prefix_table, self.prefix_lens, self.groups, **kw)
@@ -84,6 +89,10 @@ def shape(kind):
     if kind == "many":  # more than one CTA scans by itself: a launch of its own for the plan
         g = [40, 0, 660]
         return g, [100, 5, 333], [1] * 700, rng.integers(1, 30, 700).tolist()
+    if kind == "few keys":  # up to as many own keys as the kernel for few serves, and more sequences than a CTA checks
+        g = [100, 1300, 3]
+        new = rng.integers(0, 4, 1403)
+        return g, [70, 40, 200], new.tolist(), np.minimum(new + rng.integers(-1, 100, 1403), 112).clip(0).tolist()
     if kind == "many groups":
         g = rng.integers(0, 3, 600).tolist()
         n = sum(g)
@@ -116,15 +125,21 @@ CASES = [
     ("chunks", "bf16", "bf16", 130, 1, 64, 64, 64, True),
     ("many", "bf16", "bf16", 4, 4, 64, 64, 16, True),
     ("many", "bf16", "mxfp8", 8, 2, 128, 128, 16, True),
+    ("few keys", "bf16", "bf16", 6, 1, 64, 64, 16, True),
+    ("few keys", "bf16", "mxfp8", 2, 2, 128, 96, 16, True),
+    ("few keys", "bf16", "bf16", 2, 1, 40, 24, 16, False),
+    ("few keys", "f32", "f32", 4, 4, 64, 128, 16, True),
+    ("few keys", "f32", "mxfp8", 5, 1, 32, 64, 16, False),
     ("many groups", "bf16", "bf16", 8, 2, 64, 64, 16, True),
     ("many groups", "f32", "f32", 2, 1, 32, 32, 16, True),
 ]
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("case", CASES, ids=["%s-%s-%s-%d-%d-D%d-%d-p%d-%d" % c for c in CASES])
-def test_attention(case):
+def test_attention(case, wide):
     kind, dtype, cache, hq, hk, dqk, dv, page, causal = case
-    b = Shared(*shape(kind), hk, dqk, dv, page, cache, dtype)
+    b = Shared(*shape(kind), hk, dqk, dv, page, cache, dtype, wide=wide)
     ws = space(b, hq)
     q, o, lse = check(b, hq, causal, ws=ws)
     assert jfa.jfa_status_check(ws) == jfa.JFA_OK
@@ -183,11 +198,11 @@ def spoiled(t, at, value):
     return t
 
 
-@pytest.mark.parametrize("big", [False, True])
-def test_errors_found_on_the_device(big):
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("n", [3, 300, 600])
+def test_errors_found_on_the_device(n, wide):
     """Invalid groups, prefixes and sequences leave the outputs alone; bad pages read as zeros."""
-    n = 300 if big else 3
-    b = Shared([n, n], [100, 200], [1] * 2 * n, [5] * 2 * n, 2, 64, 64, 16, "bf16", "bf16")
+    b = Shared([n, n], [100, 200], [1] * 2 * n, [5] * 2 * n, 2, 64, 64, 16, "bf16", "bf16", wide=wide)
     q, ws = queries(b, 4), space(b, 4)
     good = (b.own[1], b.own[2], b.own[3], b.prefix_table, b.prefix_lens, b.groups)
     o, lse = torch.full((b.T, 4, 64), 7.0, device="cuda").bfloat16(), torch.full((b.T, 4), 7.0, device="cuda")
