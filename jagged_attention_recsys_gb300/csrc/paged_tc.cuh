@@ -392,12 +392,14 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
           ok = mbar_wait(bar(B_VTAIL + st), (phase >> st) & 1, abort, status);
           if (!ok) break;
           phase ^= 1u << st;
-          const int nk = WIN ? 0 : g.seq.lk - k0;
-          for (int c = lane; c < (kKeys - nk) * (DV / 8); c += 32) {
-            const int row = nk + c / (DV / 8), ch = c % (DV / 8);
-            if (WIN && k0 + row < g.seq.lk && paged_sees(p, g.span.low, k0 + row)) continue;
-            st_shared_v4(tile + (ch >> 3) * 16384 + row * 128 + (ch & 7) * 16, 0u, 0u, 0u, 0u);
-          }
+          auto clean = [&](int r0, int r1) {
+            for (int c = r0 * (DV / 8) + lane; c < r1 * (DV / 8); c += 32) {
+              const int row = c / (DV / 8), ch = c % (DV / 8);
+              st_shared_v4(tile + (ch >> 3) * 16384 + row * 128 + (ch & 7) * 16, 0u, 0u, 0u, 0u);
+            }
+          };
+          if constexpr (WIN) clean(max(p.sinks - k0, 0), min(g.span.low - k0, kKeys));
+          clean(max(g.seq.lk - k0, 0), kKeys);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_FULL + st));
@@ -446,7 +448,11 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
           const int from = max(limit - p.window, 0) - k0, front = p.sinks - k0;
           if (seen < kKeys || (from > 0 && front < kKeys)) {
 #pragma unroll
-            for (int k = 0; k < kKeys; ++k) sv[k] = k < seen && (k >= from || k < front) ? sv[k] : -INFINITY;
+            for (int c = 0; c < kKeys; c += 32) {
+              const uint32_t bits = window_bits(c, from, front, seen);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : -INFINITY;
+            }
           }
         } else if (seen < kKeys) {
 #pragma unroll

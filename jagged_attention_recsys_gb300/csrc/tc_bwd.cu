@@ -713,7 +713,16 @@ tc_dkdv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         int hi = j < Lk ? Lq - i0 : 0;
         if (p.block_mask > 0 && (j ^ i0) >= p.block_mask) hi = 0;  // another block's queries
         if (WIN && j >= p.sinks) hi = min(hi, j - i0 + p.window);
-        if (lo > 0 || hi < HC) {
+        if (WIN) {
+          if (lo > 0 || hi < HC) {
+#pragma unroll
+            for (int c = 0; c < HC; c += 32) {
+              const uint32_t bits = window_bits(c, lo, 0, hi);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : sv[c + k] - shift_raw;
+            }
+          }
+        } else if (lo > 0 || hi < HC) {
 #pragma unroll
           for (int c = 0; c < HC; ++c) sv[c] -= (c >= lo && c < hi) ? 0.f : shift_raw;
         }
@@ -1333,7 +1342,11 @@ tc_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
           const int from = max(i - p.window + 1, 0) - kb, front = p.sinks - kb;
           if (nvalid < HC || (from > 0 && front < HC)) {
 #pragma unroll
-            for (int c = 0; c < HC; ++c) sv[c] -= c < nvalid && (c >= from || c < front) ? 0.f : shift_raw;
+            for (int c = 0; c < HC; c += 32) {
+              const uint32_t bits = window_bits(c, from, front, nvalid);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : sv[c + k] - shift_raw;
+            }
           }
         } else if (nvalid < HC) {
 #pragma unroll

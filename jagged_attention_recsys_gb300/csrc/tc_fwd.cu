@@ -456,7 +456,11 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           const int from = max(i - p.window + 1, 0) - kb, front = p.sinks - kb;
           if (nvalid < HC || (from > 0 && front < HC)) {
 #pragma unroll
-            for (int c = 0; c < HC; ++c) sv[c] -= c < nvalid && (c >= from || c < front) ? 0.f : shift_raw;
+            for (int c = 0; c < HC; c += 32) {
+              const uint32_t bits = window_bits(c, from, front, nvalid);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : sv[c + k] - shift_raw;
+            }
           }
         } else if (nvalid < HC) {
 #pragma unroll

@@ -288,6 +288,15 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
+// The lowest n bits, n <= 0: none, n >= 32: all.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+}
+// Of the columns [c, c + 32): those in front of `end` that are behind `from` or in front of `front`, a
+// bit each.  A window's mask by bits takes one instruction a score where comparisons take four.
+__device__ __forceinline__ uint32_t window_bits(int c, int from, int front, int end) {
+  return low_bits(end - c) & (~low_bits(from - c) | low_bits(front - c));
+}
 // max(a, b, c) in one instruction
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
