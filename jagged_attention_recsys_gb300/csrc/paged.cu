@@ -256,10 +256,11 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
 
 // --------------------------------------------------------------------------- the join
 // A warp a row: the parts of a split tile, rescaled to their common maximum and added in CTA
-// order.  CTA x of the grid serves the tile whose parts begin with CTA x's last one.  A row a warp, with
-// the parts' places and statistics a lane each and four parts' rows on their way: 16 tiles of 256 rows in
-// ten parts each take JOIN_NEW us, where eight rows a warp and one part after the other took 60.
-constexpr int kJoinWarps = 4;
+// order.  CTA x of the grid serves the tile whose parts begin with CTA x's last one.  Bound: latency, of
+// the look-ups first; places and statistics of 32 parts are a lane's each, two rows of a warp and four
+// parts of each are on their way at once.  16 tiles of 256 rows in some ten parts each: 10 us, where eight
+// rows a warp and one part after the other took 60; 152 tiles in two parts each, 25 us.
+constexpr int kJoinWarps = 4, kJoinTall = 32;  // warps of a CTA, most CTAs of a tile
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinWarps * 32)
@@ -287,64 +288,74 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
     }
     last += 32;
   }
-  auto empty = [&](int i) {  // a CTA without work inside the tile
+  auto has_part = [&](int i) {  // not a CTA without work inside the tile
+    if (i > last) return false;
     const PagedPos a = paged_pos(p, t, w, i), e = paged_pos(p, t, w, i + 1);
-    return i != c && cut.same(e) && a.blk >= e.blk;
+    return i == c || !(cut.same(e) && a.blk >= e.blk);
   };
-  for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < t.rows; r += gridDim.y * kJoinWarps) {
-    int tok, head;
-    if (!cut.row(p, t, r, tok, head)) continue;
-    auto slot_row = [&](int i) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * t.rows + r; };
-    // this lane's parts: statistics of the first 32, whose rows' loads then need not wait for them
-    float m = -INFINITY, m0 = -INFINITY, l0 = 0.f;
-    for (int i = c + lane; i <= last; i += 32) {
-      if (empty(i)) continue;
-      const float2 x = *reinterpret_cast<const float2*>(w.part_ml + 2 * slot_row(i));
-      m = fmaxf(m, x.x);
-      if (i == c + lane) {
-        m0 = x.x;
-        l0 = x.y;
-      }
+  const bool mine = has_part(c + lane);  // of the first 32
+  const unsigned parts = __ballot_sync(0xffffffffu, mine);
+  // two rows of a warp at once, four columns a lane
+  constexpr int R = 2, U = 4;  // U: parts whose rows are on their way
+  const int step = gridDim.y * kJoinWarps, c4 = 4 * lane;
+  const bool in_v = c4 < p.dim_v;
+  for (int r0 = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r0 < t.rows; r0 += R * step) {
+    int64_t orow[R];
+    float4 x[R][U], acc[R];
+    float2 first[R];
+    auto slot_row = [&](int q, int i) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * t.rows + r0 + q * step; };
+    auto stats = [&](int q, bool has, int i) {
+      return has ? *reinterpret_cast<const float2*>(w.part_ml + 2 * slot_row(q, i)) : make_float2(-INFINITY, 0.f);
+    };
+    auto load = [&](int q, unsigned on, int i0, int i) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        x[q][u] = (on >> (i + u)) & 1 && in_v && orow[q] >= 0
+                      ? *reinterpret_cast<const float4*>(w.part_o + slot_row(q, i0 + i + u) * p.dim_v + c4)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      int tok, head;
+      const bool ok = r0 + q * step < t.rows && cut.row(p, t, r0 + q * step, tok, head);
+      orow[q] = ok ? (int64_t)(seq.q0 + tok) * p.heads_q + head : -1;
+      first[q] = stats(q, mine && ok, c + lane);
+      load(q, parts, c, 0);  // with the statistics, not behind them
     }
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};  // columns lane + 32 i
-    for (int i0 = c; i0 <= last; i0 += 32) {
-      float mi = m0, li = l0;
-      if (i0 > c) {
-        const bool has = i0 + lane <= last && !empty(i0 + lane);
-        const float2 x = has ? *reinterpret_cast<const float2*>(w.part_ml + 2 * slot_row(i0 + lane)) : make_float2(-INFINITY, 0.f);
-        mi = x.x;
-        li = x.y;
-      }
-      const float fi = exp2f(mi - ref);
-      // a part without keys has no output (nor has an empty CTA): its maximum says so
-      const unsigned full = __ballot_sync(0xffffffffu, mi != -INFINITY);
-      constexpr int U = 4;  // parts whose rows are on their way
-      for (int i = 0; i < 32 && i0 + i <= last; i += U) {
-        float x[U][4];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+    for (int q = 0; q < R; ++q) {
+      if (orow[q] < 0) continue;
+      float m = first[q].x;
+      for (int i = c + 32 + lane; i <= last; i += 32) m = fmaxf(m, stats(q, has_part(i), i).x);
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float ref = m == -INFINITY ? 0.f : m;
+      float l = 0.f;
+      acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = c; i0 <= last; i0 += 32) {
+        const float2 st = i0 == c ? first[q] : stats(q, has_part(i0 + lane), i0 + lane);
+        const float fi = exp2f(st.x - ref);
+        // a part without keys has no output: its maximum says so
+        const unsigned full = __ballot_sync(0xffffffffu, st.x != -INFINITY);
+        for (int i = 0; i < 32 && i0 + i <= last; i += U) {
+          if (i0 > c || i > 0) load(q, full, i0, i);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            x[u][k] = (full >> (i + u)) & 1 && lane + 32 * k < p.dim_v
-                          ? w.part_o[slot_row(i0 + i + u) * p.dim_v + lane + 32 * k] : 0.f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float f = __shfl_sync(0xffffffffu, fi, i + u);
-          l = fmaf(__shfl_sync(0xffffffffu, li, i + u), f, l);
-          if (!((full >> (i + u)) & 1)) continue;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[k] = fmaf(x[u][k], f, acc[k]);
+          for (int u = 0; u < U; ++u) {
+            const float f = __shfl_sync(0xffffffffu, fi, i + u);
+            l = fmaf(__shfl_sync(0xffffffffu, st.y, i + u), f, l);
+            if (!((full >> (i + u)) & 1)) continue;
+            acc[q] = make_float4(fmaf(x[q][u].x, f, acc[q].x), fmaf(x[q][u].y, f, acc[q].y), fmaf(x[q][u].z, f, acc[q].z),
+                                 fmaf(x[q][u].w, f, acc[q].w));
+          }
         }
       }
-    }
-    const int64_t orow = (int64_t)(seq.q0 + tok) * p.heads_q + head;
-    RowEnd<T> end(p, orow, m, l);
+      RowEnd<T> end(p, orow[q], m, l);
+      if (in_v) {
+        const float y[4] = {acc[q].x, acc[q].y, acc[q].z, acc[q].w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (lane + 32 * k < p.dim_v) end.put(p, orow * p.dim_v + lane + 32 * k, acc[k]);
-    if (lane == 0) end.finish(p, orow);
+        for (int k = 0; k < 4; ++k) end.put(p, orow[q] * p.dim_v + c4 + k, y[k]);
+      }
+      if (lane == 0) end.finish(p, orow[q]);
+    }
   }
 }
 
@@ -465,7 +476,8 @@ cudaError_t launch_paged_simt(const Paged& p, const TileShape& t, int ctas, int 
 
 cudaError_t launch_paged_combine(const Paged& p, const TileShape& t, int ctas, int dtype, const PagedWs& w,
                                  cudaStream_t s) {
-  const int gy = (t.rows + kJoinWarps - 1) / kJoinWarps;  // a row a warp
+  int gy = (t.rows + kJoinWarps - 1) / kJoinWarps;
+  if (gy > kJoinTall) gy = kJoinTall;
   if (dtype == JFA_BF16)
     paged_join_kernel<__nv_bfloat16><<<dim3(ctas, gy), kJoinWarps * 32, 0, s>>>(p, t, ctas, w);
   else

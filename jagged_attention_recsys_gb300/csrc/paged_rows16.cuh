@@ -676,6 +676,24 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
       if (lane == 0) mbar_arrive(empty + 8 * st);
     }
 
+    // the rows that this thread adds up at the end
+    constexpr int CW = L::R / 4, PER = 32 / CW;  // columns a thread adds up in a round, threads of a row
+    const int tid = threadIdx.x, jr = tid / PER, jc = tid % PER * CW;
+    const int tok = g.tile * t.tokens + jr / t.gsub, gh = gs0 + jr % t.gsub;
+    const bool jrow_ok = jr < t.rows && tok < g.seq.lq && gh < p.group;
+    const int64_t out_row = (int64_t)(g.seq.q0 + tok) * p.heads_q + head_k * p.group + gh;
+    // a shared prefix: what phase 1 left of them is on its way through the rounds below
+    const bool joins = MODE == kShared && p.phase == 2 && g.slot < 0 && jrow_ok;
+    float2 prior[MODE == kShared ? DV / 32 : 1][CW / 2];
+    float prior_lse = 0.f;
+    if constexpr (MODE == kShared) {
+      if (joins) prior_lse = p.prior_lse[out_row];
+#pragma unroll
+      for (int rd = 0; rd < DV / 32; ++rd)
+#pragma unroll
+        for (int c = 0; c < CW / 2; ++c)
+          if (joins) prior[rd][c] = *reinterpret_cast<const float2*>(p.prior_o + out_row * DV + 32 * rd + jc + 2 * c);
+    }
     // ---- the warps' parts of the tile become one
     const uint32_t ml = sb + L::ML;
 #pragma unroll
@@ -718,18 +736,13 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
           o[nt][i][2 + e] = o[nt][i][2 + e] * a * f;
         }
       }
-    constexpr int CW = L::R / 4, PER = 32 / CW;  // columns a thread adds up in a round, threads of a row
-    const int tid = threadIdx.x, jr = tid / PER, jc = tid % PER * CW;
-    const int tok = g.tile * t.tokens + jr / t.gsub, gh = gs0 + jr % t.gsub;
-    const bool jrow_ok = jr < t.rows && tok < g.seq.lq && gh < p.group;
     float M, Ls;
     joined(jr, M, Ls);
-    const int64_t out_row = (int64_t)(g.seq.q0 + tok) * p.heads_q + head_k * p.group + gh;
     const int64_t part_row = ((int64_t)blockIdx.x * 2 + g.slot) * t.rows + jr;
     float inv = Ls > 0.f ? 1.f / Ls : (Ls == 0.f ? 0.f : Ls);
     PagedJoin join{};
-    if (MODE == kShared && p.phase == 2 && g.slot < 0 && jrow_ok) {
-      join = paged_join_prior(M, Ls, p.prior_lse[out_row]);
+    if (joins) {
+      join = paged_join_prior(M, Ls, prior_lse);
       inv = join.own;
     }
     const float* jb = (const float*)(smem_raw + (sb + L::JOIN - smem_u32(smem_raw)));
@@ -765,12 +778,12 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
           if (jr < t.rows)
             *reinterpret_cast<float2*>(w.part_o + part_row * DV + 32 * rd + jc + c) = make_float2(x[c], x[c + 1]);
         } else if (MODE == kShared && jrow_ok) {
-          float2* prior = reinterpret_cast<float2*>(p.prior_o + out_row * DV + 32 * rd + jc + c);
+          const int64_t at = out_row * DV + 32 * rd + jc + c;
           if (p.phase == 1) {
-            *prior = make_float2(x[c] * inv, x[c + 1] * inv);
+            *reinterpret_cast<float2*>(p.prior_o + at) = make_float2(x[c] * inv, x[c + 1] * inv);
           } else {
-            const float2 y = *prior;
-            *reinterpret_cast<uint32_t*>((__nv_bfloat16*)p.o + out_row * DV + 32 * rd + jc + c) =
+            const float2 y = prior[rd][c / 2];
+            *reinterpret_cast<uint32_t*>((__nv_bfloat16*)p.o + at) =
                 pack_bf16(fmaf(y.x, join.prior, x[c] * inv), fmaf(y.y, join.prior, x[c + 1] * inv));
           }
         } else if (jrow_ok) {

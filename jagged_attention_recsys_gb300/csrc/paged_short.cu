@@ -21,7 +21,9 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kScan = 4 * kThreads;  // sequences that a CTA checks by itself
-constexpr int H = 4, K = 4;          // query heads and keys at a time
+// Query heads and keys at a time, and CTAs an SM, for the figure above: four keys at a time in three
+// CTAs 53 us, in four 49; two keys in five 50; one key in six 56.
+constexpr int H = 4, K = 2, kCtas = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float4 four(const __nv_bfloat16* x) {
@@ -68,7 +70,7 @@ paged_short_check_kernel(const __grid_constant__ Paged p, PagedHeader* hdr) {
 }
 
 template <typename T, int KIND>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas)
 paged_short_kernel(const __grid_constant__ Paged p, PagedHeader* hdr) {
   if (p.batch <= kScan) {
     bool bad = *(volatile int*)&hdr->status == (int)JFA_ERR_BAD_OFFSETS;
@@ -95,16 +97,11 @@ paged_short_kernel(const __grid_constant__ Paged p, PagedHeader* hdr) {
     const int rest = (int)(task % (p.heads_k * parts)), head_k = rest / parts;
     const int h0 = head_k * p.group + rest % parts * H, hn = min(H, p.group - rest % parts * H);
     const int64_t row0 = t * p.heads_q + h0;
-    // phase 1's share of the rows, for the end
-    float4 prior[H];
-    float prior_lse[H];
     float4 q[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       const bool on = h < hn;
       q[h] = on && in_k ? four((const T*)p.q + t * p.sq + (int64_t)(h0 + h) * p.dim_qk + c) : zero;
-      prior[h] = on && in_v ? *reinterpret_cast<const float4*>(p.prior_o + (row0 + h) * p.dim_v + c) : zero;
-      prior_lse[h] = on ? p.prior_lse[row0 + h] : 0.f;
     }
     const int b = find_sequence(p, t);
     const int64_t len = __ldg(p.lens + b), pos = len - (__ldg(p.offs + b + 1) - t);
@@ -165,6 +162,15 @@ paged_short_kernel(const __grid_constant__ Paged p, PagedHeader* hdr) {
           }
         }
       }
+    }
+    // phase 1's share of the rows; asked for ahead of the keys it would cost registers and so warps (51 us)
+    float4 prior[H];
+    float prior_lse[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const bool on = h < hn;
+      prior[h] = on && in_v ? *reinterpret_cast<const float4*>(p.prior_o + (row0 + h) * p.dim_v + c) : zero;
+      prior_lse[h] = on ? p.prior_lse[row0 + h] : 0.f;
     }
 #pragma unroll
     for (int h = 0; h < H; ++h) {
