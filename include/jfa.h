@@ -169,7 +169,8 @@ jfa_status jfa_bwd(const jfa_params* p, const void* q, const void* k, const void
  * that a sequence's grows with its length and not with its square.  Every row sees its own key.
  * jfa_window_plan builds the lists of both calls for one window and its sinks (JFA_PLANNED, as by
  * jfa_plan; a plan of another window or of jfa_plan gives wrong results, within the buffers' bounds).
- * Values of keys that a row's window hides have to be finite and at most 2^120 in size.
+ * Values of keys that a row's window hides have to be finite and at most 2^120 in size; their scores
+ * count for nothing, whatever they are.
  */
 jfa_status jfa_window_plan(const jfa_params* p, int32_t window, int32_t sinks, const int64_t* offs,
                            void* ws, size_t ws_bytes, jfa_stream_t stream);
@@ -583,7 +584,7 @@ enum {
   JFA_KERNEL_BWD_DQ = 4,   /* query-tile-major dQ pass */
   JFA_KERNEL_AUX = 5,      /* pooled query broadcast and gradient sum; block offsets */
   JFA_KERNEL_NORM_ROPE = 6, /* norms with rotary positions (backward: with its weight sums) */
-  JFA_KERNEL_CACHE = 7,     /* paged cache written or read */
+  JFA_KERNEL_CACHE = 7,     /* paged cache written (with or without norm and rotation) or read */
   JFA_KERNEL_PAGED = 8,     /* attention over a paged cache, with the join of split tiles */
   JFA_KERNEL_KINDS = 9
 };
@@ -598,10 +599,10 @@ jfa_status jfa_profile_read(int kind, int64_t* launches, double* total_ms);
  * leave, waits for the CTA's own copies and MMAs in flight and frees its
  * tensor memory, so the context stays usable.  While `on` is nonzero, every
  * bf16 forward launch in the calling thread's current context (jfa_fwd,
- * jfa_cross_fwd, jfa_gdpa_fwd and the calls built on them) starts with its MMA
+ * jfa_cross_fwd, jfa_gdpa_fwd, jfa_window_fwd and the calls built on them) starts with its MMA
  * issuer waiting on a barrier that nothing arrives on, before any MMA is
- * issued; in the tensor-core kernels of jfa_paged_fwd one role of the first CTA
- * waits in the same way (a consumer warp of the few-row kernel, an MMA issuer of
+ * issued; in the tensor-core kernels of jfa_paged_fwd, jfa_paged_window_fwd and
+ * jfa_shared_fwd one role of the first CTA waits in the same way (a consumer warp of the few-row kernel, an MMA issuer of
  * the other) while its copies are in flight, in launches of the whole process.
  * The call then reports JFA_ERR_TIMEOUT through jfa_status_check and leaves its
  * outputs incomplete.  Off by default; turn it off again before

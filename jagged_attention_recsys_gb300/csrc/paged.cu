@@ -385,9 +385,13 @@ int paged_kernel(const Paged& p, int dtype) {
   // to tcgen05's 128-row tiles (groups larger than one would split them).  Measured, 64 users of
   // 2048 keys, 8 key heads of 128, us, few-row kernel against tcgen05: bf16 pages 16 rows 115 to
   // 121, 24 rows 195 to 121; MXFP8, where tcgen05 waits for the tiles in bf16, 16 rows 84 to 156,
-  // 32 rows 141 to 162, 48 rows 191 to 164.
+  // 32 rows 141 to 162, 48 rows 191 to 164.  Under a window of 256 keys tcgen05's long tiles weigh more:
+  // bf16 24 rows 68 to 86, 32 rows 72 to 86, 48 rows 84 to 86 (MXFP8 32 rows 82 to 94, 48 rows 98 to 96);
+  // of 1,024 keys as without one: bf16 16 rows 94 to 117, 24 rows 130 to 117 (MXFP8 32 rows 133 to 139,
+  // 48 rows 170 to 141).
   const int64_t rows_per_seq = p.total_q * p.group / p.batch;
-  return rows_per_seq <= (p.kind == kCacheMx ? 32 : 16) || p.group > 128 ? kPagedRows16 : kPagedTc;
+  const bool short_window = p.window > 0 && p.window <= 256;
+  return rows_per_seq <= (p.kind == kCacheMx || short_window ? 32 : 16) || p.group > 128 ? kPagedRows16 : kPagedTc;
 }
 
 TileShape paged_shape(const Paged& p, int kernel) {

@@ -26,6 +26,8 @@ __device__ __forceinline__ PagedBounds paged_bounds(const Paged& p, int64_t b) {
   if (s < 0 || n < s || n > p.seqs || (b == 0 && s != 0) || (b == p.batch - 1 && n != p.seqs)) return PagedBounds{-1, -1};
   return PagedBounds{__ldg(p.offs + s), __ldg(p.offs + n)};
 }
+// Whether a sequence of so many own keys is the short kernel's.
+__device__ __forceinline__ bool is_few(const Paged& p, int64_t keys) { return p.few > 0 && keys <= p.few; }
 __device__ __forceinline__ PagedSeq paged_seq(const Paged& p, const TileShape& t, int b) {
   PagedSeq s;
   const PagedBounds n = paged_bounds(p, b);
@@ -33,7 +35,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const Paged& p, const TileShape& t
   // (what a plan was not made for and is no batch either has no tokens)
   const bool ok = a >= 0 && e >= a && e <= p.total_q && l >= 0 && l <= ((int64_t)p.width << p.page_shift);
   s.q0 = (int)a;
-  s.lq = ok ? (int)(e - a) : 0;
+  s.lq = ok && !is_few(p, l) ? (int)(e - a) : 0;
   s.lk = (int)l;
   s.off = l - (e - a);
   s.tiles = (s.lq + t.tokens - 1) / t.tokens;
@@ -109,6 +111,7 @@ __device__ __forceinline__ int64_t checked_cost(const Paged& p, const TileShape&
   if (a < 0 || e < a || e > p.total_q || lk < 0 || lk > ((int64_t)p.width << p.page_shift) || (b == 0 && a != 0) ||
       (b == p.batch - 1 && e != p.total_q))
     return -1;
+  if (is_few(p, lk)) return 0;
   return (int64_t)p.heads_k * t.nsub * seq_cost(p, t, e - a, lk).total();
 }
 

@@ -4,9 +4,17 @@
 // Bound: latency.  The tiled kernels take 7 us a tile here, of which the keys are nothing: the walk's
 // look-ups, the loads' round trip through the ring and the join of four warps, one after the other (16
 // users' 64 candidates of 1 to 4 tokens, 8,192 tiles: 191 us).  So a warp takes a token and a key head by
-// itself, four query heads at a time: a lane has four columns, keys are looked up 32 at a time and
-// loaded four at once, a score is the warp's sum.  fp32 throughout.  What phase 1 left of the rows is
-// asked for first and used last.
+// itself, four query heads at a time.  For the scores two lanes have a key, half of its columns each,
+// against queries in shared memory; for the output a lane has four columns of every key.  fp32
+// throughout.  Those candidates take 50 us.  (A score as the warp's sum, two keys at a time: 44 us, but
+// 27 where a few sequences of 16 keys are among 128 of more, which this takes 16 for.)
+//
+// The lengths are on the device, so that the tiled kernels are launched too unless the pages decide
+// it, and pass over these sequences as this kernel does over the others (12 us where none has few keys).
+// 16 groups of 64 sequences of two tokens each, 32 heads on 8, prefixes of 256 keys, the whole call
+// against the tiled kernels alone, us: bf16 2 own keys 124 to 156, 16 keys 165 to 156; MXFP8 129 to 185 and 191
+// to 185.  Groups of 8 of one token: 66 to 74, 68 to 72; MXFP8 64 to 79, 74 to 80.  With more than 16 tokens
+// a sequence on average hardly one has so few keys, and the tiled kernels take all.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -21,9 +29,9 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kScan = 4 * kThreads;  // sequences that a CTA checks by itself
-// Query heads and keys at a time, and CTAs an SM, for the figure above: four keys at a time in three
-// CTAs 53 us, in four 49; two keys in five 50; one key in six 56.
-constexpr int H = 4, K = 2, kCtas = 4;
+constexpr int H = 4, K = 4;  // query heads, and values, at a time
+constexpr int kFew = 16;     // own keys: half a warp's lanes
+constexpr int kMaxDim = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float4 four(const __nv_bfloat16* x) {
@@ -48,8 +56,8 @@ __device__ __forceinline__ float4 cached(const void* values, const uint8_t* scal
   const float2 a = e4m3_values(w & 0xffffu), b = e4m3_values(w >> 16);
   return make_float4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
-__device__ __forceinline__ float dot4(const float4& a, const float4& b) {
-  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, a.w * b.w)));
+__device__ __forceinline__ void add4(float4& s, float k, const float4& q) {
+  s = make_float4(fmaf(k, q.x, s.x), fmaf(k, q.y, s.y), fmaf(k, q.z, s.z), fmaf(k, q.w, s.w));
 }
 
 // A batch that is none becomes the call's status, unless a wait of phase 1 ran out.
@@ -70,7 +78,7 @@ paged_short_check_kernel(const __grid_constant__ Paged p, PagedHeader* hdr) {
 }
 
 template <typename T, int KIND>
-__global__ void __launch_bounds__(kThreads, kCtas)
+__global__ void __launch_bounds__(kThreads, 4)
 paged_short_kernel(const __grid_constant__ Paged p, PagedHeader* hdr) {
   if (p.batch <= kScan) {
     bool bad = *(volatile int*)&hdr->status == (int)JFA_ERR_BAD_OFFSETS;
@@ -86,10 +94,14 @@ paged_short_kernel(const __grid_constant__ Paged p, PagedHeader* hdr) {
   } else if (*(volatile int*)&hdr->status == (int)JFA_ERR_BAD_OFFSETS) {
     return;  // phase 1 or the check in front found it
   }
+  // the queries' four heads of a column side by side, so that a lane reads them at once
+  __shared__ float4 queries[kWarps][kMaxDim];
+  float4* qs = queries[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31, c = 4 * lane;
-  const bool in_k = c < p.dim_qk, in_v = c < p.dim_v;
+  const bool in_v = c < p.dim_v;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   const float to_log2 = p.scale * kLog2e;
+  const int key = lane & (kFew - 1), half = p.dim_qk / 2, c0 = lane / kFew * half;
   const int parts = (p.group + H - 1) / H;  // of a key head's query heads
   const int64_t tasks = p.total_q * p.heads_k * parts, nw = (int64_t)gridDim.x * kWarps;
   for (int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); task < tasks; task += nw) {
@@ -97,71 +109,68 @@ paged_short_kernel(const __grid_constant__ Paged p, PagedHeader* hdr) {
     const int rest = (int)(task % (p.heads_k * parts)), head_k = rest / parts;
     const int h0 = head_k * p.group + rest % parts * H, hn = min(H, p.group - rest % parts * H);
     const int64_t row0 = t * p.heads_q + h0;
-    float4 q[H];
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const bool on = h < hn;
-      q[h] = on && in_k ? four((const T*)p.q + t * p.sq + (int64_t)(h0 + h) * p.dim_qk + c) : zero;
-    }
     const int b = find_sequence(p, t);
     const int64_t len = __ldg(p.lens + b), pos = len - (__ldg(p.offs + b + 1) - t);
+    if (len > p.few) continue;  // the tiled kernels'
     const int n = (int)max((int64_t)0, p.causal ? min(len, pos + 1) : len);  // keys the rows see
-    float m[H], l[H];
+    int64_t mine = -1;  // the row of this lane's key
+    if (key < n) {
+      const int page = paged_page(p, b, key, &hdr->status);
+      if (page >= 0) mine = paged_row(p, page, head_k, key);
+    }
+    float4 q[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      q[h] = h < hn && c < p.dim_qk ? four((const T*)p.q + t * p.sq + (int64_t)(h0 + h) * p.dim_qk + c) : zero;
+    __syncwarp();  // the last row's have been read
+    if (c < p.dim_qk) {
+      qs[c] = make_float4(q[0].x, q[1].x, q[2].x, q[3].x);
+      qs[c + 1] = make_float4(q[0].y, q[1].y, q[2].y, q[3].y);
+      qs[c + 2] = make_float4(q[0].z, q[1].z, q[2].z, q[3].z);
+      qs[c + 3] = make_float4(q[0].w, q[1].w, q[2].w, q[3].w);
+    }
+    __syncwarp();
+    // scores of this lane's key, over its half of the columns
+    float4 s4 = zero;
+    if (mine >= 0) {
+#pragma unroll 8
+      for (int i = 0; i < half; i += 4) {
+        const float4 k = cached<KIND>(p.kc, p.ks, mine, p.dim_qk, c0 + i);
+        add4(s4, k.x, qs[c0 + i]);
+        add4(s4, k.y, qs[c0 + i + 1]);
+        add4(s4, k.z, qs[c0 + i + 2]);
+        add4(s4, k.w, qs[c0 + i + 3]);
+      }
+    }
+    float s[H] = {s4.x, s4.y, s4.z, s4.w}, m[H], l[H];
     float4 o[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      m[h] = -INFINITY;
-      l[h] = 0.f;
+      s[h] += __shfl_xor_sync(0xffffffffu, s[h], kFew);
+      s[h] = key < n ? s[h] * to_log2 : -INFINITY;  // behind a bad page: a key of zeros
+      m[h] = s[h];
+#pragma unroll
+      for (int x = kFew / 2; x > 0; x >>= 1) m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], x));
+      s[h] = exp2f(s[h] - (m[h] == -INFINITY ? 0.f : m[h]));
+      l[h] = s[h];
+#pragma unroll
+      for (int x = kFew / 2; x > 0; x >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
       o[h] = zero;
     }
-    for (int j0 = 0; j0 < n; j0 += 32) {
-      int64_t mine = -1;  // this lane's key
-      if (j0 + lane < n) {
-        const int page = paged_page(p, b, j0 + lane, &hdr->status);
-        if (page >= 0) mine = paged_row(p, page, head_k, j0 + lane);
+    for (int i = 0; i < n; i += K) {
+      float4 v[K];
+#pragma unroll
+      for (int u = 0; u < K; ++u) {
+        const int64_t row = __shfl_sync(0xffffffffu, mine, (i + u) & (kFew - 1));
+        v[u] = i + u < n && row >= 0 && in_v ? cached<KIND>(p.vc, p.vs, row, p.dim_v, c) : zero;
       }
-      const int most = min(32, n - j0);
-      for (int i = 0; i < most; i += K) {
-        float4 k[K], v[K];
 #pragma unroll
-        for (int u = 0; u < K; ++u) {
-          const int64_t row = __shfl_sync(0xffffffffu, mine, (i + u) & 31);
-          const bool there = i + u < most && row >= 0;  // behind a bad page: zeros
-          k[u] = there && in_k ? cached<KIND>(p.kc, p.ks, row, p.dim_qk, c) : zero;
-          v[u] = there && in_v ? cached<KIND>(p.vc, p.vs, row, p.dim_v, c) : zero;
-        }
-        float s[H][K];
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-          for (int u = 0; u < K; ++u) s[h][u] = dot4(q[h], k[u]);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1)
-#pragma unroll
-          for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int u = 0; u < K; ++u) s[h][u] += __shfl_xor_sync(0xffffffffu, s[h][u], x);
+      for (int u = 0; u < K; ++u)
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-          float top = m[h];
-#pragma unroll
-          for (int u = 0; u < K; ++u) {
-            s[h][u] = i + u < most ? s[h][u] * to_log2 : -INFINITY;
-            top = fmaxf(top, s[h][u]);
-          }
-          const float ref = top == -INFINITY ? 0.f : top, a = exp2f(m[h] - ref);
-          m[h] = top;
-          l[h] *= a;
-          o[h] = make_float4(o[h].x * a, o[h].y * a, o[h].z * a, o[h].w * a);
-#pragma unroll
-          for (int u = 0; u < K; ++u) {
-            const float e = exp2f(s[h][u] - ref);
-            l[h] += e;
-            o[h] = make_float4(fmaf(e, v[u].x, o[h].x), fmaf(e, v[u].y, o[h].y), fmaf(e, v[u].z, o[h].z),
-                               fmaf(e, v[u].w, o[h].w));
-          }
+          const float e = __shfl_sync(0xffffffffu, s[h], (i + u) & (kFew - 1));
+          o[h] = make_float4(fmaf(e, v[u].x, o[h].x), fmaf(e, v[u].y, o[h].y), fmaf(e, v[u].z, o[h].z), fmaf(e, v[u].w, o[h].w));
         }
-      }
     }
     // phase 1's share of the rows; asked for ahead of the keys it would cost registers and so warps (51 us)
     float4 prior[H];
@@ -196,7 +205,8 @@ cudaError_t short_t(const Paged& p, PagedHeader* hdr, cudaStream_t s) {
 
 }  // namespace
 
-bool paged_short(const Paged& p) { return ((int64_t)p.width << p.page_shift) <= kShortKeys; }
+int paged_few(const Paged& p) { return p.total_q <= kFew * p.batch ? kFew : 0; }
+bool paged_short(const Paged& p) { return paged_few(p) > 0 && ((int64_t)p.width << p.page_shift) <= kFew; }
 
 cudaError_t launch_paged_short(const Paged& p, int dtype, PagedHeader* hdr, cudaStream_t s) {
   if (p.batch > kScan || p.total_q == 0) {

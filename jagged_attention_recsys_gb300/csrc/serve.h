@@ -73,6 +73,7 @@ struct Paged {
   int64_t seqs;
   float *prior_o, *prior_lse;  // [T, heads_q, dim_v], [T, heads_q]
   const int* prior_status;     // phase 2: how phase 1 ended
+  int few;                     // phase 2: sequences of at most so many own keys are the short kernel's
 };
 
 // Where a CTA's share of the attention begins: block `blk` of keys of tile `tile` of unit
@@ -127,7 +128,7 @@ int paged_ctas(const Paged& p, int kernel);
 size_t paged_layout(const Paged& p, void* base, PagedWs* out);
 // The workspace of attention over a shared prefix: phase 2's, then phase 1's header and plan (its
 // parts lie in phase 2's place, which begins behind it) and its results.  Where phase 2 is the short
-// kernel's, both have the first header.
+// kernel's alone, both have the first header.
 size_t shared_layout(const Paged& prefix, const Paged& own, void* base, PagedWs* first, PagedWs* second, float** prior_o,
                      float** prior_lse);
 
@@ -151,9 +152,10 @@ cudaError_t launch_paged_rows16_shared(const Paged& p, const TileShape& t, int c
 cudaError_t launch_paged_tc(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
 cudaError_t launch_paged_tc_window(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
 cudaError_t launch_paged_tc_shared(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
-// Phase 2 of a shared prefix where the pages of a sequence have room for few keys.  hdr: phase 1's header,
-// whose status it goes on with.
-constexpr int kShortKeys = 128;
+// Phase 2 of a shared prefix for the sequences of at most p.few own keys; hdr is the call's header, whose
+// status it goes on with.  paged_few: p.few for a request, 0 where the tiled kernels take all; paged_short:
+// no sequence can have more.
+int paged_few(const Paged& p);
 bool paged_short(const Paged& p);
 cudaError_t launch_paged_short(const Paged& p, int dtype, PagedHeader* hdr, cudaStream_t s);
 cudaError_t launch_paged_combine(const Paged& p, const TileShape& t, int ctas, int dtype, const PagedWs& w,

@@ -508,11 +508,11 @@ jfa_status jfa_shared_fwd(const jfa_paged_params* p, int64_t groups, int32_t pre
   if ((st = groups > 0 ? run_paged(prefix, p->dtype, kShared, false, first, s)
                        : cu(cudaMemsetAsync(first.hdr, 0, sizeof(PagedHeader), s))) != JFA_OK)
     return st;
-  if (paged_short(own)) {
-    Timed t(JFA_KERNEL_PAGED, s);
-    return cu(launch_paged_short(own, p->dtype, second.hdr, s));
-  }
-  return run_paged(own, p->dtype, kShared, false, second, s);
+  own.few = paged_few(own);
+  if (!paged_short(own) && (st = run_paged(own, p->dtype, kShared, false, second, s)) != JFA_OK) return st;
+  if (own.few == 0) return JFA_OK;
+  Timed t(JFA_KERNEL_PAGED, s);
+  return cu(launch_paged_short(own, p->dtype, second.hdr, s));
 }
 
 }  // extern "C"

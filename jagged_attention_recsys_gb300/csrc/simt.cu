@@ -60,6 +60,9 @@ __device__ __forceinline__ bool in_window(const Problem& p, int i, int j) {
   return p.window == 0 || i - j < p.window || j < p.sinks;
 }
 
+// A hidden pair's score: under a window of the constant alone, so that none of any size counts.
+__device__ __forceinline__ float masked(const Problem& p, float s) { return (p.window > 0 ? 0.f : s) - kMaskShift; }
+
 template <typename T, int DQ, int DV>
 struct SimtFwdSmem {
   float q[kTileRows][DQ];
@@ -122,7 +125,7 @@ simt_fwd_kernel(Problem p, const T* __restrict__ q, const T* __restrict__ k,
 #pragma unroll 8
         for (int d = 0; d < DQ; ++d) s = fmaf(sm.q[r][d], sm.k[lane][d], s);
         const bool valid = j < Lk && (!p.causal || j <= i) && in_window(p, i, j);
-        s -= valid ? 0.f : kMaskShift;
+        s = valid ? s : masked(p, s);
         float pj;
         if (p.act == kActSoftmax) {
           const float mn = fmaxf(m[rr], warp_max(s));
@@ -249,7 +252,7 @@ simt_dq_kernel(Problem p, const T* __restrict__ q, const T* __restrict__ k,
 #pragma unroll 8
         for (int d = 0; d < DV; ++d) dp = fmaf(sm.dout[r][d], sm.v[lane][d], dp);
         const bool valid = i < Lq && j < Lk && (!p.causal || j <= i) && in_window(p, i, j);
-        s -= valid ? 0.f : kMaskShift;
+        s = valid ? s : masked(p, s);
         float ds;
         if (softmax) {
           const float pj = exp2f(s - lse2[rr]);
@@ -358,7 +361,7 @@ simt_dkdv_kernel(Problem p, const T* __restrict__ q, const T* __restrict__ k,
 #pragma unroll 8
         for (int d = 0; d < DV; ++d) dp = fmaf(sm.dout[lane][d], sm.v[r][d], dp);
         const bool valid = i < Lq && j < Lk && (!p.causal || j <= i) && in_window(p, i, j);
-        s -= valid ? 0.f : kMaskShift;
+        s = valid ? s : masked(p, s);
         float pi, ds;
         if (softmax) {
           pi = exp2f(s - sm.lse2[lane]);

@@ -452,14 +452,16 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (CAUSAL) nvalid = min(nvalid, i - kb + 1);
         if (p.block_mask > 0 && (kb ^ i) >= p.block_mask) nvalid = 0;  // another block's keys
         if (WIN) {
-          // the row's window, and the sinks
+          // the row's window, and the sinks.  A hidden score is replaced, so that none of any size counts.  A
+          // first block that the row sees nothing of leaves weights that the next rescaling, by
+          // exp2(-2^20) = 0, takes back: every row sees its own key, in the last block.
           const int from = max(i - p.window + 1, 0) - kb, front = p.sinks - kb;
           if (nvalid < HC || (from > 0 && front < HC)) {
 #pragma unroll
             for (int c = 0; c < HC; c += 32) {
               const uint32_t bits = window_bits(c, from, front, nvalid);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : sv[c + k] - shift_raw;
+              for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : -shift_raw;
             }
           }
         } else if (nvalid < HC) {

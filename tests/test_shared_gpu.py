@@ -21,10 +21,10 @@ class Shared(Batch):
         self.group_h = np.concatenate([[0], np.cumsum(groups)]).astype(np.int64)
         self.groups = torch.tensor(self.group_h, device="cuda")
         self.prefix_table, self.prefix_lens = self.table[self.S:].contiguous(), self.lens[self.S:].clone()
-        # a table of few pages takes the kernel for few keys, a wide one the tiled kernels
-        width = self.table.shape[1] if wide else max([-(-int(n) // page) for n in lens] + [0]) + 1
-        if wide and width * page <= 128:
-            width = 128 // page + 1
+        # a table of one page of 16 takes the kernel for few keys alone, a wider one the tiled kernels too
+        width = self.table.shape[1] if wide else max([-(-int(n) // page) for n in lens] + [1])
+        if wide and width * page <= 16:
+            width = 2
         own = torch.nn.functional.pad(self.table[:self.S], (0, max(0, width - self.table.shape[1])), value=-1)
         self.own = (self.cache, own[:, :width].contiguous(), self.offs[:self.S + 1].clone(), self.lens[:self.S].clone())
 
@@ -89,10 +89,15 @@ def shape(kind):
     if kind == "many":  # more than one CTA scans by itself: a launch of its own for the plan
         g = [40, 0, 660]
         return g, [100, 5, 333], [1] * 700, rng.integers(1, 30, 700).tolist()
-    if kind == "few keys":  # up to as many own keys as the kernel for few serves, and more sequences than a CTA checks
+    if kind in ("few keys", "few and more"):  # more sequences than a CTA checks
         g = [100, 1300, 3]
         new = rng.integers(0, 4, 1403)
-        return g, [70, 40, 200], new.tolist(), np.minimum(new + rng.integers(-1, 100, 1403), 112).clip(0).tolist()
+        most = 16 if kind == "few keys" else 40
+        return g, [70, 40, 200], new.tolist(), np.minimum(new + rng.integers(-1, most, 1403), most).clip(0).tolist()
+    if kind == "few or many":  # by turns at the kernel for few's bound
+        n = 60
+        own = np.array([16, 17, 0, 200, 15, 16])[np.arange(n) % 6]
+        return [n // 2, n // 2], [300, 77], (1 + np.arange(n) % 3).tolist(), own.tolist()
     if kind == "many groups":
         g = rng.integers(0, 3, 600).tolist()
         n = sum(g)
@@ -125,6 +130,10 @@ CASES = [
     ("chunks", "bf16", "bf16", 130, 1, 64, 64, 64, True),
     ("many", "bf16", "bf16", 4, 4, 64, 64, 16, True),
     ("many", "bf16", "mxfp8", 8, 2, 128, 128, 16, True),
+    ("few and more", "bf16", "bf16", 8, 2, 128, 128, 16, True),
+    ("few or many", "bf16", "mxfp8", 8, 2, 64, 64, 16, True),
+    ("few or many", "bf16", "bf16", 8, 1, 128, 64, 64, True),
+    ("few or many", "f32", "f32", 3, 3, 40, 48, 32, False),
     ("few keys", "bf16", "bf16", 6, 1, 64, 64, 16, True),
     ("few keys", "bf16", "mxfp8", 2, 2, 128, 96, 16, True),
     ("few keys", "bf16", "bf16", 2, 1, 40, 24, 16, False),

@@ -160,18 +160,40 @@ def test_a_window_of_one_key_is_its_value(dtype, dim):
         assert bool((g.float().abs() <= bound).all())
 
 
-def test_scores_far_apart():
-    """Rows whose hidden keys score far above what they see: nothing of them may remain."""
-    q, k, v, do, offs = batch([700, 300], 2, 128, 128, "bf16", seed=4)
-    at = torch.arange(1000, device="cuda")
-    k[(at % 150) < 20] *= 20
-    lens, window, sinks = [700, 300], 64, 3
-    ws = jfa.workspace(jfa.params_for(q, k, v, offs, None, True))
-    o, lse = jfa.jfa_window_fwd(q, k, v, offs, window, sinks=sinks, ws=ws)
-    grads = jfa.jfa_window_bwd(q, k, v, o, lse, do, offs, window, sinks=sinks, ws=ws)
-    want = reference(*(f64(x) for x in (q, k, v, do)), lens, window, sinks, float(np.float32(128 ** -0.5)))
-    got = dict(zip(("o", "lse", "dq", "dk", "dv"), (f64(x) for x in (o, lse, *grads))))
-    compare(got, want, "bf16")
+def spiky(dtype, dim, size):
+    lens = [700, 300]
+    q, k, v, do, offs = batch(lens, 2, dim, dim, dtype, seed=4)
+    at = torch.cat([torch.arange(n, device="cuda") for n in lens]) % 150
+    k[(at >= 10) & (at < 30)] *= size
+    return lens, q, k, v, do, offs, at
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("bf16", 64), ("f32", 40)])
+def test_hidden_scores_far_above_the_seen(dtype, dim):
+    """Keys that score far above what rows behind their window see: nothing of them may remain."""
+    window, sinks = 64, 3
+    lens, q, k, v, do, offs, _ = spiky(dtype, dim, 20.0)
+    o, lse = jfa.jfa_window_fwd(q, k, v, offs, window, sinks=sinks)
+    grads = jfa.jfa_window_bwd(q, k, v, o, lse, do, offs, window, sinks=sinks)
+    want = reference(*(f64(x) for x in (q, k, v, do)), lens, window, sinks, float(np.float32(dim ** -0.5)))
+    compare(dict(zip(("o", "lse", "dq", "dk", "dv"), (f64(x) for x in (o, lse, *grads)))), want, dtype)
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("bf16", 64), ("f32", 40)])
+def test_hidden_scores_of_any_size(dtype, dim):
+    """Hidden scores of 10^30 leave the rows that do not see them as they are without those keys' size.  (The
+    rows that see them have scores whose own fp32 rounding is 10^23: no backward is defined there.)"""
+    window, sinks = 64, 3
+    outs = []
+    for size in (1.0, 1e30):
+        _, q, k, v, _, offs, at = spiky(dtype, dim, size)
+        outs.append(jfa.jfa_window_fwd(q, k, v, offs, window, sinks=sinks))
+    free = (at < 10) | (at >= 30 + window - 1)
+    free[:30 + window] &= False  # (the first sequence's rows before any big key: nothing hidden)
+    for a, b in zip(*outs):
+        # the running maximum may move in other steps: fp32 sums, one rounding to bf16
+        assert bool(torch.isfinite(b[free].float()).all())
+        assert float((a[free].float() - b[free].float()).norm() / a[free].float().norm()) <= (2.0 ** -8 if a.dtype == torch.bfloat16 else 1e-5)
 
 
 def test_gradient_against_differences():
