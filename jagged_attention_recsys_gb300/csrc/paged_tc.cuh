@@ -219,22 +219,24 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
       const Streams s = streams_of<WIN>(p, t, g);
       if (s.blocks == 0) continue;
       const int head = g.unit;
+      // The queries go behind the first keys: their place is free only when the last tile's last scores are
+      // done, while the ring has room before, and the page look-up lies in front of the wait too.
+      auto queries = [&]() {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (!ok || s.n(x) == 0 || (s.split && x == 1)) continue;
-        if (!mbar_wait(bar(B_QEMPTY + x), (q_it[x] & 1) ^ 1, abort, status)) {
-          ok = false;
-          continue;
-        }
-        if (lane == 0) {
-          mbar_expect_tx(bar(B_QFULL + x), qbytes);
+        for (int x = 0; x < 2; ++x) {
+          if (s.n(x) == 0 || (s.split && x == 1)) continue;
+          if (!mbar_wait(bar(B_QEMPTY + x), (q_it[x] & 1) ^ 1, abort, status)) return false;
+          if (lane == 0) {
+            mbar_expect_tx(bar(B_QFULL + x), qbytes);
 #pragma unroll
-          for (int a = 0; a < DQK / 64; ++a)
-            tma_load_3d(sb + L::TILE0 + x * L::Q_BYTES + a * 16384, &tm_q, a * 64, head * p.group,
-                        g.seq.q0 + g.tile * t.tokens + x * (t.tokens / 2), bar(B_QFULL + x));
+            for (int a = 0; a < DQK / 64; ++a)
+              tma_load_3d(sb + L::TILE0 + x * L::Q_BYTES + a * 16384, &tm_q, a * 64, head * p.group,
+                          g.seq.q0 + g.tile * t.tokens + x * (t.tokens / 2), bar(B_QFULL + x));
+          }
+          ++q_it[x];
         }
-        ++q_it[x];
-      }
+        return true;
+      };
       for (int i0 = g.blk0; ok && i0 < g.blk1; i0 += 32 / per) {
         const int pos = WIN ? g.span.block(i0 + lane / per) * kKeys + lane % per * box : i0 * kKeys + lane * box;
         int row = none;
@@ -251,7 +253,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
             constexpr int ring = MX ? NR : NS;
             const uint32_t st = it % ring;
             const uint32_t full = bar((MX ? B_RFULL : B_FULL) + st), empty = bar((MX ? B_REMPTY : B_EMPTY) + st);
-            if (!mbar_wait(empty, ((it / ring) & 1) ^ 1, abort, status)) {
+            if ((kv == 1 && i0 + i == g.blk0 && !queries()) || !mbar_wait(empty, ((it / ring) & 1) ^ 1, abort, status)) {
               ok = false;
               break;
             }

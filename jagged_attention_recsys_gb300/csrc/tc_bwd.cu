@@ -727,7 +727,11 @@ tc_dkdv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           for (int c = 0; c < HC; ++c) sv[c] -= (c >= lo && c < hi) ? 0.f : shift_raw;
         }
         // P^T (and, for SiLU/L, the factor SiLU'(u)/L used by dS^T), packed bf16
+        // Under a window P stays in fp32 until dS is formed, which is then rounded once: dQ and dK are off by
+        // 2.4e-3 of their norm against 3.8e-3 with both factors in bf16 (2-norm, of which bf16's own
+        // rounding of the results is 1.7e-3).
         uint32_t pk[HC / 2], fk[ACT == kActSoftmax ? 1 : HC / 2];
+        float pf[WIN ? HC : 1];
 #pragma unroll
         for (int c = 0; c < HC; c += 2) {
           const float2 x = make_float2(sv[c], sv[c + 1]);
@@ -735,6 +739,11 @@ tc_dkdv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           if (ACT == kActSoftmax) {
             const float2 e = ffma2(x, cc, *reinterpret_cast<const float2*>(rs + c));
             pv = make_float2(ex2(e.x), ex2(e.y));
+            if constexpr (WIN) {
+              pf[c] = pv.x;
+              pf[c + 1] = pv.y;
+              continue;
+            }
           } else {
             // u = s c, h = u/2, t = tanh h: P = h (1+t)/L, SiLU'(u)/L = (1+t)/(2L) (1 + h - h t).
             // The factor formed here is twice SiLU'(u)/L, sharing (1+t)/L with P; dS^T and dK
@@ -751,13 +760,30 @@ tc_dkdv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         // dS^T = P^T (dP^T - D)  or  dP^T SiLU'(u)/L
         if (!mbar_wait(bar(KV_DPFULL + b), (s_it >> 1) & 1, abort, status)) { ok = false; break; }
         tc_fence_after();
-        float dp[HC];
-#pragma unroll
-        for (int c = 0; c < HC / 32; ++c) tmem_ld32(x_tm + 32 * c, dp + 32 * c);
-        tmem_wait_ld();
         uint32_t dk2[HC / 2];
+        if constexpr (WIN) {
 #pragma unroll
-        for (int c = 0; c < HC; c += 2) {
+          for (int h = 0; h < HC; h += 32) {
+            float dp[32];
+            tmem_ld32(x_tm + h, dp);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float2 t = fadd2(make_float2(dp[c], dp[c + 1]), *reinterpret_cast<const float2*>(rs + KSTEP + h + c));
+              const float2 ds = fmul2(make_float2(pf[h + c], pf[h + c + 1]), t);
+              dk2[(h + c) / 2] = pack_bf16(ds.x, ds.y);
+              pk[(h + c) / 2] = pack_bf16(pf[h + c], pf[h + c + 1]);
+            }
+          }
+        }
+        float dp[WIN ? 2 : HC];
+        if constexpr (!WIN) {
+#pragma unroll
+          for (int c = 0; c < HC / 32; ++c) tmem_ld32(x_tm + 32 * c, dp + 32 * c);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int c = 0; c < (WIN ? 0 : HC); c += 2) {
           const float2 d = make_float2(dp[c], dp[c + 1]);
           if (ACT == kActSoftmax) {  // dP^T - D in fp32, rounded to bf16, times the bf16 P^T
             const float2 t = fadd2(d, *reinterpret_cast<const float2*>(rs + KSTEP + c));
@@ -1354,6 +1380,7 @@ tc_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
         // P (softmax) or SiLU'(u)/L, packed bf16; both multiply dP into dS
         uint32_t fk[HC / 2];
+        float pf[WIN ? HC : 1];  // as in dK/dV: dS is rounded once
 #pragma unroll
         for (int c = 0; c < HC; c += 2) {
           const float2 x = make_float2(sv[c], sv[c + 1]);
@@ -1361,6 +1388,11 @@ tc_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
           if (ACT == kActSoftmax) {
             const float2 e = ffma2(x, cc, nl);
             f = make_float2(ex2(e.x), ex2(e.y));
+            if constexpr (WIN) {
+              pf[c] = f.x;
+              pf[c + 1] = f.y;
+              continue;
+            }
           } else {
             const float2 hh = fmul2(x, hc);
             const float2 t = make_float2(tanh_approx(hh.x), tanh_approx(hh.y));
@@ -1379,6 +1411,11 @@ tc_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         uint32_t dk2[HC / 2];
 #pragma unroll
         for (int c = 0; c < HC; c += 2) {
+          if constexpr (WIN) {
+            const float2 ds = fmul2(make_float2(pf[c], pf[c + 1]), fadd2(make_float2(dp[c], dp[c + 1]), nd));
+            dk2[c / 2] = pack_bf16(ds.x, ds.y);
+            continue;
+          }
           const float2 d = make_float2(dp[c], dp[c + 1]);
           if (ACT == kActSoftmax) {  // dP - D in fp32, rounded to bf16, times the bf16 P
             const float2 t = fadd2(d, nd);

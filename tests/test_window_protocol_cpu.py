@@ -1,12 +1,17 @@
-"""The ring of the paged attention's 128-row kernel under a window (`csrc/paged_tc.cuh`), on the CPU: tiles of
+"""Parts of the paged attention's 128-row kernel (`csrc/paged_tc.cuh`) on the CPU.  Its loader asks for a tile's
+queries behind the tile's first keys: the whole kernel's model with that order.  And under a window:
+
+The ring of the paged attention's 128-row kernel under a window (`csrc/paged_tc.cuh`), on the CPU: tiles of
 values of which some keys are hidden from every row, the sinks' block and the window's first among them,
 land on a barrier of their own and become full once a cleaner has zeroed those rows.  Every random interleaving
 of the loader, the loads, the cleaner and the two readers has to finish, and no reader may find a tile that is
 another's or not clean."""
+import inspect
 import random
 
 import pytest
 
+import test_paged_protocol_cpu as model
 from test_barrier_protocols import Bar
 
 
@@ -106,3 +111,36 @@ def test_cleaned_tiles(stages):
 def test_a_cleaner_of_the_last_block_alone_is_caught():
     rng = random.Random(1)
     assert any(play(segments(rng), 5, seed, clean_all=False, limit=3000) for seed in range(20))
+
+
+QUERIES = '''            for x in (0, 1):
+                if g.n[x] == 0 or (g.split and x):
+                    continue
+                yield lambda: qempty[x].done((q_it[x] & 1) ^ 1)
+                fly(land(qfull[x], qmem, x, n))
+                q_it[x] += 1
+'''
+RING = '''                for kv in (0, 1):
+                    f, e, mem, ring = (rfull, rempty, raw, raws) if raws else (full, empty, stage, stages)
+'''
+
+
+def with_keys_first():
+    """The model of the kernel with the loader's new order."""
+    source = inspect.getsource(model.play_tc)
+    assert source.count(QUERIES) == 1 and source.count(RING) == 1
+    late = " " * 20 + "if d == 0 and kv == 1:\n" + "".join(" " * 12 + line + "\n" for line in QUERIES.splitlines())
+    source = source.replace(QUERIES, "")
+    head, body = RING.split("\n", 1)
+    source = source.replace(RING, head + "\n" + late + body)
+    space = dict(vars(model))
+    exec(compile(source, "model", "exec"), space)
+    return space["play_tc"]
+
+
+@pytest.mark.parametrize("stages,raws", [(5, 0), (8, 0), (3, 3), (6, 3)])
+def test_queries_behind_the_first_keys(stages, raws):
+    play_tc = with_keys_first()
+    rng = random.Random(stages + 100)
+    for seed in range(150):
+        assert play_tc(model.tc_segments(rng), stages, raws, seed) is None
