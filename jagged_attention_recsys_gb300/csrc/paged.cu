@@ -34,6 +34,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSmemSeqs = 4096;  // scan kept in shared memory up to this batch
 
+template <int MODE>
 __global__ void __launch_bounds__(kPlanThreads)
 paged_plan_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, const PagedWs w) {
   extern __shared__ int64_t smem_cum[];
@@ -45,13 +46,13 @@ paged_plan_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
   int64_t* cum = B <= kPlanSmemSeqs ? smem_cum : w.cum;
   if (tid == 0) {
     carry_s = 0;
-    bad_s = (B == 0 && p.offs[0] != 0) || (p.phase == 2 && prior_failed(p));
+    bad_s = (B == 0 && p.offs[0] != 0) || (serves_shared(MODE) && p.phase == 2 && prior_failed(p));
     cum[0] = 0;
   }
   __syncthreads();
   for (int64_t base = 0; base < B; base += kPlanThreads) {
     const int64_t b = base + tid;
-    int64_t x = b < B ? checked_cost(p, t, b) : 0;
+    int64_t x = b < B ? checked_cost<MODE>(p, t, b) : 0;
     if (x < 0) {
       bad_s = 1;
       x = 0;
@@ -80,8 +81,11 @@ paged_plan_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
   }
   const int64_t W = carry_s;
   const bool bad = bad_s != 0;
-  if (tid == 0) w.hdr->status = bad ? (int)JFA_ERR_BAD_OFFSETS : p.phase == 2 ? *(volatile const int*)p.prior_status : (int)JFA_OK;
-  for (int c = tid; c <= ctas; c += kPlanThreads) w.pos[c] = paged_cut(p, t, ctas, c, cum, W, bad);
+  if (tid == 0)
+    w.hdr->status = bad                                    ? (int)JFA_ERR_BAD_OFFSETS
+                    : serves_shared(MODE) && p.phase == 2 ? *(volatile const int*)p.prior_status
+                                                          : (int)JFA_OK;
+  for (int c = tid; c <= ctas; c += kPlanThreads) w.pos[c] = paged_cut<MODE>(p, t, ctas, c, cum, W, bad);
 }
 
 // ------------------------------------------------------------------- the CUDA-core kernel
@@ -111,11 +115,11 @@ __device__ __forceinline__ float cache_value(const void* codes, const uint8_t* s
 
 // The end of a whole row: normalised to its place, or, of a shared prefix, phase 1's in fp32 and
 // phase 2's joined with it.
-template <typename T>
+template <typename T, int MODE>
 struct RowEnd {
   float own, prior, lse;
   __device__ __forceinline__ RowEnd(const Paged& p, int64_t row, float m, float l) {
-    if (p.phase == 2) {
+    if (serves_shared(MODE) && p.phase == 2) {
       const PagedJoin j = paged_join_prior(m, l, p.prior_lse[row]);
       own = j.own;
       prior = j.prior;
@@ -123,24 +127,25 @@ struct RowEnd {
     } else {
       own = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no key: 0; NaN stays NaN
       prior = 0.f;
-      lse = l == 0.f ? -INFINITY : p.phase == 1 ? m + log2f(l) : (m + log2f(l)) * kLn2;
+      lse = l == 0.f ? -INFINITY : serves_shared(MODE) && p.phase == 1 ? m + log2f(l) : (m + log2f(l)) * kLn2;
     }
   }
   __device__ __forceinline__ void put(const Paged& p, int64_t at, float x) const {
     x *= own;
-    if (p.phase == 1) p.prior_o[at] = x;
-    else ((T*)p.o)[at] = result<T>(p.phase == 2 ? fmaf(p.prior_o[at], prior, x) : x);
+    if (serves_shared(MODE) && p.phase == 1) p.prior_o[at] = x;
+    else ((T*)p.o)[at] = result<T>(serves_shared(MODE) && p.phase == 2 ? fmaf(p.prior_o[at], prior, x) : x);
   }
   __device__ __forceinline__ void finish(const Paged& p, int64_t row) const {
-    if (p.phase == 1) p.prior_lse[row] = lse;
+    if (serves_shared(MODE) && p.phase == 1) p.prior_lse[row] = lse;
     else p.lse[row] = lse;
   }
 };
 
-template <typename T, int KIND>
+template <typename T, int KIND, int MODE>
 __global__ void __launch_bounds__(kSimtThreads)
 paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedWs w) {
   extern __shared__ __align__(16) float sm[];
+  constexpr bool WIN = serves_windows(MODE);
   const int dq = p.dim_qk, dv = p.dim_v, ldq = dq + 1, ldv = dv + 1;
   float* Q = sm;                  // [16][dq + 1]
   float* K = Q + kRows * ldq;     // [32][dq + 1]
@@ -149,11 +154,11 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
   __shared__ int64_t row_of[kKeys];
   const int tid = threadIdx.x, r = tid >> 3, sub = tid & 7;
   __shared__ PagedPos share[2];
-  int* status = paged_share(p, t, w, share, sm);
+  int* status = paged_share<MODE>(p, t, w, share, sm);
   PagedWalk walk;
   walk.init(share);
   PagedSegment g;
-  while (walk.next(p, t, g)) {
+  while (walk.next<MODE>(p, t, g)) {
     const int head_k = g.unit / t.nsub, gs0 = (g.unit % t.nsub) * t.gsub;
     // this thread's row
     const int tok = g.tile * t.tokens + r / t.gsub, gh = gs0 + r % t.gsub;
@@ -168,7 +173,7 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
     }
     for (int i = tid + t.rows * ldq; i < kRows * ldq; i += kSimtThreads) Q[i] = 0.f;
     const int64_t limit = !row_ok ? 0 : p.causal ? g.seq.off + tok + 1 : g.seq.lk;  // keys the row sees
-    const int64_t from = p.window > 0 ? limit - p.window : 0;  // but for the sinks, none in front of this one
+    const int64_t from = WIN && p.window > 0 ? limit - p.window : 0;  // but for the sinks, none in front of this one
     float m = -INFINITY, l = 0.f, acc[16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) acc[c] = 0.f;
@@ -177,7 +182,7 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
       __syncthreads();
       if (tid < kKeys) {
         int64_t row = -1;
-        if (tid < nk && paged_sees(p, g.span.low, k0 + tid)) {
+        if (tid < nk && (!WIN || p.window == 0 || paged_sees(p, g.span.low, k0 + tid))) {
           const int page = paged_page(p, g.b, k0 + tid, status);
           if (page >= 0) row = paged_row(p, page, head_k, k0 + tid);
         }
@@ -201,7 +206,7 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
         float x = 0.f;
         for (int c = 0; c < dq; ++c) x = fmaf(Q[r * ldq + c], K[j * ldq + c], x);
         const int at = k0 + j;
-        s[i] = at < limit && j < nk && (at >= from || at < p.sinks) ? x * p.scale * kLog2e : -INFINITY;
+        s[i] = at < limit && j < nk && (!WIN || at >= from || at < p.sinks) ? x * p.scale * kLog2e : -INFINITY;
         mt = fmaxf(mt, s[i]);
       }
       for (int o = 4; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
@@ -245,7 +250,7 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
       }
     } else if (row_ok) {
       const int64_t orow = (int64_t)(g.seq.q0 + tok) * p.heads_q + head;
-      RowEnd<T> end(p, orow, m, l);
+      RowEnd<T, MODE> end(p, orow, m, l);
 #pragma unroll
       for (int c = 0; c < 16; ++c)
         if (sub + 8 * c < dv) end.put(p, orow * dv + sub + 8 * c, acc[c]);
@@ -257,12 +262,13 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
 // --------------------------------------------------------------------------- the join
 // A warp a row: the parts of a split tile, rescaled to their common maximum and added in CTA
 // order.  CTA x of the grid serves the tile whose parts begin with CTA x's last one.  Bound: latency, of
-// the look-ups first; places and statistics of 32 parts are a lane's each, two rows of a warp and four
-// parts of each are on their way at once.  16 tiles of 256 rows in some ten parts each: 10 us, where eight
-// rows a warp and one part after the other took 60; 152 tiles in two parts each, 25 us.
+// the look-ups first; places and statistics of 32 parts are a lane's each, four parts of a row are on
+// their way at once, and two rows where a warp has more than one.  16 tiles of 256 rows in some ten parts
+// each: 10 us, where eight rows a warp and one part after the other took 60; 152 tiles in two parts each,
+// 24 us; some 300 parts of 16 rows, a row a warp: 6.0 us, 7.4 with the code for two.
 constexpr int kJoinWarps = 4, kJoinTall = 32;  // warps of a CTA, most CTAs of a tile
 
-template <typename T>
+template <typename T, int MODE, int R>  // R: rows of a warp at once
 __global__ void __launch_bounds__(kJoinWarps * 32)
 paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, const PagedWs w) {
   const int c = blockIdx.x, lane = threadIdx.x & 31;
@@ -271,13 +277,13 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
     static_assert(JFA_OK < 1 && 1 < JFA_ERR_BAD_OFFSETS && JFA_ERR_BAD_OFFSETS < JFA_ERR_TIMEOUT, "ranks");
     int st = 0;
     for (int i = lane; i < w.ctas; i += 32) st = max(st, w.cta_status[i] == JFA_ERR_BAD_PAGES ? 1 : w.cta_status[i]);
-    if (p.phase == 2) st = max(st, *p.prior_status == JFA_ERR_BAD_PAGES ? 1 : *p.prior_status);
+    if (serves_shared(MODE) && p.phase == 2) st = max(st, *p.prior_status == JFA_ERR_BAD_PAGES ? 1 : *p.prior_status);
     st = __reduce_max_sync(0xffffffffu, st);
     if (lane == 0) w.hdr->status = st == 1 ? (int)JFA_ERR_BAD_PAGES : st;
   }
   // the CTAs that hold the tile's parts: c (slot 1), then c + 1 .. last (slot 0), looked up 32 at a time
   PagedCutTile cut;
-  if (!cut.begins(p, t, w, ctas, c)) return;
+  if (!cut.begins<MODE>(p, t, w, ctas, c)) return;
   const PagedSeq& seq = cut.seq;
   int last = c + 1;
   for (;;) {
@@ -295,8 +301,7 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
   };
   const bool mine = has_part(c + lane);  // of the first 32
   const unsigned parts = __ballot_sync(0xffffffffu, mine);
-  // two rows of a warp at once, four columns a lane
-  constexpr int R = 2, U = 4;  // U: parts whose rows are on their way
+  constexpr int U = 4;  // parts whose rows are on their way, four columns a lane
   const int step = gridDim.y * kJoinWarps, c4 = 4 * lane;
   const bool in_v = c4 < p.dim_v;
   for (int r0 = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r0 < t.rows; r0 += R * step) {
@@ -348,7 +353,7 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
           }
         }
       }
-      RowEnd<T> end(p, orow[q], m, l);
+      RowEnd<T, MODE> end(p, orow[q], m, l);
       if (in_v) {
         const float y[4] = {acc[q].x, acc[q].y, acc[q].z, acc[q].w};
 #pragma unroll
@@ -359,9 +364,12 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
   }
 }
 
+// The instances that carry neither windows nor prefixes serve what needs neither.
+bool plain(const Paged& p) { return p.window == 0 && p.phase == 0; }
+
 template <typename T, int KIND>
 cudaError_t simt_t(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s) {
-  auto kern = paged_simt_kernel<T, KIND>;
+  auto kern = plain(p) ? paged_simt_kernel<T, KIND, kAll> : paged_simt_kernel<T, KIND, kAny>;
   size_t smem = sizeof(float) * ((kRows + kKeys) * (p.dim_qk + 1) + kKeys * (p.dim_v + 1) + kRows * 33);
   if (smem < kPlanScratch) smem = kPlanScratch;
   constexpr size_t most = sizeof(float) * ((kRows + kKeys) * 129 + kKeys * 129 + kRows * 33);
@@ -466,7 +474,8 @@ size_t shared_layout(const Paged& prefix, const Paged& own, void* base, PagedWs*
 
 cudaError_t launch_paged_plan(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s) {
   const size_t smem = p.batch <= kPlanSmemSeqs ? sizeof(int64_t) * (size_t)(p.batch + 1) : 0;
-  paged_plan_kernel<<<1, kPlanThreads, smem, s>>>(p, t, ctas, w);
+  if (plain(p)) paged_plan_kernel<kAll><<<1, kPlanThreads, smem, s>>>(p, t, ctas, w);
+  else paged_plan_kernel<kAny><<<1, kPlanThreads, smem, s>>>(p, t, ctas, w);
   return cudaGetLastError();
 }
 
@@ -482,10 +491,15 @@ cudaError_t launch_paged_combine(const Paged& p, const TileShape& t, int ctas, i
                                  cudaStream_t s) {
   int gy = (t.rows + kJoinWarps - 1) / kJoinWarps;
   if (gy > kJoinTall) gy = kJoinTall;
-  if (dtype == JFA_BF16)
-    paged_join_kernel<__nv_bfloat16><<<dim3(ctas, gy), kJoinWarps * 32, 0, s>>>(p, t, ctas, w);
-  else
-    paged_join_kernel<float><<<dim3(ctas, gy), kJoinWarps * 32, 0, s>>>(p, t, ctas, w);
+  const bool two = t.rows > gy * kJoinWarps;
+  using Join = void (*)(Paged, TileShape, int, PagedWs);
+  const Join bf16[2][2] = {{paged_join_kernel<__nv_bfloat16, kAny, 1>, paged_join_kernel<__nv_bfloat16, kAny, 2>},
+                           {paged_join_kernel<__nv_bfloat16, kAll, 1>, paged_join_kernel<__nv_bfloat16, kAll, 2>}};
+  const Join f32[2][2] = {{paged_join_kernel<float, kAny, 1>, paged_join_kernel<float, kAny, 2>},
+                          {paged_join_kernel<float, kAll, 1>, paged_join_kernel<float, kAll, 2>}};
+  const int more = t.rows > gy * kJoinWarps;
+  const Join kern = (dtype == JFA_BF16 ? bf16 : f32)[plain(p)][more];
+  kern<<<dim3(ctas, gy), kJoinWarps * 32, 0, s>>>(p, t, ctas, w);
   return cudaGetLastError();
 }
 

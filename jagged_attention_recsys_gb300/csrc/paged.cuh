@@ -20,22 +20,27 @@ struct PagedSeq {
 struct PagedBounds {
   int64_t x, y;
 };
+template <int MODE = kAny>
 __device__ __forceinline__ PagedBounds paged_bounds(const Paged& p, int64_t b) {
-  if (!p.groups) return PagedBounds{__ldg(p.offs + b), __ldg(p.offs + b + 1)};
+  if (!serves_shared(MODE) || !p.groups) return PagedBounds{__ldg(p.offs + b), __ldg(p.offs + b + 1)};
   const int64_t s = __ldg(p.groups + b), n = __ldg(p.groups + b + 1);
   if (s < 0 || n < s || n > p.seqs || (b == 0 && s != 0) || (b == p.batch - 1 && n != p.seqs)) return PagedBounds{-1, -1};
   return PagedBounds{__ldg(p.offs + s), __ldg(p.offs + n)};
 }
 // Whether a sequence of so many own keys is the short kernel's.
-__device__ __forceinline__ bool is_few(const Paged& p, int64_t keys) { return p.few > 0 && keys <= p.few; }
+template <int MODE = kAny>
+__device__ __forceinline__ bool is_few(const Paged& p, int64_t keys) {
+  return serves_shared(MODE) && p.few > 0 && keys <= p.few;
+}
+template <int MODE = kAny>
 __device__ __forceinline__ PagedSeq paged_seq(const Paged& p, const TileShape& t, int b) {
   PagedSeq s;
-  const PagedBounds n = paged_bounds(p, b);
+  const PagedBounds n = paged_bounds<MODE>(p, b);
   const int64_t a = n.x, e = n.y, l = __ldg(p.lens + b);
   // (what a plan was not made for and is no batch either has no tokens)
   const bool ok = a >= 0 && e >= a && e <= p.total_q && l >= 0 && l <= ((int64_t)p.width << p.page_shift);
   s.q0 = (int)a;
-  s.lq = ok && !is_few(p, l) ? (int)(e - a) : 0;
+  s.lq = ok && !is_few<MODE>(p, l) ? (int)(e - a) : 0;
   s.lk = (int)l;
   s.off = l - (e - a);
   s.tiles = (s.lq + t.tokens - 1) / t.tokens;
@@ -56,16 +61,16 @@ struct PagedSpan {
   __device__ __forceinline__ int block(int i) const { return i < ns ? i : i - ns + first; }
 };
 // off: position of the sequence's first new token, end: keys that the tile's last row sees
-template <bool WIN = true>
-__device__ __forceinline__ PagedSpan paged_span(const Paged& p, const TileShape& t, int64_t off, int64_t end, int64_t tile) {
+template <int MODE = kAny>
+__device__ __forceinline__ PagedSpan paged_span(const Paged& p, const TileShape& t, int64_t off, int end, int tile) {
   PagedSpan s;
-  s.nb = (int)((end + t.keys - 1) / t.keys);
+  s.nb = (end + t.keys - 1) / t.keys;
   s.ns = s.first = s.low = 0;
-  if (WIN && p.window > 0) {
-    const int64_t low = off + tile * t.tokens - p.window + 1;
-    s.low = (int)min(max((int64_t)0, low), end);
+  if (serves_windows(MODE) && p.window > 0) {
+    const int64_t low = off + (int64_t)tile * t.tokens - p.window + 1;
+    s.low = (int)min(max((int64_t)0, low), (int64_t)end);
     s.first = min(s.low / t.keys, max(s.nb - 1, 0));
-    s.ns = min((int)(((int64_t)p.sinks + t.keys - 1) / t.keys), s.first);
+    s.ns = min(p.sinks / t.keys + (p.sinks % t.keys != 0), s.first);
     s.nb -= s.first - s.ns;
   }
   return s;
@@ -74,9 +79,10 @@ __device__ __forceinline__ PagedSpan paged_span(const Paged& p, const TileShape&
 __device__ __forceinline__ bool paged_sees(const Paged& p, int low, int x) { return x >= low || x < p.sinks; }
 
 // ------------------------------------------------------------------- cutting the work
+template <int MODE = kAny>
 struct SeqCost {
   int64_t off, lk, tiles, s, over;
-  int64_t most;  // keys that a tile meets at most: a window's with its sinks, and part of a block
+  int64_t most;  // a window: keys that a tile meets at most, with its sinks and part of a block
   int causal;
   // cost of the tiles in front of tile t, t <= tiles - 1
   __device__ int64_t before(int64_t t) const {
@@ -84,39 +90,49 @@ struct SeqCost {
     // tile u sees max(0, off + (u + 1) s) keys, and meets at most `most`
     int64_t u0 = off < 0 ? (-off) / s : 0;  // tiles that see nothing
     if (u0 > t) u0 = t;
-    int64_t u1 = most > off ? (most - off) / s : 0;  // tiles that meet all that they see
-    if (u1 > t) u1 = t;
-    if (u1 < u0) u1 = u0;
-    return t * over + (u1 - u0) * off + s * ((u1 * (u1 + 1) - u0 * (u0 + 1)) / 2) + (t - u1) * (u1 < t ? most : 0);
+    int64_t u1 = t;  // tiles that meet all that they see
+    if constexpr (serves_windows(MODE)) {
+      if (most < (int64_t)1 << 40) u1 = most > off ? (most - off) / s : 0;
+      if (u1 > t) u1 = t;
+      if (u1 < u0) u1 = u0;
+    }
+    const int64_t c = t * over + (u1 - u0) * off + s * ((u1 * (u1 + 1) - u0 * (u0 + 1)) / 2);
+    return serves_windows(MODE) && u1 < t ? c + (t - u1) * most : c;
   }
-  __device__ int64_t total() const { return tiles == 0 ? 0 : before(tiles - 1) + over + min(lk, most); }
+  __device__ int64_t total() const {
+    return tiles == 0 ? 0 : before(tiles - 1) + over + (serves_windows(MODE) ? min(lk, most) : lk);
+  }
 };
-__device__ __forceinline__ SeqCost seq_cost(const Paged& p, const TileShape& t, int64_t lq, int64_t lk) {
-  SeqCost c;
+template <int MODE = kAny>
+__device__ __forceinline__ SeqCost<MODE> seq_cost(const Paged& p, const TileShape& t, int64_t lq, int64_t lk) {
+  SeqCost<MODE> c;
   c.off = lk - lq;
   c.lk = lk;
   c.s = t.tokens;
   c.tiles = (lq + t.tokens - 1) / t.tokens;
   c.over = t.overhead;
   c.most = (int64_t)1 << 40;
-  if (p.window > 0) c.most = (int64_t)p.window + t.tokens + t.keys + ((int64_t)p.sinks + t.keys - 1) / t.keys * t.keys;
+  if (serves_windows(MODE) && p.window > 0)
+    c.most = (int64_t)p.window + t.tokens + t.keys + ((int64_t)p.sinks + t.keys - 1) / t.keys * t.keys;
   c.causal = p.causal;
   return c;
 }
 
 // Cost of sequence b in all its units, or -1: the arrays do not describe a batch.
+template <int MODE = kAny>
 __device__ __forceinline__ int64_t checked_cost(const Paged& p, const TileShape& t, int64_t b) {
-  const PagedBounds n = paged_bounds(p, b);
+  const PagedBounds n = paged_bounds<MODE>(p, b);
   const int64_t a = n.x, e = n.y, lk = __ldg(p.lens + b);
   if (a < 0 || e < a || e > p.total_q || lk < 0 || lk > ((int64_t)p.width << p.page_shift) || (b == 0 && a != 0) ||
       (b == p.batch - 1 && e != p.total_q))
     return -1;
-  if (is_few(p, lk)) return 0;
-  return (int64_t)p.heads_k * t.nsub * seq_cost(p, t, e - a, lk).total();
+  if (is_few<MODE>(p, lk)) return 0;
+  return (int64_t)p.heads_k * t.nsub * seq_cost<MODE>(p, t, e - a, lk).total();
 }
 
 // Where CTA c of `ctas` begins (c = ctas: the end); cum[b]: cost of the sequences before b, in all
 // W = cum[B].  Little work goes to fewer CTAs, so that a share is worth its tile's fixed cost.
+template <int MODE = kAny>
 __device__ __forceinline__ PagedPos paged_cut(const Paged& p, const TileShape& t, int ctas, int c, const int64_t* cum,
                                               int64_t W, bool bad) {
   const int64_t n = max((int64_t)1, min((int64_t)ctas, W / t.share));
@@ -129,8 +145,8 @@ __device__ __forceinline__ PagedPos paged_cut(const Paged& p, const TileShape& t
     if (cum[m + 1] > x) hi = m;
     else lo = m + 1;
   }
-  const PagedBounds bounds = paged_bounds(p, lo);
-  const SeqCost sc = seq_cost(p, t, bounds.y - bounds.x, __ldg(p.lens + lo));
+  const PagedBounds bounds = paged_bounds<MODE>(p, lo);
+  const SeqCost<MODE> sc = seq_cost<MODE>(p, t, bounds.y - bounds.x, __ldg(p.lens + lo));
   const int64_t S = sc.total(), y = x - cum[lo];
   const int64_t unit = y / S, z = y - unit * S;
   int64_t tl = 0, th = sc.tiles - 1;
@@ -140,7 +156,7 @@ __device__ __forceinline__ PagedPos paged_cut(const Paged& p, const TileShape& t
     else th = m - 1;
   }
   const int64_t vis = tl == sc.tiles - 1 || !sc.causal ? sc.lk : max((int64_t)0, sc.off + (tl + 1) * sc.s);
-  const int64_t nb = paged_span(p, t, sc.off, vis, tl).nb;
+  const int64_t nb = paged_span<MODE>(p, t, sc.off, (int)vis, (int)tl).nb;
   const int64_t d = z - sc.before(tl) - sc.over;
   const int64_t blk = d <= 0 ? 0 : (d + t.keys / 2) / t.keys;
   r.b = (int)lo;
@@ -173,6 +189,7 @@ __device__ __forceinline__ bool prior_failed(const Paged& p) {
 // kPlanScratch bytes), and leaves its cut and its status in the workspace for the join.  All
 // threads of the CTA call it (at least 128), ahead of any other use of scratch.  Returns
 // where the CTA records errors.
+template <int MODE = kAny>
 __device__ __forceinline__ int* paged_share(const Paged& p, const TileShape& t, const PagedWs& w, PagedPos* pos,
                                             void* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
@@ -189,11 +206,11 @@ __device__ __forceinline__ int* paged_share(const Paged& p, const TileShape& t, 
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int b = tid * kEach + i;
-    cost[i] = tid < kThreads && b < p.batch ? checked_cost(p, t, b) : 0;
+    cost[i] = tid < kThreads && b < p.batch ? checked_cost<MODE>(p, t, b) : 0;
     bad |= cost[i] < 0;
     x += cost[i];
   }
-  if (p.phase == 2 && tid == 0) bad |= prior_failed(p);
+  if (serves_shared(MODE) && p.phase == 2 && tid == 0) bad |= prior_failed(p);
   bad = __syncthreads_or(bad) != 0;
   int64_t before = x;
   if (tid < kThreads) {
@@ -213,7 +230,7 @@ __device__ __forceinline__ int* paged_share(const Paged& p, const TileShape& t, 
   }
   __syncthreads();
   if (tid < 2) {
-    pos[tid] = paged_cut(p, t, w.ctas, c + tid, cum, cum[p.batch], bad);
+    pos[tid] = paged_cut<MODE>(p, t, w.ctas, c + tid, cum, cum[p.batch], bad);
     if (tid == 0 || c == w.ctas - 1) w.pos[c + tid] = pos[tid];
     if (tid == 0) w.cta_status[c] = bad ? JFA_ERR_BAD_OFFSETS : JFA_OK;
   }
@@ -238,14 +255,13 @@ struct PagedWalk {
     end = share[1];
     fresh = true;
   }
-  // WIN false: of kernels that serve no window
-  template <bool WIN = true>
+  template <int MODE = kAny>
   __device__ __forceinline__ bool next(const Paged& p, const TileShape& t, PagedSegment& s) {
     const int units = p.heads_k * t.nsub;
     for (;;) {
       if (at.b > end.b || at.b >= p.batch) return false;
       if (fresh) {
-        seq = paged_seq(p, t, at.b);
+        seq = paged_seq<MODE>(p, t, at.b);
         fresh = false;
       }
       if (at.tile >= seq.tiles) {
@@ -266,7 +282,7 @@ struct PagedWalk {
       s.unit = at.unit;
       s.tile = at.tile;
       s.seq = seq;
-      s.span = paged_span<WIN>(p, t, seq.off, tile_keys(p, t, seq, at.tile), at.tile);
+      s.span = paged_span<MODE>(p, t, seq.off, tile_keys(p, t, seq, at.tile), at.tile);
       s.nb = s.span.nb;
       s.blk0 = min(at.blk, s.nb);
       s.blk1 = same ? min(end.blk, s.nb) : s.nb;
@@ -288,12 +304,13 @@ struct PagedCutTile {
     return x.b == end.b && x.unit == end.unit && x.tile == end.tile;
   }
   // False: no tile is cut here, or it begins in an earlier CTA's share, or the plan is another request's.
+  template <int MODE = kAny>
   __device__ __forceinline__ bool begins(const Paged& p, const TileShape& t, const PagedWs& w, int ctas, int c) {
     end = paged_pos(p, t, w, c + 1);
     if (end.blk == 0 || end.b >= p.batch || c + 1 == ctas) return false;
     const PagedPos at = paged_pos(p, t, w, c);
     if (same(at) && at.blk > 0) return false;
-    seq = paged_seq(p, t, end.b);
+    seq = paged_seq<MODE>(p, t, end.b);
     return end.tile < seq.tiles;
   }
   // Whether CTA i, whose parts would follow CTA i - 1's, has work of the tile (or a share that is empty).

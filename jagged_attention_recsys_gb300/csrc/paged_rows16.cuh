@@ -208,7 +208,7 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
   volatile int* abort = (volatile int*)(smem_raw + (sb - smem_u32(smem_raw)) + 16 * NS);
   // in the stages' place, before any load
   PagedPos* share = reinterpret_cast<PagedPos*>(smem_raw + (sb - smem_u32(smem_raw)) + L::ML - 32);
-  int* status = paged_share(p, t, w, share, smem_raw + (sb - smem_u32(smem_raw)) + L::TILES);
+  int* status = paged_share<MODE>(p, t, w, share, smem_raw + (sb - smem_u32(smem_raw)) + L::TILES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -234,7 +234,7 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
     const int box = min(1 << p.page_shift, kStage), per = kStage / box;  // rows of a box, boxes of a stage
     const int none = (int)((p.pages * p.heads_k) << p.page_shift);    // behind the last row: read as zeros
     bool ok = true;
-    while (ok && walk.next<WIN>(p, t, g)) {
+    while (ok && walk.next<MODE>(p, t, g)) {
       const int head = g.unit / t.nsub;
       for (int i0 = g.blk0; ok && i0 < g.blk1; i0 += 32 / per) {
         // this lane's box of the next 32: its first row, or one behind the cache where it has no keys
@@ -298,7 +298,7 @@ paged_rows16_kernel(const __grid_constant__ Paged p, const TileShape t, const Pa
   constexpr int NBK = DQK / 32, NBV = DV / 32;
   // a consumer that gave up in a wait walks on without computing, so that its barriers still match
   bool dead = w.hold && blockIdx.x == 0 && warp == 0 && !mbar_wait(hold, 0, abort, status);
-  while (walk.next<WIN>(p, t, g)) {
+  while (walk.next<MODE>(p, t, g)) {
     const int head_k = g.unit / t.nsub, gs0 = (g.unit % t.nsub) * t.gsub;
     uint32_t qb[NT][DQK / 16][2];
     int limit[NT][2];  // keys that rows 2 q, 2 q + 1 see

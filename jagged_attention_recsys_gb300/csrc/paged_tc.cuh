@@ -27,9 +27,9 @@
 // its commit PV has completed: O may then be rescaled without a further wait.
 // The row maximum is kept lazily: O and the sum are rescaled only when it grows by more
 // than 2^8.
-// Measured: 8 prompts of 1024 to 4096 tokens, 32 heads on 8 of 128, causal, bf16: 428 us, 1070
-// TFLOP/s; 13 chunks of up to 512 tokens over caches of up to 16384, 32 heads on 4, MXFP8: 463 us,
-// 970 TFLOP/s.  The prompts without any softmax take 335 us, with its TMEM loads and stores 343:
+// Measured: 8 prompts of 1024 to 4096 tokens, 32 heads on 8 of 128, causal, bf16: 420 us, 1090
+// TFLOP/s; 13 chunks of up to 512 tokens over caches of up to 16384, 32 heads on 4, MXFP8: 457 us,
+// 980 TFLOP/s.  The prompts without any softmax take 335 us, with its TMEM loads and stores 343:
 // a stream's softmax and its products follow one another, since its S and P share their columns
 // of TMEM, and both streams' tiles fill the 512.  Not faster: the weights handed over in halves
 // (433 us), two threads a row (495; they share a scheduler), the exponentials begun against an
@@ -159,7 +159,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
   const uint32_t sb = (raw + 1023u) & ~1023u;
   uint8_t* const sp = smem_raw + (sb - raw);
   PagedPos* share = reinterpret_cast<PagedPos*>(sp + L::XCH - 32);
-  int* status = paged_share(p, t, w, share, sp + L::TILE0);  // in the queries' place, before any load
+  int* status = paged_share<MODE>(p, t, w, share, sp + L::TILE0);  // in the queries' place, before any load
   auto bar = [&](uint32_t i) { return sb + 8u * i; };
   uint32_t* tmem_slot = (uint32_t*)(sp + 8 * B_COUNT);
   volatile int* abort = (volatile int*)(sp + 8 * B_COUNT + 4);
@@ -215,12 +215,14 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
     const uint32_t qbytes = DQK * 2 * (uint32_t)rows1;
     uint32_t it = 0, q_it[2] = {0, 0};
     bool ok = true;
-    while (ok && walk.next<WIN>(p, t, g)) {
+    while (ok && walk.next<MODE>(p, t, g)) {
       const Streams s = streams_of<WIN>(p, t, g);
       if (s.blocks == 0) continue;
       const int head = g.unit;
-      // The queries go behind the first keys: their place is free only when the last tile's last scores are
-      // done, while the ring has room before, and the page look-up lies in front of the wait too.
+      // In bf16 the queries go behind the first keys: their place is free only when the last tile's last
+      // products are done, and the keys need not wait for that (prompts 420 us, 434 with the queries
+      // first).  MXFP8's keys are still to be converted, from stages that run full ahead of the tile's end
+      // anyway: there the queries go first (chunks 457 us, 479 with the keys first).
       auto queries = [&]() {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -237,6 +239,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
         }
         return true;
       };
+      if (MX) ok = queries();
       for (int i0 = g.blk0; ok && i0 < g.blk1; i0 += 32 / per) {
         const int pos = WIN ? g.span.block(i0 + lane / per) * kKeys + lane % per * box : i0 * kKeys + lane * box;
         int row = none;
@@ -253,7 +256,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
             constexpr int ring = MX ? NR : NS;
             const uint32_t st = it % ring;
             const uint32_t full = bar((MX ? B_RFULL : B_FULL) + st), empty = bar((MX ? B_REMPTY : B_EMPTY) + st);
-            if ((kv == 1 && i0 + i == g.blk0 && !queries()) || !mbar_wait(empty, ((it / ring) & 1) ^ 1, abort, status)) {
+            if ((!MX && kv == 1 && i0 + i == g.blk0 && !queries()) || !mbar_wait(empty, ((it / ring) & 1) ^ 1, abort, status)) {
               ok = false;
               break;
             }
@@ -298,7 +301,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
     const uint32_t t_s = tmem + T_S + x * 128, t_o = tmem + T_O + x * 128;
     uint32_t it = 0, qa_it = 0, qb_it = 0, p_it = 0, o_it = 0, turn = 0;
     bool ok = !(w.hold && blockIdx.x == 0 && x == 0) || mbar_wait(bar(B_HOLD), 0, abort, status);
-    while (ok && walk.next<WIN>(p, t, g)) {
+    while (ok && walk.next<MODE>(p, t, g)) {
       const Streams s = streams_of<WIN>(p, t, g);
       if (s.blocks == 0) continue;
       const int n = s.n(x);
@@ -384,7 +387,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
       PagedSegment g;
       uint32_t it = 0, phase = 0;  // phase: a bit a stage
       bool ok = true;
-      while (ok && walk.next<WIN>(p, t, g)) {
+      while (ok && walk.next<MODE>(p, t, g)) {
         // without a window, the segment's last block alone may have hidden keys
         for (int blk = WIN ? g.blk0 : max(g.blk0, g.blk1 - 1); ok && blk < g.blk1; ++blk) {
           const int k0 = (WIN ? g.span.block(blk) : blk) * kKeys;
@@ -425,7 +428,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
     const int rt = r / t.gsub, rg = r - rt * t.gsub;
     uint32_t s_it = 0, o_it = 0, x_it = 0;
     bool ok = true;
-    while (ok && walk.next<WIN>(p, t, g)) {
+    while (ok && walk.next<MODE>(p, t, g)) {
       const Streams s = streams_of<WIN>(p, t, g);
       const int n = s.n(x);
       const int tok = g.tile * t.tokens + (s.split ? 0 : x * half) + rt;
@@ -638,7 +641,7 @@ paged_tc_kernel(const __grid_constant__ Paged p, const TileShape t, const PagedW
       const int row = threadIdx.x & 127, part = (threadIdx.x - 384) >> 7;  // key of the block, half of its columns
       uint32_t it = 0;
       bool ok = true;
-      while (ok && walk.next<WIN>(p, t, g)) {
+      while (ok && walk.next<MODE>(p, t, g)) {
         for (int blk = g.blk0; ok && blk < g.blk1; ++blk) {
           // hidden rows become zeros
           const int at = (WIN ? g.span.block(blk) : blk) * kKeys + row;

@@ -41,9 +41,11 @@ constexpr int kNormRopeParts = 1024;  // most partial sums a backward writes
 // ------------------------------------------------------------- paged cache and attention
 enum : int { kCacheF32 = 0, kCacheBf16 = 1, kCacheMx = 2 };
 
-// What a kernel over a paged cache is compiled for: attention of all keys, of a window with sinks, or
-// one of the two phases of a shared prefix.
-enum : int { kAll = 0, kWindow = 1, kShared = 2 };
+// What a kernel over a paged cache is compiled for: attention of all keys, of a window with sinks, one
+// of the two phases of a shared prefix, or any of these as the request says.
+enum : int { kAll = 0, kWindow = 1, kShared = 2, kAny = 3 };
+constexpr bool serves_windows(int mode) { return mode == kWindow || mode == kAny; }
+constexpr bool serves_shared(int mode) { return mode == kShared || mode == kAny; }
 
 // One request on a paged cache.
 struct Paged {
@@ -142,6 +144,8 @@ cudaError_t launch_cache_read(const Paged& p, int dtype, void* k, void* v, Paged
 cudaError_t launch_cache_check(const Paged& p, PagedHeader* hdr, cudaStream_t s);
 // a.side: queries (heads 0: none) and keys; p.v, p.sv: values.
 cudaError_t launch_append(const Paged& p, const NormRopeArgs& a, int dtype, PagedHeader* hdr, int planned, cudaStream_t s);
+// (Calls without windows and prefixes have instances of their own: carried along, those cost a step of four
+// users 4 us and the MXFP8 step 25.)
 cudaError_t launch_paged_plan(const Paged& p, const TileShape& t, int ctas, const PagedWs& w, cudaStream_t s);
 cudaError_t launch_paged_simt(const Paged& p, const TileShape& t, int ctas, int dtype, const PagedWs& w,
                               cudaStream_t s);
