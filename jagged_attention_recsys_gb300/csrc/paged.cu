@@ -23,6 +23,7 @@
 
 #include "paged.cuh"
 #include "paged_join.cuh"
+#include "tc_ptx.cuh"
 
 namespace jfa {
 namespace {
@@ -134,6 +135,20 @@ struct RowEnd {
     x *= own;
     if (serves_shared(MODE) && p.phase == 1) p.prior_o[at] = x;
     else ((T*)p.o)[at] = result<T>(serves_shared(MODE) && p.phase == 2 ? fmaf(p.prior_o[at], prior, x) : x);
+  }
+  // four columns at once, `at` a multiple of four
+  __device__ __forceinline__ void put4(const Paged& p, int64_t at, float4 x) const {
+    x = make_float4(x.x * own, x.y * own, x.z * own, x.w * own);
+    if (serves_shared(MODE) && p.phase == 1) {
+      *reinterpret_cast<float4*>(p.prior_o + at) = x;
+      return;
+    }
+    if (serves_shared(MODE) && p.phase == 2) {
+      const float4 y = *reinterpret_cast<const float4*>(p.prior_o + at);
+      x = make_float4(fmaf(y.x, prior, x.x), fmaf(y.y, prior, x.y), fmaf(y.z, prior, x.z), fmaf(y.w, prior, x.w));
+    }
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>((T*)p.o + at) = x;
+    else *reinterpret_cast<uint2*>((T*)p.o + at) = make_uint2(tc::pack_bf16(x.x, x.y), tc::pack_bf16(x.z, x.w));
   }
   __device__ __forceinline__ void finish(const Paged& p, int64_t row) const {
     if (serves_shared(MODE) && p.phase == 1) p.prior_lse[row] = lse;
@@ -262,13 +277,13 @@ paged_simt_kernel(const __grid_constant__ Paged p, const TileShape t, const Page
 // --------------------------------------------------------------------------- the join
 // A warp a row: the parts of a split tile, rescaled to their common maximum and added in CTA
 // order.  CTA x of the grid serves the tile whose parts begin with CTA x's last one.  Bound: latency, of
-// the look-ups first; places and statistics of 32 parts are a lane's each, four parts of a row are on
-// their way at once, and two rows where a warp has more than one.  16 tiles of 256 rows in some ten parts
-// each: 10 us, where eight rows a warp and one part after the other took 60; 152 tiles in two parts each,
-// 24 us; some 300 parts of 16 rows, a row a warp: 6.0 us, 7.4 with the code for two.
+// the look-ups first; places and statistics of 32 parts are a lane's each, and two parts of a row are on
+// their way at once.  152 tiles of 256 rows in two parts each: 19 us (four parts 23, two rows a warp with
+// four parts each 24); 16 such tiles in some ten parts each 13 us, where eight rows a warp and one part
+// after the other took 60; some 300 tiles of 16 rows 5.5 us.
 constexpr int kJoinWarps = 4, kJoinTall = 32;  // warps of a CTA, most CTAs of a tile
 
-template <typename T, int MODE, int R>  // R: rows of a warp at once
+template <typename T, int MODE>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, const PagedWs w) {
   const int c = blockIdx.x, lane = threadIdx.x & 31;
@@ -301,66 +316,52 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
   };
   const bool mine = has_part(c + lane);  // of the first 32
   const unsigned parts = __ballot_sync(0xffffffffu, mine);
-  constexpr int U = 4;  // parts whose rows are on their way, four columns a lane
-  const int step = gridDim.y * kJoinWarps, c4 = 4 * lane;
+  constexpr int U = 2;  // parts whose rows are on their way, four columns a lane
+  const int c4 = 4 * lane;
   const bool in_v = c4 < p.dim_v;
-  for (int r0 = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r0 < t.rows; r0 += R * step) {
-    int64_t orow[R];
-    float4 x[R][U], acc[R];
-    float2 first[R];
-    auto slot_row = [&](int q, int i) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * t.rows + r0 + q * step; };
-    auto stats = [&](int q, bool has, int i) {
-      return has ? *reinterpret_cast<const float2*>(w.part_ml + 2 * slot_row(q, i)) : make_float2(-INFINITY, 0.f);
+  for (int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); r < t.rows; r += gridDim.y * kJoinWarps) {
+    int tok, head;
+    if (!cut.row(p, t, r, tok, head)) continue;
+    const int64_t orow = (int64_t)(seq.q0 + tok) * p.heads_q + head;
+    auto slot_row = [&](int i) { return ((int64_t)i * 2 + (i == c ? 1 : 0)) * t.rows + r; };
+    auto stats = [&](bool has, int i) {
+      return has ? *reinterpret_cast<const float2*>(w.part_ml + 2 * slot_row(i)) : make_float2(-INFINITY, 0.f);
     };
-    auto load = [&](int q, unsigned on, int i0, int i) {
+    float4 x[U];
+    auto load = [&](unsigned on, int i0, int i) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        x[q][u] = (on >> (i + u)) & 1 && in_v && orow[q] >= 0
-                      ? *reinterpret_cast<const float4*>(w.part_o + slot_row(q, i0 + i + u) * p.dim_v + c4)
-                      : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[u] = (on >> (i + u)) & 1 && in_v
+                   ? *reinterpret_cast<const float4*>(w.part_o + slot_row(i0 + i + u) * p.dim_v + c4)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
     };
+    const float2 first = stats(mine, c + lane);
+    load(parts, c, 0);  // with the statistics, not behind them
+    float m = first.x;
+    for (int i = c + 32 + lane; i <= last; i += 32) m = fmaxf(m, stats(has_part(i), i).x);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = c; i0 <= last; i0 += 32) {
+      const float2 st = i0 == c ? first : stats(has_part(i0 + lane), i0 + lane);
+      const float fi = exp2f(st.x - ref);
+      // a part without keys has no output: its maximum says so
+      const unsigned full = __ballot_sync(0xffffffffu, st.x != -INFINITY);
+      for (int i = 0; i < 32 && i0 + i <= last; i += U) {
+        if (i0 > c || i > 0) load(full, i0, i);
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      int tok, head;
-      const bool ok = r0 + q * step < t.rows && cut.row(p, t, r0 + q * step, tok, head);
-      orow[q] = ok ? (int64_t)(seq.q0 + tok) * p.heads_q + head : -1;
-      first[q] = stats(q, mine && ok, c + lane);
-      load(q, parts, c, 0);  // with the statistics, not behind them
-    }
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      if (orow[q] < 0) continue;
-      float m = first[q].x;
-      for (int i = c + 32 + lane; i <= last; i += 32) m = fmaxf(m, stats(q, has_part(i), i).x);
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float ref = m == -INFINITY ? 0.f : m;
-      float l = 0.f;
-      acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i0 = c; i0 <= last; i0 += 32) {
-        const float2 st = i0 == c ? first[q] : stats(q, has_part(i0 + lane), i0 + lane);
-        const float fi = exp2f(st.x - ref);
-        // a part without keys has no output: its maximum says so
-        const unsigned full = __ballot_sync(0xffffffffu, st.x != -INFINITY);
-        for (int i = 0; i < 32 && i0 + i <= last; i += U) {
-          if (i0 > c || i > 0) load(q, full, i0, i);
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const float f = __shfl_sync(0xffffffffu, fi, i + u);
-            l = fmaf(__shfl_sync(0xffffffffu, st.y, i + u), f, l);
-            if (!((full >> (i + u)) & 1)) continue;
-            acc[q] = make_float4(fmaf(x[q][u].x, f, acc[q].x), fmaf(x[q][u].y, f, acc[q].y), fmaf(x[q][u].z, f, acc[q].z),
-                                 fmaf(x[q][u].w, f, acc[q].w));
-          }
+        for (int u = 0; u < U; ++u) {
+          const float f = __shfl_sync(0xffffffffu, fi, i + u);
+          l = fmaf(__shfl_sync(0xffffffffu, st.y, i + u), f, l);
+          if (!((full >> (i + u)) & 1)) continue;
+          acc = make_float4(fmaf(x[u].x, f, acc.x), fmaf(x[u].y, f, acc.y), fmaf(x[u].z, f, acc.z), fmaf(x[u].w, f, acc.w));
         }
       }
-      RowEnd<T, MODE> end(p, orow[q], m, l);
-      if (in_v) {
-        const float y[4] = {acc[q].x, acc[q].y, acc[q].z, acc[q].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) end.put(p, orow[q] * p.dim_v + c4 + k, y[k]);
-      }
-      if (lane == 0) end.finish(p, orow[q]);
     }
+    RowEnd<T, MODE> end(p, orow, m, l);
+    if (in_v) end.put4(p, orow * p.dim_v + c4, acc);
+    if (lane == 0) end.finish(p, orow);
   }
 }
 
@@ -491,14 +492,8 @@ cudaError_t launch_paged_combine(const Paged& p, const TileShape& t, int ctas, i
                                  cudaStream_t s) {
   int gy = (t.rows + kJoinWarps - 1) / kJoinWarps;
   if (gy > kJoinTall) gy = kJoinTall;
-  const bool two = t.rows > gy * kJoinWarps;
-  using Join = void (*)(Paged, TileShape, int, PagedWs);
-  const Join bf16[2][2] = {{paged_join_kernel<__nv_bfloat16, kAny, 1>, paged_join_kernel<__nv_bfloat16, kAny, 2>},
-                           {paged_join_kernel<__nv_bfloat16, kAll, 1>, paged_join_kernel<__nv_bfloat16, kAll, 2>}};
-  const Join f32[2][2] = {{paged_join_kernel<float, kAny, 1>, paged_join_kernel<float, kAny, 2>},
-                          {paged_join_kernel<float, kAll, 1>, paged_join_kernel<float, kAll, 2>}};
-  const int more = t.rows > gy * kJoinWarps;
-  const Join kern = (dtype == JFA_BF16 ? bf16 : f32)[plain(p)][more];
+  auto kern = dtype == JFA_BF16 ? (plain(p) ? paged_join_kernel<__nv_bfloat16, kAll> : paged_join_kernel<__nv_bfloat16, kAny>)
+                                : (plain(p) ? paged_join_kernel<float, kAll> : paged_join_kernel<float, kAny>);
   kern<<<dim3(ctas, gy), kJoinWarps * 32, 0, s>>>(p, t, ctas, w);
   return cudaGetLastError();
 }

@@ -27,9 +27,9 @@
 // its commit PV has completed: O may then be rescaled without a further wait.
 // The row maximum is kept lazily: O and the sum are rescaled only when it grows by more
 // than 2^8.
-// Measured: 8 prompts of 1024 to 4096 tokens, 32 heads on 8 of 128, causal, bf16: 420 us, 1090
-// TFLOP/s; 13 chunks of up to 512 tokens over caches of up to 16384, 32 heads on 4, MXFP8: 457 us,
-// 980 TFLOP/s.  The prompts without any softmax take 335 us, with its TMEM loads and stores 343:
+// Measured: 8 prompts of 1024 to 4096 tokens, 32 heads on 8 of 128, causal, bf16: 412 us, 1110
+// TFLOP/s; 13 chunks of up to 512 tokens over caches of up to 16384, 32 heads on 4, MXFP8: 451 us,
+// 995 TFLOP/s.  The prompts without any softmax take 335 us, with its TMEM loads and stores 343:
 // a stream's softmax and its products follow one another, since its S and P share their columns
 // of TMEM, and both streams' tiles fill the 512.  Not faster: the weights handed over in halves
 // (433 us), two threads a row (495; they share a scheduler), the exponentials begun against an
