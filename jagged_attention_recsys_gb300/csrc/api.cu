@@ -359,7 +359,7 @@ jfa_status run_bwd(const jfa_params* p, Kind kind, int act, const void* q, const
     cudaStream_t rs = sd ? sd->s : s;
     {
       Timed t(JFA_KERNEL_BWD_D, rs);
-      st = path == 1 ? cu(launch_tc_rowstat(pr, o, dout, lse, w, rs))
+      st = path == 1 ? cu(launch_tc_rowstat(pr, q, k, v, o, dout, lse, w, rs))
                      : cu(launch_bwd_rowterm(pr, p->dtype, o, dout, w, rs));
     }
     if (sd && (cudaEventRecord(sd->join, rs) != cudaSuccess ||

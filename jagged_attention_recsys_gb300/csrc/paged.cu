@@ -17,6 +17,9 @@
 // for it unless the caller asks for a plan: each CTA scans the lengths itself (1 us of loads and
 // shuffles) and the join gathers the CTAs' statuses.  A step of four users over short caches
 // takes 24 us a call instead of 33 by that and lighter argument handling.
+//
+// A window bounds the keys of a tile, so the series has a third part, tiles of the window's and the
+// sinks' keys; a shared prefix takes groups of sequences for sequences in its first phase.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -34,6 +34,14 @@
 // rest is the consumers' latency: registers allow two CTAs an SM.  With scores of three times the
 // spread nearly every stage takes its values to bf16: 228 us (weights scaled in bf16 against codes
 // in bf16 instead: 222 us, but 189 us for scores of the usual spread).
+//
+// Windows and shared prefixes are instances of their own (MODE).  A tile under a window walks the blocks
+// that hold its rows' windows and the sinks'; boxes in front of them are not looked up, and what such a
+// block holds in front of the window is cleaned, a stage at a time, by the warps that use it.  One token
+// for each of 256 users, histories to 8,192, window 1,024 and 4 sinks, 32 heads on 8: 178 us, 5.7 TB/s, 85%.
+// Of a shared prefix this is phase 1 where groups have few rows, and phase 2 over the sequences' own
+// keys: 128 continuations over up to 1,024 MXFP8 keys each, 32 heads on 4: 42 us; phase 1's results are
+// asked for ahead of the join of the four warps.
 #pragma once
 
 #include <cuda.h>

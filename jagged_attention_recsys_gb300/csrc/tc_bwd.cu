@@ -21,6 +21,12 @@
 // The SiLU/L variant has no lse and no D: P = SiLU(u)/L and
 // dS = dP SiLU'(u)/L with u = scale s.  Masking is by subtraction as in the
 // forward; masked (query, key) pairs contribute exact zeros.
+//
+// Windows (WIN instances).  A key tile's rows are one stretch from its own first row on, a query
+// tile's keys the blocks of the forward.  96 histories of 1 to 4,096 rows, 8 heads of 128, window 512, 4
+// sinks: dQ 564 us, 1,900 cycles a step, of which the MMAs take 1,536; dK/dV 965 us, 3,400 cycles a step for
+// MMAs of 2,048: P and dS pass through registers between them.  The sinks cost 62 and 97 us: a tile of
+// keys that all rows meet, though they see 4 of it.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -98,6 +104,100 @@ rowstat_kernel(int64_t total, int heads, const __nv_bfloat16* __restrict__ o,
       rowstat[(int64_t)h * total + t] = make_float2(lse[row] * kLog2e, acc);
     }
   }
+}
+
+// Rows under a window that see at most kFewKeys keys: D = sum_j P_ij <dO_i, v_j> from the scores instead of
+// <dO_i, O_i>.  O is rounded to bf16, and with few keys it is as large as the values, so its rounding makes
+// up the larger part of D's error and, since dS = P (dP - D), of the gradients' (2-norm: a window of 2 keys
+// 3.9e-3, 2.4e-3 with this; of 10, 2.5e-3 and 2.4e-3; what remains is the rounding of dS and of the results).
+// Those are the first rows of every sequence, and all rows where window and sinks are that few.
+//
+// A warp takes 16 rows of a head.  Their keys are the 16 in front of them, their own 16, and the
+// sinks: six tiles of 8 keys on mma.sync, its operands straight from global memory, with the columns of
+// the contraction in an order that gives a lane 16 bytes of a row at a time.
+constexpr int kFewKeys = 16;
+
+__device__ __forceinline__ void mma_few(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int DQK, int DV>
+__global__ void __launch_bounds__(128)
+window_rowstat_kernel(const Problem p, const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
+                      const __nv_bfloat16* __restrict__ v, const __nv_bfloat16* __restrict__ dout,
+                      const float* __restrict__ lse, float2* __restrict__ rowstat) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, H = p.heads;
+  const bool all = (int64_t)p.window + p.sinks <= kFewKeys;
+  const float c = p.scale * kLog2e;
+  for (int64_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
+    const int64_t lo = __ldg(p.offs_q + b), hi = __ldg(p.offs_q + b + 1);
+    if (lo < 0 || hi <= lo || hi > p.total_q) continue;  // no rows, or no batch
+    const int len = (int)(hi - lo);
+    const int64_t items = (int64_t)(all ? (len + 15) / 16 : 1) * H;
+    for (int64_t item = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 5); item < items; item += (int64_t)gridDim.y * 4) {
+      const int h = (int)(item % H), r0 = (int)(item / H) * 16;
+      // 8 columns at 8 t of every 32 of a row (rows outside the sequence: another of its rows, masked below)
+      auto row = [&](const __nv_bfloat16* x, int r, int dim) {
+        return reinterpret_cast<const uint4*>(x + ((lo + min(max(r, 0), len - 1)) * H + h) * dim + 8 * t);
+      };
+      uint4 a[2][DQK / 32], e[2][DV / 32];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int i = 0; i < DQK / 32; ++i) a[x][i] = __ldg(row(q, r0 + g + 8 * x, DQK) + 4 * i);
+#pragma unroll
+        for (int i = 0; i < DV / 32; ++i) e[x][i] = __ldg(row(dout, r0 + g + 8 * x, DV) + 4 * i);
+      }
+      float l2[2], d[2] = {0.f, 0.f};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) l2[x] = __ldg(lse + (lo + min(r0 + g + 8 * x, len - 1)) * H + h) * kLog2e;
+#pragma unroll
+      for (int n = 0; n < 6; ++n) {
+        const int k0 = n < 4 ? r0 - 16 + 8 * n : 8 * (n - 4);  // the rows' keys, then sinks in front of those
+        if (n < 4 ? k0 < 0 || k0 >= len : k0 >= min(p.sinks, r0 - 16)) continue;
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, dp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < DQK / 32; ++i) {
+          const uint4 y = __ldg(row(k, k0 + g, DQK) + 4 * i);
+          mma_few(s, a[0][i].x, a[1][i].x, a[0][i].y, a[1][i].y, y.x, y.y);
+          mma_few(s, a[0][i].z, a[1][i].z, a[0][i].w, a[1][i].w, y.z, y.w);
+        }
+#pragma unroll
+        for (int i = 0; i < DV / 32; ++i) {
+          const uint4 y = __ldg(row(v, k0 + g, DV) + 4 * i);
+          mma_few(dp, e[0][i].x, e[1][i].x, e[0][i].y, e[1][i].y, y.x, y.y);
+          mma_few(dp, e[0][i].z, e[1][i].z, e[0][i].w, e[1][i].w, y.z, y.w);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int i = r0 + g + 8 * (x >> 1), j = k0 + 2 * t + (x & 1);
+          const bool sees = n < 4 ? j <= i && (i - j < p.window || j < p.sinks) : j < min(p.sinks, r0 - 16);
+          d[x >> 1] += sees ? ex2(s[x] * c - l2[x >> 1]) * dp[x] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        d[x] += __shfl_xor_sync(0xffffffffu, d[x], 1);
+        d[x] += __shfl_xor_sync(0xffffffffu, d[x], 2);
+        const int i = r0 + g + 8 * x;
+        if (t == 0 && i < len) rowstat[(int64_t)h * p.total_q + lo + i].y = d[x];
+      }
+    }
+  }
+}
+
+template <int DQK, int DV>
+void launch_window_rowstat(const Problem& p, const void* q, const void* k, const void* v, const void* dout, const float* lse,
+                           float2* rs, cudaStream_t s) {
+  const bool all = (int64_t)p.window + p.sinks <= kFewKeys;
+  const int64_t most = (int64_t)num_sms() * 16, x = p.batch < most ? p.batch : most;
+  const int64_t need = ((all ? p.total_q / p.batch / 16 + 1 : 1) * p.heads + 3) / 4, room = most / x;
+  const int64_t y = need < room ? need : room;
+  window_rowstat_kernel<DQK, DV><<<dim3((unsigned)x, (unsigned)y), 128, 0, s>>>(
+      p, (const __nv_bfloat16*)q, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, (const __nv_bfloat16*)dout, lse, rs);
 }
 
 // Shared pieces ---------------------------------------------------------------
@@ -1569,8 +1669,8 @@ cudaError_t dq_t(const Maps& m, const Problem& p, const float2* rowstat, void* d
 // q-list: 128-row tiles over 128-key steps (dQ); k-list: 128-key tiles over 128-row steps (dK/dV)
 SchedConfig tc_bwd_sched(const Problem&) { return SchedConfig{TILE, STEP, TILE, KSTEP, 1, 1, 0}; }
 
-cudaError_t launch_tc_rowstat(const Problem& p, const void* o, const void* dout, const float* lse,
-                              const Workspace& ws, cudaStream_t s) {
+cudaError_t launch_tc_rowstat(const Problem& p, const void* q, const void* k, const void* v, const void* o,
+                              const void* dout, const float* lse, const Workspace& ws, cudaStream_t s) {
   const int64_t threads = p.total_q * p.heads * (p.dim_v / 8);
   if (threads == 0) return cudaSuccess;
   int64_t blocks = (threads + 255) / 256;  // one pass; the loop covers grids past the cap
@@ -1583,6 +1683,12 @@ cudaError_t launch_tc_rowstat(const Problem& p, const void* o, const void* dout,
   else
     rowstat_kernel<64><<<(unsigned)blocks, 256, 0, s>>>(p.total_q, p.heads, (const __nv_bfloat16*)o,
                                                         (const __nv_bfloat16*)dout, lse, rs);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.window == 0 || p.batch == 0) return e;
+  if (p.dim_qk == 128 && p.dim_v == 128) launch_window_rowstat<128, 128>(p, q, k, v, dout, lse, rs, s);
+  else if (p.dim_qk == 128) launch_window_rowstat<128, 64>(p, q, k, v, dout, lse, rs, s);
+  else if (p.dim_v == 128) launch_window_rowstat<64, 128>(p, q, k, v, dout, lse, rs, s);
+  else launch_window_rowstat<64, 64>(p, q, k, v, dout, lse, rs, s);
   return cudaGetLastError();
 }
 

@@ -31,6 +31,15 @@
 // subtract a finite shift from masked columns, keep an online max with lazy
 // rescaling of O (only when it grows by more than 2^8), take exp2 and the row
 // sum, and write P.  Epilogue: O / l -> bf16, lse = (m + log2 l) ln 2.
+//
+// Windows (WIN instances).  A tile's steps are the key blocks that its rows' windows reach and the
+// sinks' in front of them, so a row's work no longer grows with its sequence.  Bound: the softmax
+// warps, 1,640 cycles a step, of which the MMAs take 1,024; a third of the pairs of a window of 512 are
+// hidden.  96 histories of 1 to 4,096 rows, 8 heads of 128, window 512, 4 sinks: 535 us, 54 of them for
+// the sinks' block (the visible pairs alone are 231 us of MMAs), with the lists' launch 549; window 128: 387,
+// window 2,048: 932.  Masks by bits instead of comparisons took it from 659.  Not faster: stretches that
+// no row of a warp sees without exponentials (561; window 2,048 993: the branch costs whole blocks more
+// than it spares), the output through shared memory and TMA (541, but short windows up to 40% slower).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
