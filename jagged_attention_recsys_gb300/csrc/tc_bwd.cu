@@ -110,12 +110,18 @@ rowstat_kernel(int64_t total, int heads, const __nv_bfloat16* __restrict__ o,
 // <dO_i, O_i>.  O is rounded to bf16, and with few keys it is as large as the values, so its rounding makes
 // up the larger part of D's error and, since dS = P (dP - D), of the gradients' (2-norm: a window of 2 keys
 // 3.9e-3, 2.4e-3 with this; of 10, 2.5e-3 and 2.4e-3; what remains is the rounding of dS and of the results).
-// Those are the first rows of every sequence, and all rows where window and sinks are that few.
+// Those are the first rows of every sequence, and all rows where window and sinks are that few: this is
+// then the whole row pass.
 //
 // A warp takes 16 rows of a head.  Their keys are the 16 in front of them, their own 16, and the
 // sinks: six tiles of 8 keys on mma.sync, its operands straight from global memory, with the columns of
-// the contraction in an order that gives a lane 16 bytes of a row at a time.
+// the contraction in an order that gives a lane 16 bytes of a row at a time.  Bound: HBM, Q, K, V and dO are
+// read once more.  96 histories of 1 to 4,096 rows, 8 heads of 128: 5.6 us for their first rows, 372 us for all
+// (4.3 TB/s; the pass over O and dO takes 140).
 constexpr int kFewKeys = 16;
+__host__ __device__ __forceinline__ bool few_keys(const Problem& p) {  // no row sees more
+  return p.window > 0 && (int64_t)p.window + p.sinks <= kFewKeys;
+}
 
 __device__ __forceinline__ void mma_few(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -130,7 +136,7 @@ window_rowstat_kernel(const Problem p, const __nv_bfloat16* __restrict__ q, cons
                       const __nv_bfloat16* __restrict__ v, const __nv_bfloat16* __restrict__ dout,
                       const float* __restrict__ lse, float2* __restrict__ rowstat) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, H = p.heads;
-  const bool all = (int64_t)p.window + p.sinks <= kFewKeys;
+  const bool all = few_keys(p);
   const float c = p.scale * kLog2e;
   for (int64_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
     const int64_t lo = __ldg(p.offs_q + b), hi = __ldg(p.offs_q + b + 1);
@@ -183,7 +189,7 @@ window_rowstat_kernel(const Problem p, const __nv_bfloat16* __restrict__ q, cons
         d[x] += __shfl_xor_sync(0xffffffffu, d[x], 1);
         d[x] += __shfl_xor_sync(0xffffffffu, d[x], 2);
         const int i = r0 + g + 8 * x;
-        if (t == 0 && i < len) rowstat[(int64_t)h * p.total_q + lo + i].y = d[x];
+        if (t == 0 && i < len) rowstat[(int64_t)h * p.total_q + lo + i] = make_float2(l2[x], d[x]);
       }
     }
   }
@@ -192,7 +198,7 @@ window_rowstat_kernel(const Problem p, const __nv_bfloat16* __restrict__ q, cons
 template <int DQK, int DV>
 void launch_window_rowstat(const Problem& p, const void* q, const void* k, const void* v, const void* dout, const float* lse,
                            float2* rs, cudaStream_t s) {
-  const bool all = (int64_t)p.window + p.sinks <= kFewKeys;
+  const bool all = few_keys(p);
   const int64_t most = (int64_t)num_sms() * 16, x = p.batch < most ? p.batch : most;
   const int64_t need = ((all ? p.total_q / p.batch / 16 + 1 : 1) * p.heads + 3) / 4, room = most / x;
   const int64_t y = need < room ? need : room;
@@ -1673,16 +1679,18 @@ cudaError_t launch_tc_rowstat(const Problem& p, const void* q, const void* k, co
                               const void* dout, const float* lse, const Workspace& ws, cudaStream_t s) {
   const int64_t threads = p.total_q * p.heads * (p.dim_v / 8);
   if (threads == 0) return cudaSuccess;
-  int64_t blocks = (threads + 255) / 256;  // one pass; the loop covers grids past the cap
-  const int64_t cap = (int64_t)1 << 30;
-  if (blocks > cap) blocks = cap;
   float2* rs = reinterpret_cast<float2*>(ws.drow);
-  if (p.dim_v == 128)
-    rowstat_kernel<128><<<(unsigned)blocks, 256, 0, s>>>(p.total_q, p.heads, (const __nv_bfloat16*)o,
-                                                         (const __nv_bfloat16*)dout, lse, rs);
-  else
-    rowstat_kernel<64><<<(unsigned)blocks, 256, 0, s>>>(p.total_q, p.heads, (const __nv_bfloat16*)o,
-                                                        (const __nv_bfloat16*)dout, lse, rs);
+  if (!few_keys(p)) {
+    int64_t blocks = (threads + 255) / 256;  // one pass; the loop covers grids past the cap
+    const int64_t cap = (int64_t)1 << 30;
+    if (blocks > cap) blocks = cap;
+    if (p.dim_v == 128)
+      rowstat_kernel<128><<<(unsigned)blocks, 256, 0, s>>>(p.total_q, p.heads, (const __nv_bfloat16*)o,
+                                                           (const __nv_bfloat16*)dout, lse, rs);
+    else
+      rowstat_kernel<64><<<(unsigned)blocks, 256, 0, s>>>(p.total_q, p.heads, (const __nv_bfloat16*)o,
+                                                          (const __nv_bfloat16*)dout, lse, rs);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.window == 0 || p.batch == 0) return e;
   if (p.dim_qk == 128 && p.dim_v == 128) launch_window_rowstat<128, 128>(p, q, k, v, dout, lse, rs, s);
