@@ -116,8 +116,9 @@ rowstat_kernel(int64_t total, int heads, const __nv_bfloat16* __restrict__ o,
 // A warp takes 16 rows of a head.  Their keys are the 16 in front of them, their own 16, and the
 // sinks: six tiles of 8 keys on mma.sync, its operands straight from global memory, with the columns of
 // the contraction in an order that gives a lane 16 bytes of a row at a time.  Bound: HBM, Q, K, V and dO are
-// read once more.  96 histories of 1 to 4,096 rows, 8 heads of 128: 5.6 us for their first rows, 372 us for all
-// (4.3 TB/s; the pass over O and dO takes 140).
+// read once more.  96 histories of 1 to 4,096 rows, 8 heads of 128: 5.6 us for their first rows, 284 us for all
+// under a window of 16 (5.7 TB/s; the pass over O and dO takes 140), 302 with four sinks.  The grid is many
+// times what the GPU holds, since sequences differ in length (a fourth of it: 372).
 constexpr int kFewKeys = 16;
 __host__ __device__ __forceinline__ bool few_keys(const Problem& p) {  // no row sees more
   return p.window > 0 && (int64_t)p.window + p.sinks <= kFewKeys;
@@ -199,7 +200,7 @@ template <int DQK, int DV>
 void launch_window_rowstat(const Problem& p, const void* q, const void* k, const void* v, const void* dout, const float* lse,
                            float2* rs, cudaStream_t s) {
   const bool all = few_keys(p);
-  const int64_t most = (int64_t)num_sms() * 16, x = p.batch < most ? p.batch : most;
+  const int64_t most = (int64_t)num_sms() * 64, x = p.batch < most ? p.batch : most;
   const int64_t need = ((all ? p.total_q / p.batch / 16 + 1 : 1) * p.heads + 3) / 4, room = most / x;
   const int64_t y = need < room ? need : room;
   window_rowstat_kernel<DQK, DV><<<dim3((unsigned)x, (unsigned)y), 128, 0, s>>>(
