@@ -138,3 +138,63 @@ def test_plans_of_another_window():
             assert bool((whole[:pad] == 7).all()) and bool((whole[-pad:] == 7).all())
         o, lse = jfa.jfa_paged_window_fwd(pq, *b.args(), 77, sinks=2, ws=pws)
         wref.compare(f64(o), f64(lse), want(b, pq, hq, 77, 2), 128, int(b.lens_h.max()), "bf16")
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("bf16", "mxfp8"), ("f32", "f32")])
+@pytest.mark.parametrize("new", [1, 3, 200])
+def test_the_longest_cache(dtype, cache, new):
+    """The last positions of a cache as long as calls allow: tokens appended there, and attended under a window
+    whose pages alone are in the table."""
+    page, hk, hq, d, window, sinks = 256, 2, 8, 64, 100, 5
+    width = (2 ** 31 - 256) // page
+    n = width * page  # 2^31 - 256
+    c = jfa.paged_cache(5, hk, d, page_size=page, dtype=DT[dtype], mxfp8=cache == "mxfp8")
+    dev = lambda x: torch.tensor(x, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(new)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(DT[dtype])
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    table[0, 0], table[0, -2], table[0, -1] = 3, 0, 4
+    # the first page and the last two as a sequence of their own, filled; then the new tokens over its end
+    short = table[:, [0, -2, -1]].contiguous()
+    m = 3 * page
+    jfa.jfa_cache_write(r(m, hk, d), r(m, hk, d), c, short, dev([0, m]), dev([m]))
+    q, k, v = r(new, hq, d), r(new, hk, d), r(new, hk, d)
+    ws = jfa.paged_workspace(jfa.paged_params(c, table, dev([0, new]), dev([n]), new, DT[dtype], heads_q=hq))
+    q, _ = jfa.jfa_rope_append(q, k, v, c, table, dev([0, new]), dev([n]), norm=False, rope=jfa.jfa_rope(d), ws=ws)
+    assert jfa.jfa_status_check(ws) == jfa.JFA_OK
+    kr, vr = jfa.jfa_cache_read(c, short, dev([0, m]), dev([m]), m, dtype=DT[dtype])
+    assert torch.equal(vr[m - new:], v) or cache == "mxfp8"
+    at = np.concatenate([np.arange(page), np.arange(n - 2 * page, n)])
+    see = wref.window_mask(np.arange(n - new, n), at, window, sinks)
+    want = wref.attend(f64(q), [(0, f64(kr).transpose(1, 0, 2), f64(vr).transpose(1, 0, 2), see)], hq // hk,
+                       float(np.float32(d ** -0.5)), d)
+    for planned in (False, True):
+        if planned:
+            jfa.jfa_paged_window_plan(q, c, table, dev([0, new]), dev([n]), window, sinks=sinks, ws=ws)
+        o, lse = jfa.jfa_paged_window_fwd(q, c, table, dev([0, new]), dev([n]), window, sinks=sinks, ws=ws, planned=planned)
+        assert jfa.jfa_status_check(ws) == jfa.JFA_OK
+        wref.compare(f64(o), f64(lse), want, d, m, dtype)
+
+
+def test_tables_without_pages():
+    """Groups without prefixes, sequences without keys of their own, and neither."""
+    b = Shared([2, 3], [70, 33], [1, 2, 1, 20, 3], [5, 9, 1, 20, 40], 2, 64, 64, 16, "bf16", "bf16")
+    q = queries(b, 4)
+    c, table, offs, lens = b.own
+    none = lambda n: torch.empty(n, 0, dtype=torch.int32, device="cuda")
+    zeros = lambda n: torch.zeros(n, dtype=torch.int64, device="cuda")
+    o, lse = jfa.jfa_shared_fwd(q, c, table, offs, lens, none(2), zeros(2), b.groups)
+    o2, lse2 = jfa.jfa_paged_fwd(q, c, table, offs, lens)
+    assert float((o.float() - o2.float()).abs().max()) <= 2.0 ** -5 and torch.allclose(lse, lse2, atol=1e-5)
+    o, lse = jfa.jfa_shared_fwd(q, c, none(5), offs, zeros(5), b.prefix_table, b.prefix_lens, b.groups)
+    scale, seqs = float(np.float32(64 ** -0.5)), []
+    for x in range(5):
+        g = int(x >= 2)
+        n, m = int(b.new[x]), int(b.lens_h[b.S + g])
+        seqs.append((int(b.offs_h[x]), b.k_of(b.S + g), b.v_of(b.S + g), np.ones((n, m), bool)))
+    wref.compare(f64(o), f64(lse), wref.attend(f64(q), seqs, 2, scale, 64), 64, 100, "bf16")
+    o, lse = jfa.jfa_shared_fwd(q, c, none(5), offs, zeros(5), none(2), zeros(2), b.groups)
+    assert bool((o == 0).all()) and bool((lse == -float("inf")).all())
+    # a window over sequences without pages
+    o, lse = jfa.jfa_paged_window_fwd(q, c, none(5), offs, zeros(5), 7, sinks=1)
+    assert bool((o == 0).all()) and bool((lse == -float("inf")).all())
