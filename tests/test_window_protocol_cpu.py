@@ -1,5 +1,6 @@
-"""Parts of the paged attention's 128-row kernel (`csrc/paged_tc.cuh`) on the CPU.  Its loader asks for a tile's
-queries behind the tile's first keys: the whole kernel's model with that order.  And under a window:
+"""Parts of the paged attention's 128-row kernel (`csrc/paged_tc.cuh`) on the CPU.  Over bf16 pages its loader
+asks for a tile's queries behind the tile's first keys: the whole kernel's model with that order (over MXFP8
+the queries go first, as in the model itself).  And under a window:
 
 The ring of the paged attention's 128-row kernel under a window (`csrc/paged_tc.cuh`), on the CPU: tiles of
 values of which some keys are hidden from every row, the sinks' block and the window's first among them,
@@ -126,7 +127,7 @@ RING = '''                for kv in (0, 1):
 
 
 def with_keys_first():
-    """The model of the kernel with the loader's new order."""
+    """The model of the kernel with the loader's order over bf16 pages."""
     source = inspect.getsource(model.play_tc)
     assert source.count(QUERIES) == 1 and source.count(RING) == 1
     late = " " * 20 + "if d == 0 and kv == 1:\n" + "".join(" " * 12 + line + "\n" for line in QUERIES.splitlines())
@@ -138,7 +139,7 @@ def with_keys_first():
     return space["play_tc"]
 
 
-@pytest.mark.parametrize("stages,raws", [(5, 0), (8, 0), (3, 3), (6, 3)])
+@pytest.mark.parametrize("stages,raws", [(5, 0), (8, 0)])
 def test_queries_behind_the_first_keys(stages, raws):
     play_tc = with_keys_first()
     rng = random.Random(stages + 100)
