@@ -170,7 +170,7 @@ jfa_status jfa_bwd(const jfa_params* p, const void* q, const void* k, const void
  * jfa_window_plan builds the lists of both calls for one window and its sinks (JFA_PLANNED, as by
  * jfa_plan; a plan of another window or of jfa_plan gives wrong results, within the buffers' bounds).
  * Values of keys that a row's window hides have to be finite and at most 2^120 in size; their scores
- * count for nothing, whatever they are.  In bf16 at dims of 64 and 128, <dO, O> of rows that see at most
+ * count for nothing, whatever they are and however low the seen ones lie.  In bf16 at dims of 64 and 128, <dO, O> of rows that see at most
  * 16 keys is worked out from q, k, v and lse, not from the rounded o.
  */
 jfa_status jfa_window_plan(const jfa_params* p, int32_t window, int32_t sinks, const int64_t* offs,

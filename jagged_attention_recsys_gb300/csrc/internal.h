@@ -19,6 +19,8 @@ constexpr int kActSiluOverLen = 1;
 // (the "subtraction instead of -inf masking" of the Jagged Flash Attention
 // bullet, Meta GEM MFU write-up, piletech.kr/articles/112134, details).
 // The same shift drives SiLU(u - shift) to (-)0 for the non-softmax variant.
+// Windows do without it: their first blocks may hold no key that a row sees, so
+// that no finite score lies below the row's; hidden scores are -inf there.
 constexpr float kMaskShift = 1048576.0f;  // 2^20
 
 // One unit of work produced by the jagged tile scheduler: (sequence b, head h,

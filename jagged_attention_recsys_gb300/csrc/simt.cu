@@ -6,7 +6,7 @@
 // CTAs walk the scheduler's heavy-first work lists; the forward keeps an
 // online softmax (running maximum and sum, exp2 of log2-scaled scores);
 // masked scores are shifted down by a finite constant rather than set to
-// -inf; the backward is two atomic-free passes (key-tile-major for dK/dV,
+// -inf (but under windows); the backward is two atomic-free passes (key-tile-major for dK/dV,
 // query-tile-major for dQ) after a row-term pass D_i = <dO_i, O_i>.
 //
 // Under a window the loops run over the blocks that a tile's rows see.  Four histories of up to 300 rows,
@@ -64,8 +64,9 @@ __device__ __forceinline__ bool in_window(const Problem& p, int i, int j) {
   return p.window == 0 || i - j < p.window || j < p.sinks;
 }
 
-// A hidden pair's score: under a window of the constant alone, so that none of any size counts.
-__device__ __forceinline__ float masked(const Problem& p, float s) { return (p.window > 0 ? 0.f : s) - kMaskShift; }
+// A hidden pair's score: shifted down, or under a window, whose first blocks may hide all their keys from a row,
+// below any score.
+__device__ __forceinline__ float masked(const Problem& p, float s) { return p.window > 0 ? -INFINITY : s - kMaskShift; }
 
 template <typename T, int DQ, int DV>
 struct SimtFwdSmem {
@@ -133,8 +134,9 @@ simt_fwd_kernel(Problem p, const T* __restrict__ q, const T* __restrict__ k,
         float pj;
         if (p.act == kActSoftmax) {
           const float mn = fmaxf(m[rr], warp_max(s));
-          const float alpha = exp2f(m[rr] - mn);
-          pj = exp2f(s - mn);
+          const float ref = mn == -INFINITY ? 0.f : mn;  // no key seen so far
+          const float alpha = exp2f(m[rr] - ref);
+          pj = exp2f(s - ref);
           l[rr] = l[rr] * alpha + warp_sum(pj);
           m[rr] = mn;
 #pragma unroll

@@ -826,7 +826,7 @@ tc_dkdv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             for (int c = 0; c < HC; c += 32) {
               const uint32_t bits = window_bits(c, lo, 0, hi);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : -shift_raw;
+              for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : -INFINITY;
             }
           }
         } else if (lo > 0 || hi < HC) {
@@ -1471,14 +1471,14 @@ tc_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         if (p.block_mask > 0 && (kb ^ i) >= p.block_mask) nvalid = 0;  // another block's keys
         if (!row_ok) nvalid = 0;
         if (WIN) {
-          // the row's window, and the sinks (a hidden score is replaced)
+          // the row's window, and the sinks: a hidden score becomes -inf, its weight 0 whatever lse is
           const int from = max(i - p.window + 1, 0) - kb, front = p.sinks - kb;
           if (nvalid < HC || (from > 0 && front < HC)) {
 #pragma unroll
             for (int c = 0; c < HC; c += 32) {
               const uint32_t bits = window_bits(c, from, front, nvalid);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : -shift_raw;
+              for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : -INFINITY;
             }
           }
         } else if (nvalid < HC) {

@@ -461,16 +461,15 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (CAUSAL) nvalid = min(nvalid, i - kb + 1);
         if (p.block_mask > 0 && (kb ^ i) >= p.block_mask) nvalid = 0;  // another block's keys
         if (WIN) {
-          // the row's window, and the sinks.  A hidden score is replaced, so that none of any size counts.  A
-          // first block that the row sees nothing of leaves weights that the next rescaling, by
-          // exp2(-2^20) = 0, takes back: every row sees its own key, in the last block.
+          // the row's window, and the sinks.  A hidden score becomes -inf and not one shifted down: blocks that
+          // a row sees nothing of may come first, so no finite number is below all that it will see.
           const int from = max(i - p.window + 1, 0) - kb, front = p.sinks - kb;
           if (nvalid < HC || (from > 0 && front < HC)) {
 #pragma unroll
             for (int c = 0; c < HC; c += 32) {
               const uint32_t bits = window_bits(c, from, front, nvalid);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : -shift_raw;
+              for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : -INFINITY;
             }
           }
         } else if (nvalid < HC) {
@@ -507,7 +506,8 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         // P = exp2(s c - m) or SiLU(s c)/L as packed bf16 pairs
         const float2 cc = make_float2(c_score, c_score);
-        const float2 nm = make_float2(-m, -m);
+        const float ref = WIN && m == -INFINITY ? 0.f : m;  // no key seen so far: weights of exp2(-inf)
+        const float2 nm = make_float2(-ref, -ref);
         const float2 hc = make_float2(0.5f * c_score, 0.5f * c_score);
         const float2 il = make_float2(inv_len, inv_len);
         float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
