@@ -144,7 +144,11 @@ jfa_status jfa_block_plan(const jfa_params* p, const int64_t* offs, void* ws, si
 /*
  * Softmax self-attention forward (Jagged Flash Attention bullet).  One offsets
  * array serves queries and keys (total_k must equal total_q).  Writes O and lse.
- * Causal masking is allowed.
+ * Causal masking is allowed.  Inputs have to be finite.  Hidden scores are shifted
+ * down by 2^20 in log2 units, not replaced: a row's largest score may lie at most
+ * that far below any score of its tiles with hidden keys, neighbouring sequences'
+ * and the 0 of what lies behind the last row among them (jfa_window_fwd has no such
+ * bound).
  */
 jfa_status jfa_fwd(const jfa_params* p, const void* q, const void* k, const void* v,
                    const int64_t* offs, void* o, float* lse, void* ws, size_t ws_bytes,
@@ -154,7 +158,9 @@ jfa_status jfa_fwd(const jfa_params* p, const void* q, const void* k, const void
  * Softmax self-attention backward, without atomics (Jagged Flash Attention
  * bullet): a key-tile-major pass writes dK and dV, a query-tile-major pass
  * writes dQ, each output element is written exactly once.  o and lse are the
- * outputs of jfa_fwd on the same inputs; dout is dL/dO.
+ * outputs of jfa_fwd on the same inputs; dout is dL/dO.  <dO_i, v_j> has to stay
+ * in fp32's range for hidden pairs too, and for rows and keys of neighbouring
+ * sequences (jfa_window_bwd has no such bound).
  */
 jfa_status jfa_bwd(const jfa_params* p, const void* q, const void* k, const void* v,
                    const void* o, const float* lse, const void* dout, const int64_t* offs,
@@ -169,9 +175,10 @@ jfa_status jfa_bwd(const jfa_params* p, const void* q, const void* k, const void
  * that a sequence's grows with its length and not with its square.  Every row sees its own key.
  * jfa_window_plan builds the lists of both calls for one window and its sinks (JFA_PLANNED, as by
  * jfa_plan; a plan of another window or of jfa_plan gives wrong results, within the buffers' bounds).
- * Values of keys that a row's window hides have to be finite and at most 2^120 in size; their scores
- * count for nothing, whatever they are and however low the seen ones lie.  In bf16 at dims of 64 and 128, <dO, O> of rows that see at most
- * 16 keys is worked out from q, k, v and lse, not from the rounded o.
+ * Queries, keys, values and gradients have to be finite; a key that a row's window hides may be of any size,
+ * and so may its value: neither its score nor <dO, v> counts, however low the seen scores lie.  In bf16 at
+ * dims of 64 and 128, <dO, O> of rows that see at most 16 keys is worked out from q, k, v and lse, not from
+ * the rounded o.
  */
 jfa_status jfa_window_plan(const jfa_params* p, int32_t window, int32_t sinks, const int64_t* offs,
                            void* ws, size_t ws_bytes, jfa_stream_t stream);

@@ -208,6 +208,31 @@ void launch_window_rowstat(const Problem& p, const void* q, const void* k, const
 }
 
 // Shared pieces ---------------------------------------------------------------
+// Under a window a hidden pair's dP may be past fp32, and its weight of 0 times that is NaN and no 0.  Blocks with
+// hidden pairs look after them: dK/dV, which has the weights in bf16 at hand, clears dS where they are 0, and dQ
+// looks for the NaN that dS then holds.  64 sequences of up to 3,000 rows, 8 heads of 128, window 512, 4 sinks: dK/dV 589 us
+// (without 566; by the mask's bits 592, by a search 667), dQ 298 (291; by the weights 323).
+// Ones in the halves of a word of two bf16 that are not 0 (NaN is not).
+__device__ __forceinline__ uint32_t nonzero_halves(uint32_t w) {
+  uint32_t m;
+  asm("set.neu.u32.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(w), "r"(0u));
+  return m;
+}
+// Whether one of 2 N bf16 that were converted from fp32 is NaN: 0x7fff, the largest of 16-bit integers.
+template <int N>
+__device__ __forceinline__ bool has_nan(const uint32_t (&w)[N]) {
+  static_assert(N % 2 == 0, "two words at a time");
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) m = __vimax3_s16x2(m, w[i], w[i + 1]);
+  return (int16_t)m > 0x7f80 || (int32_t)m >> 16 > 0x7f80;
+}
+// Zeros for the pairs of 32 columns that are hidden.
+__device__ __forceinline__ void hide_pairs(uint32_t* w, uint32_t bits) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    w[i] &= ((bits >> (2 * i)) & 1 ? 0xffffu : 0u) | ((bits >> (2 * i + 1)) & 1 ? 0xffff0000u : 0u);
+}
 __device__ __forceinline__ void store_row_bf16(__nv_bfloat16* dst, const float* x, float f) {
   store32_bf16(dst, x, f);
 }
@@ -820,8 +845,9 @@ tc_dkdv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         int hi = j < Lk ? Lq - i0 : 0;
         if (p.block_mask > 0 && (j ^ i0) >= p.block_mask) hi = 0;  // another block's queries
         if (WIN && j >= p.sinks) hi = min(hi, j - i0 + p.window);
+        const bool cut = lo > 0 || hi < HC;  // some pairs are hidden
         if (WIN) {
-          if (lo > 0 || hi < HC) {
+          if (cut) {
 #pragma unroll
             for (int c = 0; c < HC; c += 32) {
               const uint32_t bits = window_bits(c, lo, 0, hi);
@@ -829,7 +855,7 @@ tc_dkdv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
               for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : -INFINITY;
             }
           }
-        } else if (lo > 0 || hi < HC) {
+        } else if (cut) {
 #pragma unroll
           for (int c = 0; c < HC; ++c) sv[c] -= (c >= lo && c < hi) ? 0.f : shift_raw;
         }
@@ -880,6 +906,10 @@ tc_dkdv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
               const float2 ds = fmul2(make_float2(pf[h + c], pf[h + c + 1]), t);
               dk2[(h + c) / 2] = pack_bf16(ds.x, ds.y);
               pk[(h + c) / 2] = pack_bf16(pf[h + c], pf[h + c + 1]);
+            }
+            if (cut) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) dk2[(h + c) / 2] &= nonzero_halves(pk[(h + c) / 2]);
             }
           }
         }
@@ -1470,10 +1500,11 @@ tc_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         if (CAUSAL) nvalid = min(nvalid, i - kb + 1);
         if (p.block_mask > 0 && (kb ^ i) >= p.block_mask) nvalid = 0;  // another block's keys
         if (!row_ok) nvalid = 0;
+        // the row's window, and the sinks
+        const int from = WIN ? max(i - p.window + 1, 0) - kb : 0, front = WIN ? p.sinks - kb : 0;
+        const bool cut = nvalid < HC || (WIN && from > 0 && front < HC);  // some pairs are hidden
         if (WIN) {
-          // the row's window, and the sinks: a hidden score becomes -inf, its weight 0 whatever lse is
-          const int from = max(i - p.window + 1, 0) - kb, front = p.sinks - kb;
-          if (nvalid < HC || (from > 0 && front < HC)) {
+          if (cut) {  // a hidden score becomes -inf, its weight 0 whatever lse is
 #pragma unroll
             for (int c = 0; c < HC; c += 32) {
               const uint32_t bits = window_bits(c, from, front, nvalid);
@@ -1481,7 +1512,7 @@ tc_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
               for (int k = 0; k < 32; ++k) sv[c + k] = (bits >> k) & 1 ? sv[c + k] : -INFINITY;
             }
           }
-        } else if (nvalid < HC) {
+        } else if (cut) {
 #pragma unroll
           for (int c = 0; c < HC; ++c) sv[c] -= c < nvalid ? 0.f : shift_raw;
         }
@@ -1535,6 +1566,10 @@ tc_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
           } else {  // dP rounded to bf16, times the bf16 factor, rounded once
             dk2[c / 2] = mul_bf16x2(pack_bf16(d.x, d.y), fk[c / 2]);
           }
+        }
+        if (WIN && cut && has_nan<HC / 2>(dk2)) {
+#pragma unroll
+          for (int c = 0; c < HC; c += 32) hide_pairs(dk2 + c / 2, window_bits(c, from, front, nvalid));
         }
         // dS over this group's own S columns (already loaded above)
         if constexpr (HC == 64)

@@ -73,3 +73,46 @@ def test_the_lowest_scores_under_one_window_of_everything(dtype, dim):
             mean, size = np.cumsum(x, 0) / count, np.cumsum(np.abs(x), 0) / count
             assert np.all(np.abs(f64(o[t:t + n]) - mean) <= (one + 2.0 ** -23 * (n + 64)) * size + one * np.abs(mean))
             assert np.all(np.abs(f64(lse[t:t + n]) - low - np.log(count[..., 0])) <= 2.0 ** -21 * -low)
+
+
+def loud_values(lens, window, sinks, dqk, dv, dtype, size):
+    """Values of `size` at positions 10 to 29 of every sequence, gradients of 16 where rows do not see them, of 0
+    where they do.  Returns which rows do not."""
+    q, k, v, do, offs = batch(lens, 2, dqk, dv, dtype, seed=6)
+    at = torch.cat([torch.arange(n, device="cuda") for n in lens])
+    loud = (at >= 10) & (at < 30)
+    free = (at < 10) | (at >= 29 + window)
+    v[loud] = size
+    do[free] = 16.0
+    do[~free] = 0.0
+    return q, k, v, do, offs, free
+
+
+@pytest.mark.parametrize("window,sinks", [(64, 0), (64, 3), (140, 0), (5, 2), (128, 10)])
+@pytest.mark.parametrize("dtype,dqk,dv", KINDS)
+def test_gradients_beside_large_hidden_values(dtype, dqk, dv, window, sinks):
+    """<dO, v> of hidden pairs is past fp32: nothing of it may reach the gradients."""
+    lens = [300, 70, 450, 9]
+    q, k, v, do, offs, free = loud_values(lens, window, sinks, dqk, dv, dtype, 2.0 ** 120)
+    assert 16 * dv * 2 ** 120 > 2 ** 128
+    o, lse = jfa.jfa_window_fwd(q, k, v, offs, window, sinks=sinks)
+    grads = jfa.jfa_window_bwd(q, k, v, o, lse, do, offs, window, sinks=sinks)
+    want = reference(*(f64(x) for x in (q, k, v, do)), lens, window, sinks, float(np.float32(dqk ** -0.5)))
+    # weights, dS, o (in D) and the result, each rounded once; sums in fp32
+    one = 1.01 * 2.0 ** -8 if dtype == "bf16" else 0.0
+    for name, g in zip(("dq", "dk", "dv"), grads):
+        g = f64(g)
+        assert np.all(np.isfinite(g)), name
+        assert np.all(np.abs(g - want[name]) <= (3 * one + want["rel"]) * want["size"][name] + one * np.abs(want[name]) + 1e-30), name
+
+
+@pytest.mark.parametrize("window,sinks", [(64, 0), (64, 3), (1, 0), (5, 2), (128, 10)])
+@pytest.mark.parametrize("dtype,dqk,dv", KINDS)
+def test_outputs_beside_the_largest_hidden_values(dtype, dqk, dv, window, sinks):
+    lens = [300, 70, 450, 9]
+    outs = []
+    for size in (0.0, 3e38):
+        q, k, v, _, offs, free = loud_values(lens, window, sinks, dqk, dv, dtype, size)
+        outs.append(jfa.jfa_window_fwd(q, k, v, offs, window, sinks=sinks))
+    for a, b in zip(*outs):
+        assert torch.equal(a[free], b[free])
