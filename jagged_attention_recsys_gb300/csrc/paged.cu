@@ -300,23 +300,15 @@ paged_join_kernel(const __grid_constant__ Paged p, const TileShape t, int ctas, 
     if (lane == 0) w.hdr->status = st == 1 ? (int)JFA_ERR_BAD_PAGES : st;
   }
   // the CTAs that hold the tile's parts: c (slot 1), then c + 1 .. last (slot 0), looked up 32 at a time
-  PagedCutTile cut;
-  if (!cut.begins<MODE>(p, t, w, ctas, c)) return;
-  const PagedSeq& seq = cut.seq;
-  int last = c + 1;
-  for (;;) {
-    const unsigned on = __ballot_sync(0xffffffffu, cut.goes_on(p, t, w, ctas, last + 1 + lane));
-    if (on != ~0u) {
-      last += __ffs(~on) - 1;
-      break;
-    }
-    last += 32;
-  }
-  auto has_part = [&](int i) {  // not a CTA without work inside the tile
-    if (i > last) return false;
-    const PagedPos a = paged_pos(p, t, w, i), e = paged_pos(p, t, w, i + 1);
-    return i == c || !(cut.same(e) && a.blk >= e.blk);
+  auto lanes = [&](auto f) {
+    const unsigned on = __ballot_sync(0xffffffffu, f(lane));
+    return on == ~0u ? 32 : __ffs(~on) - 1;
   };
+  PagedCutTile cut;
+  if (!cut.find<MODE>(p, t, w, ctas, c, lanes)) return;
+  const PagedSeq& seq = cut.seq;
+  const int last = cut.last;
+  auto has_part = [&](int i) { return cut.part(p, t, w, c, i); };
   const bool mine = has_part(c + lane);  // of the first 32
   const unsigned parts = __ballot_sync(0xffffffffu, mine);
   constexpr int U = 2;  // parts whose rows are on their way, four columns a lane

@@ -294,6 +294,16 @@ struct PagedWalk {
   }
 };
 
+// How many of 32 lanes, from the first on and without a gap, `f` holds for: one thread in a warp's place.
+struct OneThread {
+  template <class F>
+  __device__ __forceinline__ int operator()(F f) const {
+    int n = 0;
+    while (n < 32 && f(n)) ++n;
+    return n;
+  }
+};
+
 // The tile that the cut at CTA c's end falls into, where its parts begin with CTA c's last one; they
 // go to CTA `last`.
 struct PagedCutTile {
@@ -317,11 +327,20 @@ struct PagedCutTile {
   __device__ __forceinline__ bool goes_on(const Paged& p, const TileShape& t, const PagedWs& w, int ctas, int i) const {
     return i < ctas && same(paged_pos(p, t, w, i));
   }
-  __device__ __forceinline__ bool find(const Paged& p, const TileShape& t, const PagedWs& w, int ctas, int c) {
-    if (!begins(p, t, w, ctas, c)) return false;
+  // lanes: looks at 32 CTAs at a time.
+  template <int MODE = kAny, class Lanes = OneThread>
+  __device__ __forceinline__ bool find(const Paged& p, const TileShape& t, const PagedWs& w, int ctas, int c,
+                                       Lanes lanes = Lanes{}) {
+    if (!begins<MODE>(p, t, w, ctas, c)) return false;
     last = c + 1;
-    while (goes_on(p, t, w, ctas, last + 1)) ++last;
+    for (int n = 32; n == 32; last += n) n = lanes([&](int i) { return goes_on(p, t, w, ctas, last + 1 + i); });
     return true;
+  }
+  // Whether CTA i, of those from c on, has a part: not one without work inside the tile.
+  __device__ __forceinline__ bool part(const Paged& p, const TileShape& t, const PagedWs& w, int c, int i) const {
+    if (i > last) return false;
+    const PagedPos a = paged_pos(p, t, w, i), e = paged_pos(p, t, w, i + 1);
+    return i == c || !(same(e) && a.blk >= e.blk);
   }
   // Token and head of row r; false: it has none.
   __device__ __forceinline__ bool row(const Paged& p, const TileShape& t, int r, int& tok, int& head) const {
