@@ -389,12 +389,14 @@ int paged_kernel(const Paged& p, int dtype) {
   // to tcgen05's 128-row tiles (groups larger than one would split them).  Measured, 64 users of
   // 2048 keys, 8 key heads of 128, us, few-row kernel against tcgen05: bf16 pages 16 rows 115 to
   // 121, 24 rows 195 to 121; MXFP8, where tcgen05 waits for the tiles in bf16, 16 rows 84 to 156,
-  // 32 rows 141 to 162, 48 rows 191 to 164.  Under a window of 256 keys tcgen05's long tiles weigh more:
-  // bf16 24 rows 68 to 86, 32 rows 72 to 86, 48 rows 84 to 86 (MXFP8 32 rows 82 to 94, 48 rows 98 to 96);
-  // of 1,024 keys as without one: bf16 16 rows 94 to 117, 24 rows 130 to 117 (MXFP8 32 rows 133 to 139,
-  // 48 rows 170 to 141).
+  // 32 rows 141 to 162, 48 rows 191 to 164.  Under a window tcgen05's long tiles weigh more, the longer
+  // the fewer the keys of window and sinks are: bf16 with 256 of them 24 rows 48 to 62, 32 rows 54 to 62, 48 rows
+  // 66 to 62; with 512 68 to 79, 72 to 76 and 91 to 79; with 768 91 to 89 and 93 to 89 already (the same keys as
+  // sinks in front of a window of 64: 192 50 to 62, 448 68 to 81, 960 111 to 99; 8,192 of 16 users 193 to
+  // 130).  MXFP8 as without a window: with 256 keys 32 rows 64 to 68, 48 rows 81 to 68, with 1,024 111 to 115 and
+  // 146 to 117.
   const int64_t rows_per_seq = p.total_q * p.group / p.batch;
-  const bool short_window = p.window > 0 && p.window <= 256;
+  const bool short_window = p.window > 0 && (int64_t)p.window + p.sinks <= 512;
   return rows_per_seq <= (p.kind == kCacheMx || short_window ? 32 : 16) || p.group > 128 ? kPagedRows16 : kPagedTc;
 }
 
