@@ -10,11 +10,19 @@
 // 27 where a few sequences of 16 keys are among 128 of more, which this takes 16 for.)
 //
 // The lengths are on the device, so that the tiled kernels are launched too unless the pages decide
-// it, and pass over these sequences as this kernel does over the others (12 us where none has few keys).
-// 16 groups of 64 sequences of two tokens each, 32 heads on 8, prefixes of 256 keys, the whole call
-// against the tiled kernels alone, us: bf16 2 own keys 124 to 156, 16 keys 165 to 156; MXFP8 129 to 185 and 191
-// to 185.  Groups of 8 of one token: 66 to 74, 68 to 72; MXFP8 64 to 79, 74 to 80.  With more than 16 tokens
-// a sequence on average hardly one has so few keys, and the tiled kernels take all.
+// it, and pass over these sequences as this kernel does over the others (12 us where none has few keys).  The
+// whole call with 2, 8, 12 and 16 own keys, and with the tiled kernels alone, us:
+//   groups, heads, prefix                              pages of 16 keys     wider pages          tiled kernels
+//   16 of 64 x 2 tokens, 32 on 8, 256 keys, bf16       97 115 124 136       111 128 142 150      142
+//   64 of 16 x 1 token, 8 on 8, 500 keys, bf16         83 93 99 107         97 107 115 122       130
+//   8 of 64 x 1 token, 32 on 8, 256 keys, bf16         68 72 76 81          78 83 87 91          92
+//   4 of 32 x 4 tokens, 32 on 4, 1,000 keys, bf16      70 74 79 83          83 87 91 95          95
+//   16 of 64 x 2 tokens, 32 on 8, 4,096 keys, bf16     228 244 255 265      242 259 267 279      271
+//   the first, MXFP8                                   101 117 130 142      115 132 146 156      165
+//   the last, MXFP8                                    257 271 285 296      271 283 298 310      320
+// So it takes up to 16 keys, but over bf16 pages that may hold more, where the tiled kernels are launched anyway,
+// up to 12.  With more than 16 tokens a sequence on average hardly one has so few, and the tiled kernels take
+// all.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -30,7 +38,8 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kScan = 4 * kThreads;  // sequences that a CTA checks by itself
 constexpr int H = 4, K = 4;  // query heads, and values, at a time
-constexpr int kFew = 16;     // own keys: half a warp's lanes
+constexpr int kFew = 16;     // own keys at most: half a warp's lanes
+constexpr int kFewWide = 12;  // and over bf16 pages that may hold more
 constexpr int kMaxDim = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -205,7 +214,10 @@ cudaError_t short_t(const Paged& p, PagedHeader* hdr, cudaStream_t s) {
 
 }  // namespace
 
-int paged_few(const Paged& p) { return p.total_q <= kFew * p.batch ? kFew : 0; }
+int paged_few(const Paged& p) {
+  if (p.total_q > kFew * p.batch) return 0;
+  return p.kind != kCacheBf16 || ((int64_t)p.width << p.page_shift) <= kFew ? kFew : kFewWide;
+}
 bool paged_short(const Paged& p) { return paged_few(p) > 0 && ((int64_t)p.width << p.page_shift) <= kFew; }
 
 cudaError_t launch_paged_short(const Paged& p, int dtype, PagedHeader* hdr, cudaStream_t s) {
