@@ -121,12 +121,16 @@ struct Raw16<float> {
   }
 };
 
-// (cos, sin) of pos turns, times amp
+// (cos, sin) of pos turns, times amp.  The quarter turns come off while the angle is an integer: as one float an
+// angle near a half turn would be off by 9e-8, what is left of it, at most an eighth of a turn, is by 2e-8.
 __device__ __forceinline__ float2 rotation(int64_t pos, unsigned long long turn, float amp) {
   const unsigned long long phase = (unsigned long long)pos * turn;  // modulo one turn
+  const uint32_t at = (uint32_t)(phase >> 32) + 0x20000000u;        // the nearest quarter's number, and the rest
   float s, c;
-  sincospif((float)(int32_t)(phase >> 32) * 4.656612873077392578125e-10f, &s, &c);  // 2^-31: half turns
-  return make_float2(amp * c, amp * s);
+  sincospif((float)((int32_t)(at & 0x3fffffffu) - 0x20000000) * 4.656612873077392578125e-10f, &s, &c);  // 2^-31: half turns
+  const float x = at & 0x40000000u ? -s : c, y = at & 0x40000000u ? c : s;
+  const float a = at & 0x80000000u ? -amp : amp;
+  return make_float2(a * x, a * y);
 }
 
 // A lane's place in a row: columns [a, a+8) and [b, b+8).  Halves layout: value i of the
