@@ -12,7 +12,8 @@
 //  * Angles.  The frequencies come as 64-bit binary fractions of a turn, made on the host from
 //    doubles (within 2^-53 turns).  pos times such a fraction modulo one turn is the low half
 //    of an integer product, which loses no more, with no 64-bit floating point and no range
-//    reduction; sincospif of the top 32 bits then gives cos and sin to about 1e-7.
+//    reduction; sincospif of what the top 32 bits lie beside the nearest quarter turn then gives cos
+//    and sin to about 6e-8.
 //  * A row is D/16 lane slots of 16 values (two 16-byte loads in bf16).  A slot holds whole
 //    pairs in both layouts, so the rotation needs no exchange between lanes, and a lane's
 //    slot is the same in every row it touches: its (cos, sin) are computed once a token
@@ -41,6 +42,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+
+// group lanes (a power of two) serve a row, of which slots = D/16 have values; parts warps share
+// a token's heads.  A step is the 32 / group rows of one tensor that a warp takes at once.
+struct FastShape {
+  int group, slots, parts;
+};
+
 template <typename T, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, 3)
 norm_rope_fwd_kernel(const __grid_constant__ NormRopeArgs p, const FastShape g) {

@@ -228,12 +228,6 @@ __device__ __forceinline__ void weights16(Slot16& w, const float* row, const Slo
   }
 }
 
-// group lanes (a power of two) serve a row, of which slots = D/16 have values; parts warps share
-// a token's heads.  A step is the 32 / group rows of one tensor that a warp takes at once.
-struct FastShape {
-  int group, slots, parts;
-};
-
 // ------------------------------------------------------------------ rows of any shape
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
