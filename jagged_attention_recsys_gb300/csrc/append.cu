@@ -9,9 +9,11 @@
 // where there are fewer tokens than warps; its lanes first look up a token each (sequence, position,
 // page: a chain of dependent loads that would otherwise be paid token by token).
 //
-// Measured: 64 prompts of up to 4,096 tokens, 32 + 8 heads of 128, to MXFP8: 586 us, 83% of the copy rate
+// Measured: 64 prompts of up to 4,096 tokens, 32 + 8 heads of 128, to MXFP8: 590 us, 83% of the copy rate
 // (four rows of a lane on their way; six 701, three 600, two 636; three CTAs an SM; two 663, four 603);
-// a warp a row instead, 5,476.  61 sequences of up to 700 tokens in fp32, 8 heads of 80 with 48 columns
+// a warp a row instead, 5,476.  Rows that do not divide into slots take that: 64 K tokens of 32 + 8 heads of
+// 80, bf16, with 20 columns rotated 1,994 us, with all 80 243; heads of 64 to MXFP8 with 34 rotated 2,045, with all
+// 148.  61 sequences of up to 700 tokens in fp32, 8 heads of 80 with 48 columns
 // in pairs: 60 us, 77%.  A token each of 256 users: 7.7 us on the GPU; the call on the host takes longer.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -38,7 +38,8 @@
 // Windows and shared prefixes are instances of their own (MODE).  A tile under a window walks the blocks
 // that hold its rows' windows and the sinks'; boxes in front of them are not looked up, and what such a
 // block holds in front of the window is cleaned, a stage at a time, by the warps that use it.  One token
-// for each of 256 users, histories to 8,192, window 1,024 and 4 sinks, 32 heads on 8: 178 us, 5.7 TB/s, 85%.
+// for each of 256 users, histories to 8,192, window 1,024 and 4 sinks, 32 heads on 8: 172 to 176 us with the join, 5.7
+// to 5.9 TB/s, 85 to 88%.
 // Of a shared prefix this is phase 1 where groups have few rows, and phase 2 over the sequences' own
 // keys: 128 continuations over up to 1,024 MXFP8 keys each, 32 heads on 4: 42 us; phase 1's results are
 // asked for ahead of the join of the four warps.

@@ -35,10 +35,10 @@
 // (433 us), two threads a row (495; they share a scheduler), the exponentials begun against an
 // older maximum (496), a rolled softmax that reads TMEM twice (445).
 // Windows and shared prefixes are instances of their own (MODE): 13 chunks of up to 1,024 tokens over
-// MXFP8 caches of up to 16,384, window 2,048, 16 sinks: 326 us, 37% of the MMAs' rate in visible
+// MXFP8 caches of up to 16,384, window 2,048, 16 sinks: 326 us (and 20 for the join), 37% of the MMAs' rate in visible
 // pairs (no window, 451 us above: 52%); a window's masks and a third more exponentials than visible pairs
 // are the rest.  64 candidates of 1 to 4 tokens behind each of 16 histories of 512 to 8,192 keys: phase 1
-// 199 us, 42%; 128 single tokens behind one prefix of 6,011 MXFP8 keys: 39 us.
+// 197 us, 42%; 128 single tokens behind one prefix of 6,011 MXFP8 keys: 39 us.
 #pragma once
 
 #include <cuda.h>

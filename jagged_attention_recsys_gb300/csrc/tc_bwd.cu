@@ -24,8 +24,8 @@
 //
 // Windows (WIN instances).  A key tile's rows are one stretch from its own first row on, a query
 // tile's keys the blocks of the forward.  96 histories of 1 to 4,096 rows, 8 heads of 128, window 512, 4
-// sinks: dQ 564 us, 1,900 cycles a step, of which the MMAs take 1,536; dK/dV 965 us, 3,400 cycles a step for
-// MMAs of 2,048: P and dS pass through registers between them.  The sinks cost 62 and 97 us: a tile of
+// sinks: dQ 573 us, 1,930 cycles a step, of which the MMAs take 1,536; dK/dV 999 us, 3,520 cycles a step for
+// MMAs of 2,048: P and dS pass through registers between them.  The sinks cost 75 and 228 us: a tile of
 // keys that all rows meet, though they see 4 of it.
 #include <cuda.h>
 #include <cudaTypedefs.h>

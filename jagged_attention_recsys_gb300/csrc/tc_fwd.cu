@@ -504,7 +504,8 @@ tc_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           }
           l *= alpha;
         }
-        // P = exp2(s c - m) or SiLU(s c)/L as packed bf16 pairs
+        // P = exp2(s c - m) or SiLU(s c)/L as packed bf16 pairs: the operand's type, off by 2^-9 of a
+        // weight on average, signs mixed; the sum takes them unrounded
         const float2 cc = make_float2(c_score, c_score);
         const float ref = WIN && m == -INFINITY ? 0.f : m;  // no key seen so far: weights of exp2(-inf)
         const float2 nm = make_float2(-ref, -ref);
