@@ -20,9 +20,11 @@
 //   16 of 64 x 2 tokens, 32 on 8, 4,096 keys, bf16     228 244 255 265      242 259 267 279      271
 //   the first, MXFP8                                   101 117 130 142      115 132 146 156      165
 //   the last, MXFP8                                    257 271 285 296      271 283 298 310      320
-// So it takes up to 16 keys, but over bf16 pages that may hold more, where the tiled kernels are launched anyway,
-// up to 12.  With more than 16 tokens a sequence on average hardly one has so few, and the tiled kernels take
-// all.
+//   8 of 64 x 1 token, 32 on 8 of 80, 64 keys, bf16    158 - 163 165        167 - 173 174        363-385 (CUDA cores)
+//   the same, heads of 128, fp32                       232 - 243 248        244 - 255 259        451-583 (CUDA cores)
+// So it takes up to 16 keys, but beside the tensor-core kernels over bf16 pages that may hold more, where those are
+// launched anyway, up to 12.  With more than 16 tokens a sequence on average hardly one has so few, and the tiled
+// kernels take all.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -39,7 +41,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kScan = 4 * kThreads;  // sequences that a CTA checks by itself
 constexpr int H = 4, K = 4;  // query heads, and values, at a time
 constexpr int kFew = 16;     // own keys at most: half a warp's lanes
-constexpr int kFewWide = 12;  // and over bf16 pages that may hold more
+constexpr int kFewWide = 12;  // and beside tensor-core kernels over bf16 pages that may hold more
 constexpr int kMaxDim = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -216,7 +218,8 @@ cudaError_t short_t(const Paged& p, PagedHeader* hdr, cudaStream_t s) {
 
 int paged_few(const Paged& p) {
   if (p.total_q > kFew * p.batch) return 0;
-  return p.kind != kCacheBf16 || ((int64_t)p.width << p.page_shift) <= kFew ? kFew : kFewWide;
+  if (p.kind != kCacheBf16 || ((int64_t)p.width << p.page_shift) <= kFew) return kFew;
+  return paged_kernel(p, JFA_BF16) == kPagedSimt ? kFew : kFewWide;
 }
 bool paged_short(const Paged& p) { return paged_few(p) > 0 && ((int64_t)p.width << p.page_shift) <= kFew; }
 

@@ -35,3 +35,15 @@ def test_results_on_both_sides_of_the_bounds(kind, dtype, wide):
     b = Shared([20, 36], [300, 77], (1 + np.arange(n) % 4).tolist(), own.tolist(), 2, 64, 64, 16, kind, dtype, wide=wide)
     for causal in (True, False):
         check(b, 8, causal)
+
+
+@pytest.mark.parametrize("kind,dtype,dqk,dv", [("bf16", "bf16", 80, 80), ("bf16", "bf16", 64, 40), ("f32", "f32", 64, 64)])
+@pytest.mark.parametrize("own,few", [(13, True), (16, True), (17, False)])
+def test_which_sequences_have_few_keys_beside_cuda_cores(kind, dtype, dqk, dv, own, few):
+    """CUDA cores take far longer a tile than the kernel for few keys: all up to 16 keys are its own there."""
+    n = 40
+    b = Shared([n], [70], [1] * n, [own] * n, 2, dqk, dv, 16, kind, dtype, wide=True)
+    ws = torch.zeros_like(space(b, 4))
+    check(b, 4, ws=ws)
+    assert jfa.jfa_status_check(ws) == jfa.JFA_OK
+    assert (int(ws[256:260].cpu().numpy().view(np.int32)[0]) == n) == few
